@@ -70,6 +70,10 @@ struct GemmArgs {
   uint16_t *Out;         // M x Ntot
   const uint8_t *keep;   // dX with adapter-input dropout: keep nibbles (M x Ntot/4), else NULL
   float inv_keep;        // 1/(1-p)
+  // many adapters (AD kernels): tile row p is token perm[p], whose adapter is
+  // sid[p] (-1: none); In and Out are addressed by token, S by p, and L holds
+  // one r x Ntot (or Ntot x r) matrix per adapter
+  const int *perm, *sid;
 };
 
 // LDS, one object per stage. The level table is the most aligned object, so
@@ -141,7 +145,7 @@ QL_DEV float scale_of(uint32_t qd, float s2, int64_t blk, float mu) {
 // codes (waves 0-3) or scale words (waves 4-7).
 constexpr int kLoadsPerStep = 5;
 
-template <int MODE, bool DQ>
+template <int MODE, bool DQ, bool AD>
 struct Tile {
   GemmArgs g;
   int tid, lane, wave, r32, h, wn, wm;
@@ -169,6 +173,7 @@ struct Tile {
   // the rank-r epilogue's operands of rank chunk 0 (L rows of the forward's
   // whole-piece path, and the S hi/lo parts), loaded before the last K-steps
   uint4 pre_a[2], pre_b[2][2];
+  int ad0, pre_id[2];   // AD: adapter of the wave's first row; of this lane's two rows
 
   // tile (tm, tn): token rows tm*BM.., output columns tn*BN..
   QL_DEV void init(const GemmArgs &ga, int64_t tm, int64_t tn) {
@@ -193,6 +198,7 @@ struct Tile {
       const int chunk = (lane & 7) ^ ((row ^ (row >> 2)) & 7);
       int64_t m = m0 + row;
       m = m < g.M ? m : g.M - 1;  // rows past M: duplicate data, outputs discarded
+      if (AD) m = token(m);
       xoff[i] = (m * g.Ktot + 8 * chunk) * 2;
     }
     const int p = 64 * (wave & 3) + lane;   // code DMA lane (waves 0-3)
@@ -236,12 +242,23 @@ struct Tile {
         roff[h2] = ra | (ra << 8) | (rb << 16) | (rb << 24);
       }
     }
+    if (AD) {
+      const int64_t p0 = m0 + 64 * wm;
+      ad0 = __builtin_amdgcn_readfirstlane(g.sid[p0 < g.M ? p0 : g.M - 1]);
+      if (ad0 < 0) ad0 = 0;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+  }
+
+  // AD: the token of row p (clamped, so that no stale plan addresses past In)
+  QL_DEV int64_t token(int64_t p) const {
+    const int64_t t = (uint32_t)g.perm[p];
+    return t < g.M ? t : g.M - 1;
   }
 
   // Row group i (8 rows, 1 KB) of this wave's eighth of the In tile of step
@@ -524,9 +541,48 @@ struct Tile {
       keep_block<1, 0>(kw);
       keep_block<1, 1>(kw);
     } else {
-      lora_term<0, 2, 0, 2>(acc);
+      if (AD)
+        adapter_terms();
+      else
+        lora_term<0, 2, 0, 2>(acc, g.L, true);
     }
     store();
+  }
+
+  // Many adapters: rows are ordered by adapter, so a wave's 64 rows hold a
+  // few runs. For each adapter present, the rank-r term with that adapter's
+  // matrix is added to a copy of the accumulators, and each lane keeps the
+  // copy where its row (one per 32 x 32 block: column l % 32 of D) belongs to
+  // the adapter. Selecting results, rather than zeroing the other rows'
+  // operands, keeps an infinity or NaN in one adapter's matrix out of the
+  // others' rows.
+  QL_DEV void adapter_terms() {
+    int id[2];
+    uint64_t pend[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t m = m0 + wm * 64 + 32 * j + r32;
+      id[j] = m < g.M ? pre_id[j] : -1;
+      pend[j] = __ballot(id[j] >= 0);
+    }
+    while (pend[0] | pend[1]) {
+      const int a = pend[0] ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(pend[0]))
+                            : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(pend[1]));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) pend[j] &= ~__ballot(id[j] == a);
+      f32x16 t[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) t[i][j] = acc[i][j];
+      lora_term<0, 2, 0, 2>(t, g.L + (int64_t)a * g.r * g.Ntot, a == ad0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[i][j][q] = id[j] == a ? t[i][j][q] : acc[i][j][q];
+    }
   }
 
   // One 32 x 32 block of the dropout epilogue (one block at a time keeps the
@@ -536,7 +592,7 @@ struct Tile {
     f32x16 lacc[1][1];
 #pragma unroll
     for (int q = 0; q < 16; ++q) lacc[0][0][q] = 0.0f;
-    lora_term<I, 1, J, 1>(lacc);
+    lora_term<I, 1, J, 1>(lacc, g.L, true);
     const uint32_t w4[4] = {kw[J].x, kw[J].y, kw[J].z, kw[J].w};
 #pragma unroll
     for (int q4 = 0; q4 < 4; ++q4) {
@@ -553,11 +609,19 @@ struct Tile {
   QL_DEV void lora_prefetch() {
     if (MODE == 0 && g.r % 8 == 0) {
       const int tq = 8 * h < g.r ? 8 * h : g.r - 8;
+      const uint16_t *L = AD ? g.L + (int64_t)ad0 * g.r * g.Ntot : g.L;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int64_t n = n0 + wn * 64 + 32 * i + r32;
         const int64_t nc = n < g.Ntot ? n : g.Ntot - 1;
-        pre_a[i] = *(const uint4 *)(g.L + nc * g.r + tq);
+        pre_a[i] = *(const uint4 *)(L + nc * g.r + tq);
+      }
+    }
+    if (AD) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t m = m0 + wm * 64 + 32 * j + r32;
+        pre_id[j] = g.sid[m < g.M ? m : g.M - 1];
       }
     }
 #pragma unroll
@@ -572,9 +636,10 @@ struct Tile {
     }
   }
 
-  // the rank-r term of the 32 x 32 blocks (I0 .., J0 ..), NI x NJ of them
+  // the rank-r term of the 32 x 32 blocks (I0 .., J0 ..), NI x NJ of them,
+  // with L rows from `L` (pre: pre_a holds its first rank chunk)
   template <int I0, int NI, int J0, int NJ>
-  QL_DEV void lora_term(f32x16 (&dst)[NI][NJ]) {
+  QL_DEV void lora_term(f32x16 (&dst)[NI][NJ], const uint16_t *L, bool pre) {
     for (int t0 = 0; t0 < g.rp; t0 += 16) {
       // L[n][t0 + 8h .. +7] read in place (ranks past r and n past Ntot: 0);
       // loads from clamped addresses, the zeroing applied afterwards
@@ -586,8 +651,9 @@ struct Tile {
         for (int ii = 0; ii < NI; ++ii) {
           const int64_t n = n0 + wn * 64 + 32 * (I0 + ii) + r32;
           const int64_t nc = n < g.Ntot ? n : g.Ntot - 1;
-          const uint4 v = t0 == 0 ? pre_a[I0 + ii]
-                                  : *(const uint4 *)(g.L + nc * g.r + (tq < g.r ? tq : g.r - 8));
+          const uint4 v = (t0 == 0 && pre)
+                              ? pre_a[I0 + ii]
+                              : *(const uint4 *)(L + nc * g.r + (tq < g.r ? tq : g.r - 8));
           a[ii] = (n < g.Ntot && tq < g.r) ? v : ql::zero4();
         }
       } else {
@@ -600,7 +666,7 @@ struct Tile {
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             const int t = t0 + 8 * h + x, tc = t < g.r ? t : g.r - 1;
-            e[ii][x] = g.L[MODE == 0 ? nc * g.r + tc : (int64_t)tc * g.Ntot + nc];
+            e[ii][x] = L[MODE == 0 ? nc * g.r + tc : (int64_t)tc * g.Ntot + nc];
           }
         }
 #pragma unroll
@@ -642,8 +708,9 @@ struct Tile {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int64_t m = m0 + wm * 64 + 32 * j + r32;
+        int64_t m = m0 + wm * 64 + 32 * j + r32;
         if (m >= g.M) continue;
+        if (AD) m = token(m);
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
           const int64_t n = n0 + wn * 64 + 32 * i + 8 * q4 + 4 * h;
@@ -668,12 +735,12 @@ QL_DEV void tile_of(int64_t ntn, int64_t ntm, int64_t &tm, int64_t &tn) {
   tn = tile % ntn;
 }
 
-template <int MODE, bool DQ>
+template <int MODE, bool DQ, bool AD>
 __global__ __launch_bounds__(NT, 1) void nf4_gemm_kernel(GemmArgs g) {
   if (threadIdx.x < 16) s_lv[threadIdx.x] = __uint_as_float(c_levels_g[threadIdx.x]);
   int64_t tm, tn;
   tile_of(ql_cdiv(g.Ntot, BN), ql_cdiv(g.M, BM), tm, tn);
-  Tile<MODE, DQ> t;
+  Tile<MODE, DQ, AD> t;
   t.init(g, tm, tn);
   __syncthreads();  // level table
   t.run();
@@ -686,17 +753,17 @@ static qlora_status launch_gemm(int mode, GemmArgs g, hipStream_t st) {
   const int64_t tiles = ql_cdiv(g.Ntot, BN) * ql_cdiv(g.M, BM);
   QlProf prof(mode == 0 ? QLORA_K_GEMM_FWD : QLORA_K_GEMM_DX, st);
   const unsigned grid = (unsigned)tiles;
+#define QL_GEMM(MODEV, DQV)                                        \
+  if (g.perm)                                                      \
+    nf4_gemm_kernel<MODEV, DQV, true><<<grid, NT, 0, st>>>(g);     \
+  else                                                             \
+    nf4_gemm_kernel<MODEV, DQV, false><<<grid, NT, 0, st>>>(g);
   if (mode == 0) {
-    if (g.sc.dq)
-      nf4_gemm_kernel<0, true><<<grid, NT, 0, st>>>(g);
-    else
-      nf4_gemm_kernel<0, false><<<grid, NT, 0, st>>>(g);
+    if (g.sc.dq) { QL_GEMM(0, true) } else { QL_GEMM(0, false) }
   } else {
-    if (g.sc.dq)
-      nf4_gemm_kernel<1, true><<<grid, NT, 0, st>>>(g);
-    else
-      nf4_gemm_kernel<1, false><<<grid, NT, 0, st>>>(g);
+    if (g.sc.dq) { QL_GEMM(1, true) } else { QL_GEMM(1, false) }
   }
+#undef QL_GEMM
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
@@ -704,15 +771,16 @@ static qlora_status launch_gemm(int mode, GemmArgs g, hipStream_t st) {
 qlora_status launch_gemm_fwd(const uint8_t *codes, ql::ScaleSrc sc, int64_t d, int64_t k,
                              const uint16_t *X, int64_t M, const uint16_t *B, int r,
                              const uint16_t *Hs_hi, const uint16_t *Hs_lo, int rp,
-                             uint16_t *Y, hipStream_t st) {
-  GemmArgs g{codes, sc, d, k, X, M, d, k, B, Hs_hi, Hs_lo, r, rp, Y};
+                             uint16_t *Y, hipStream_t st, const int *perm, const int *sid) {
+  GemmArgs g{codes, sc, d, k, X, M, d, k, B, Hs_hi, Hs_lo, r, rp, Y, nullptr, 1.0f, perm, sid};
   return launch_gemm(0, g, st);
 }
 
 qlora_status launch_gemm_dx(const uint8_t *codes, ql::ScaleSrc sc, int64_t d, int64_t k,
                             const uint16_t *dY, int64_t M, const uint16_t *A, int r,
                             const uint16_t *Gs_hi, const uint16_t *Gs_lo, int rp,
-                            uint16_t *dX, const uint8_t *keep, float inv_keep, hipStream_t st) {
-  GemmArgs g{codes, sc, d, k, dY, M, k, d, A, Gs_hi, Gs_lo, r, rp, dX, keep, inv_keep};
+                            uint16_t *dX, const uint8_t *keep, float inv_keep, hipStream_t st,
+                            const int *perm, const int *sid) {
+  GemmArgs g{codes, sc, d, k, dY, M, k, d, A, Gs_hi, Gs_lo, r, rp, dX, keep, inv_keep, perm, sid};
   return launch_gemm(1, g, st);
 }

@@ -81,6 +81,13 @@ struct GemvW {
   DropParams dp;   // dropout of X on this weight's adapter input
 };
 
+// Many adapters (AD kernels): adapter of each token. w[0].Ap is then
+// [n][r][k] and the H partials are [S][M][rp].
+struct GemvAd {
+  const int *tok;
+  int n, r;
+};
+
 struct GemvArgs {
   GemvW w[GMAXW];
   int nw;          // weights in the call (1..GMAXW)
@@ -93,6 +100,7 @@ struct GemvArgs {
   float *part;     // [S][M][dtot]: slice partial sums, weights side by side
   int64_t dtot;
   int rp;
+  GemvAd ad;
 };
 
 // Weight i of the call, field by field through uniform selects (a dynamic
@@ -359,17 +367,106 @@ QL_DEV void lora_down_partial(const GemvArgs &g, int64_t slice, int nblk, int wa
   }
 }
 
+// Sum v[i] over the 64 lanes of a wave for every i, in a fixed order: each
+// butterfly step hands half of the entries to the lane partner that keeps
+// them, so after the steps lane l holds the sum of entry l >> (6 - log2 N)
+// in its return value (all lanes of a group of 64 / N hold the same bits).
+template <int N>
+QL_DEV float wave_transpose_sum(float (&v)[N], int lane) {
+  static_assert(N >= 1 && N <= 64 && (N & (N - 1)) == 0, "N: power of two up to 64");
+#pragma unroll
+  for (int st = 0; st < 6; ++st) {
+    const int mask = 32 >> st;
+    const int half = N >> (st + 1);
+    const bool up = (lane & mask) != 0;
+    if (half >= 1) {
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        // the pair as opaque register values: otherwise the lane-dependent
+        // selects become an indexed access to a scratch copy of v
+        float lo = v[i], hi = v[i + half];
+        asm("" : "+v"(lo), "+v"(hi));
+        const float send = up ? lo : hi;
+        const float keep = up ? hi : lo;
+        v[i] = keep + __shfl_xor(send, mask);
+      }
+    } else {
+      v[0] += __shfl_xor(v[0], mask);
+    }
+  }
+  return v[0];
+}
+
+QL_DEV float dot2bf(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a),
+                                         __builtin_bit_cast(bf16x2, b), c, false);
+}
+
+// H = X A_a^T of one token for 16 ranks over one slice of 64 CPL columns (one
+// workgroup): lane l holds columns CPL l .. of the token, wave w takes ranks
+// 16 cb + 2 w, + 1 of the token's own adapter; ranks past r and tokens without
+// an adapter give zeros. A row is read where it lies, so each token costs r k
+// bytes x 2 from the cache or memory, which is small beside the codes.
+template <int CPL>
+QL_DEV void adapter_down(const uint16_t *X, const uint16_t *A, const GemvAd &ad, int64_t k,
+                         int64_t M, int rp, float *hpart, int hidx, int64_t slice, int wave,
+                         int lane) {
+  const int nrc = rp / 16, cb = hidx % nrc;
+  const int64_t m = hidx / nrc;
+  const int64_t col0 = slice * (64 * CPL) + CPL * lane;
+  const bool lok = col0 < k;
+  const int64_t colc = lok ? col0 : 0;
+  const int a = ad.tok[m];
+  const bool has = a >= 0 && a < ad.n;
+  float v[2] = {0.f, 0.f};
+  if (has) {   // uniform over the workgroup
+    uint4 x[CPL / 8];
+#pragma unroll
+    for (int i = 0; i < CPL / 8; ++i) x[i] = *(const uint4 *)(X + m * k + colc + 8 * i);
+    uint4 w[2][CPL / 8];
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt) {
+      const int t = min(16 * cb + 2 * wave + tt, ad.r - 1);
+      const uint16_t *row = A + ((int64_t)a * ad.r + t) * k + colc;
+#pragma unroll
+      for (int i = 0; i < CPL / 8; ++i) w[tt][i] = *(const uint4 *)(row + 8 * i);
+    }
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt) {
+      float p0 = 0.f, p1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < CPL / 8; ++i) {
+        p0 = dot2bf(w[tt][i].x, x[i].x, p0);
+        p1 = dot2bf(w[tt][i].y, x[i].y, p1);
+        p0 = dot2bf(w[tt][i].z, x[i].z, p0);
+        p1 = dot2bf(w[tt][i].w, x[i].w, p1);
+      }
+      v[tt] = (lok && 16 * cb + 2 * wave + tt < ad.r) ? p0 + p1 : 0.f;
+    }
+  }
+  const float sum = wave_transpose_sum<2>(v, lane);   // lanes 0-31: rank 0, 32-63: rank 1
+  if ((lane & 31) == 0)
+    hpart[(slice * M + m) * rp + 16 * cb + 2 * wave + (lane >> 5)] = sum;
+}
+
 // Workgroup (x, slice) takes row groups x, x + G, x + 2G, ... (at most 2 GW
 // of them) of one slice; wave w takes the workgroup's row groups w and
 // w + GW, both loaded before the table is built, then computed together. The
 // table and the X slice are built once per workgroup.
-template <bool DQ, int TP, bool FULL, bool GRP, bool QA>
+// AD: the workgroups past the G of a slice compute the H partials of the
+// tokens' own adapters instead (M rp / 16 of them).
+template <bool DQ, int TP, bool FULL, bool GRP, bool QA, bool AD>
 __global__ __launch_bounds__(GT) void nf4_gemv_kernel(GemvArgs g) {
   __shared__ __align__(16) unsigned char smem[LDS_BYTES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = lane & 15, q = lane >> 4;
   const int64_t nbr = g.k >> 6;
   const int64_t slice = blockIdx.y;
+  if (AD && (int)blockIdx.x >= g.G) {
+    adapter_down<GB>(g.X, g.w[0].Ap, g.ad, g.k, g.M, g.rp, g.w[0].hpart, (int)blockIdx.x - g.G,
+                     slice, wave, lane);
+    return;
+  }
   const int64_t b0 = slice * GB;
   const int nblk = FULL ? GB : (int)min<int64_t>(GB, nbr - b0);
   auto rg_of = [&](int j) -> int64_t { return (int64_t)blockIdx.x + (int64_t)g.G * j; };
@@ -399,7 +496,7 @@ __global__ __launch_bounds__(GT) void nf4_gemv_kernel(GemvArgs g) {
   // partial (the last one of the slice, which has the fewest units); issued
   // before the code loads so the waits for the codes count the same loads
   // in every workgroup
-  const bool hwg = blockIdx.x == gridDim.x - 1;
+  const bool hwg = !AD && blockIdx.x == gridDim.x - 1;
   HPre hp;
   if (hwg) lora_down_load(g, slice, nblk, wave, n, q, hp);
   __builtin_amdgcn_sched_barrier(0);
@@ -534,37 +631,8 @@ struct VArgs {
   float *part;      // [S][M][dtot]
   int64_t dtot;
   int rp;
+  GemvAd ad;
 };
-
-// Sum v[i] over the 64 lanes of a wave for every i, in a fixed order: each
-// butterfly step hands half of the entries to the lane partner that keeps
-// them, so after the steps lane l holds the sum of entry l >> (6 - log2 N)
-// in its return value (all lanes of a group of 64 / N hold the same bits).
-template <int N>
-QL_DEV float wave_transpose_sum(float (&v)[N], int lane) {
-  static_assert(N >= 1 && N <= 64 && (N & (N - 1)) == 0, "N: power of two up to 64");
-#pragma unroll
-  for (int st = 0; st < 6; ++st) {
-    const int mask = 32 >> st;
-    const int half = N >> (st + 1);
-    const bool up = (lane & mask) != 0;
-    if (half >= 1) {
-#pragma unroll
-      for (int i = 0; i < half; ++i) {
-        // the pair as opaque register values: otherwise the lane-dependent
-        // selects become an indexed access to a scratch copy of v
-        float lo = v[i], hi = v[i + half];
-        asm("" : "+v"(lo), "+v"(hi));
-        const float send = up ? lo : hi;
-        const float keep = up ? hi : lo;
-        v[i] = keep + __shfl_xor(send, mask);
-      }
-    } else {
-      v[0] += __shfl_xor(v[0], mask);
-    }
-  }
-  return v[0];
-}
 
 // X[m][col0 .. col0 + 31] of tokens m < MV as 16 bf16 pairs (token rows past
 // M and lanes past k read clamped addresses; their sums are never stored or
@@ -584,11 +652,6 @@ QL_DEV void valu_load_x(const VArgs &g, int64_t colc, uint32_t (&xw)[MV][16]) {
       xw[m][4 * i + 3] = v.w;
     }
   }
-}
-
-QL_DEV float dot2bf(uint32_t a, uint32_t b, float c) {
-  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a),
-                                         __builtin_bit_cast(bf16x2, b), c, false);
 }
 
 // H partials of one slice of one weight for one chunk of 16 ranks (one
@@ -642,13 +705,18 @@ QL_DEV void valu_lora_down(const VArgs &g, int hidx, int wave, int lane) {
 // slice blocks (lane l: row l / 8, blocks 4 (l % 8) .. + 3), handed to the
 // lanes that need them by one shuffle per row; otherwise one byte load per
 // row and lane.
-template <bool DQ, int MV, bool GRP, bool QA>
+template <bool DQ, int MV, bool GRP, bool QA, bool AD>
 __global__ __launch_bounds__(64 * VW) void nf4_gemv_valu_kernel(VArgs g) {
   __shared__ __align__(16) unsigned char lut[256 * 256];
   __shared__ __align__(16) uint4 xs[MV][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if ((int)blockIdx.x >= g.nrow_wg) {   // uniform per workgroup
-    valu_lora_down<MV, GRP>(g, (int)blockIdx.x - g.nrow_wg, wave, lane);
+    const int h = (int)blockIdx.x - g.nrow_wg;
+    if (AD)
+      adapter_down<VCOL / 64>(g.X, g.w[0].Ap, g.ad, g.k, g.M, g.rp, g.w[0].hpart, h / g.S, h % g.S,
+                              wave, lane);
+    else
+      valu_lora_down<MV, GRP>(g, h, wave, lane);
     return;
   }
   // workgroup b: slice b % S, row groups (b / S) VW + wave (clamped; the
@@ -872,6 +940,91 @@ __global__ __launch_bounds__(256) void gemv_epilogue_kernel(EpiArgs e) {
   W.Y[m * W.d + j] = ql::f_to_bf16(acc + e.s * l);
 }
 
+// The epilogue for tokens with adapters of their own: token m of grid row m
+// uses B_a at Bp + a d r and s_a; without an adapter Y is the base sum and
+// H_save's row is zero.
+struct EpiAdArgs {
+  const uint16_t *Bp;   // [n][d][r]
+  const float *hpart;   // [S][M][rp]
+  const float *part;    // [S][M][d]
+  const float *scale;
+  uint16_t *Y;          // M x d
+  float *hsave;         // M x r or NULL
+  int64_t M, d;
+  int S, rp;
+  GemvAd ad;
+};
+
+__global__ __launch_bounds__(256) void gemv_epilogue_adapters_kernel(EpiAdArgs e) {
+  __shared__ float hp[16][128];
+  __shared__ float hs[128];
+  const int64_t m = blockIdx.y;
+  const int tid = threadIdx.x;
+  const int rp = e.rp, r = e.ad.r;
+  const int64_t j = (int64_t)blockIdx.x * 256 + tid;
+  const int64_t jc = j < e.d ? j : e.d - 1;
+  const int at = e.ad.tok[m];
+  const bool has = at >= 0 && at < e.ad.n;
+  const int a = has ? at : 0;
+  // loads that do not depend on H first, as in the kernel above
+  const uint16_t *brow = e.Bp + ((int64_t)a * e.d + jc) * r;
+  const bool pieces = (r & 7) == 0;   // rows of whole 16-byte pieces
+  uint4 b0 = ql::zero4(), b1 = ql::zero4();
+  if (pieces) {
+    b0 = *(const uint4 *)brow;
+    if (r > 8) b1 = *(const uint4 *)(brow + 8);
+  }
+  const float s = e.scale[a];
+  float acc = 0.0f;
+  for (int s0 = 0; s0 < e.S; s0 += 8) {
+    float pv[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      pv[u] = e.part[((int64_t)min(s0 + u, e.S - 1) * e.M + m) * e.d + jc];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (s0 + u < e.S) acc += pv[u];
+  }
+  {
+    const int ng = 256 / rp, t = tid % rp, grp = tid / rp;
+    if (grp < ng) {
+      float ha = 0.0f;
+      for (int p = grp; p < e.S; p += ng) ha += e.hpart[((int64_t)p * e.M + m) * rp + t];
+      hp[grp][t] = ha;
+    }
+    __syncthreads();
+    if (tid < rp) {
+      float ha = 0.0f;
+      for (int gi = 0; gi < ng; ++gi) ha += hp[gi][tid];
+      hs[tid] = ha;
+      if (e.hsave && blockIdx.x == 0 && tid < r) e.hsave[m * r + tid] = ha;
+    }
+    __syncthreads();
+  }
+  if (j >= e.d) return;
+  float l = 0.0f;
+  if (!has) {
+    e.Y[m * e.d + j] = ql::f_to_bf16(acc);
+    return;
+  }
+  if (pieces) {
+    const uint32_t bw[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+    for (int t = 0; t < 16; ++t)   // ranks past r: both factors zero
+      l = fmaf(hs[t], (t & 1) ? ql::bf16hi(bw[t >> 1]) : ql::bf16lo(bw[t >> 1]), l);
+    for (int t = 16; t < r; t += 8) {
+      const uint4 b = *(const uint4 *)(brow + t);
+      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        l = fmaf(hs[t + i], (i & 1) ? ql::bf16hi(w[i >> 1]) : ql::bf16lo(w[i >> 1]), l);
+    }
+  } else {
+    for (int t = 0; t < r; ++t) l = fmaf(hs[t], ql::bf16_to_f(brow[t]), l);
+  }
+  e.Y[m * e.d + j] = ql::f_to_bf16(acc + s * l);
+}
+
 }  // namespace
 
 static int64_t gemv_splits(int64_t k) { return ql_cdiv(k >> 6, GB); }
@@ -884,9 +1037,21 @@ size_t gemv_part_bytes(int64_t dtot, int64_t k, int64_t M, int rp, int nw) {
 // slices (the last may be ragged), one H partial per slice and weight; its
 // partial sums fit in the workspace sized for the MFMA path (fewer slices,
 // fewer H partials).
+static qlora_status launch_epilogue_adapters(const GemvIn &in, int64_t M, int64_t S, int rp,
+                                             const GemvAd &ad, const float *scale,
+                                             const float *part, const float *hpart,
+                                             hipStream_t st) {
+  const EpiAdArgs e{in.Bp, hpart, part, scale, in.Y, in.H_save, M, in.d, (int)S, rp, ad};
+  QlProf prof(QLORA_K_GEMV_EPILOGUE, st);
+  dim3 eg((unsigned)ql_cdiv(in.d, 256), (unsigned)M);
+  gemv_epilogue_adapters_kernel<<<eg, 256, 0, st>>>(e);
+  QL_LAUNCH_CHECK();
+  return QLORA_OK;
+}
+
 static qlora_status launch_gemv_valu(int nw, const GemvIn *in, int64_t k, const uint16_t *X,
                                      int64_t M, int r, int rp, float s, float *part,
-                                     hipStream_t st) {
+                                     hipStream_t st, const GemvAd *ad, const float *scale) {
   const int64_t S = ql_cdiv(k, VCOL);
   int64_t dtot = 0, ngroups = 0, eblocks = 0;
   VArgs g{};
@@ -911,8 +1076,10 @@ static qlora_status launch_gemv_valu(int nw, const GemvIn *in, int64_t k, const 
   }
   const int64_t nunits = ngroups * S;
   const int64_t nrow_wg = ql_cdiv(ngroups, VW) * S;
-  const int64_t nh_wg = nw * S * (rp / 16);   // H: one workgroup per weight, slice, 16 ranks
+  // H: one workgroup per weight (with adapters: per token), slice and 16 ranks
+  const int64_t nh_wg = (ad ? M : nw) * S * (rp / 16);
   if (nrow_wg + nh_wg > 0x7fffffff || eblocks > 0x7fffffff) return QLORA_ERR_UNSUPPORTED;
+  if (ad) g.ad = *ad;
   g.nw = nw;
   g.k = k;
   g.X = X;
@@ -926,11 +1093,13 @@ static qlora_status launch_gemv_valu(int nw, const GemvIn *in, int64_t k, const 
   {
     QlProf prof(QLORA_K_GEMV, st);
     const unsigned grid = (unsigned)(nrow_wg + nh_wg);
-#define QL_VGEMV(DQV, MVV, QAV)                                                  \
-  if (nw > 1)                                                                    \
-    nf4_gemv_valu_kernel<DQV, MVV, true, QAV><<<grid, 64 * VW, 0, st>>>(g);      \
-  else                                                                           \
-    nf4_gemv_valu_kernel<DQV, MVV, false, QAV><<<grid, 64 * VW, 0, st>>>(g);
+#define QL_VGEMV(DQV, MVV, QAV)                                                    \
+  if (ad)                                                                          \
+    nf4_gemv_valu_kernel<DQV, MVV, false, QAV, true><<<grid, 64 * VW, 0, st>>>(g); \
+  else if (nw > 1)                                                                 \
+    nf4_gemv_valu_kernel<DQV, MVV, true, QAV, false><<<grid, 64 * VW, 0, st>>>(g); \
+  else                                                                             \
+    nf4_gemv_valu_kernel<DQV, MVV, false, QAV, false><<<grid, 64 * VW, 0, st>>>(g);
     const bool qa = (k % 256) == 0;
     if (in[0].sc.dq && qa) {
       if (M == 1) { QL_VGEMV(true, 1, true) } else { QL_VGEMV(true, 2, true) }
@@ -940,6 +1109,10 @@ static qlora_status launch_gemv_valu(int nw, const GemvIn *in, int64_t k, const 
       if (M == 1) { QL_VGEMV(false, 1, false) } else { QL_VGEMV(false, 2, false) }
     }
 #undef QL_VGEMV
+  }
+  if (ad) {
+    QL_LAUNCH_CHECK();
+    return launch_epilogue_adapters(in[0], M, S, rp, *ad, scale, part, g.w[0].hpart, st);
   }
   {
     e.nw = nw;
@@ -959,15 +1132,17 @@ static qlora_status launch_gemv_valu(int nw, const GemvIn *in, int64_t k, const 
   return QLORA_OK;
 }
 
-qlora_status launch_gemv_fwd(int nw, const GemvIn *in, int64_t k, const uint16_t *X, int64_t M,
-                             int r, int rp, float s, float *part, hipStream_t st) {
+static qlora_status launch_gemv(int nw, const GemvIn *in, int64_t k, const uint16_t *X, int64_t M,
+                                int r, int rp, float s, float *part, hipStream_t st,
+                                const GemvAd *ad, const float *scale) {
   if (M < 1 || M > 16 || rp < 16 || rp > 128 || rp % 16) return QLORA_ERR_INVALID_ARG;
   if (nw < 1 || nw > GMAXW) return QLORA_ERR_INVALID_ARG;
   for (int i = 1; i < nw; ++i)
     if (in[i].sc.dq != in[0].sc.dq) return QLORA_ERR_INVALID_ARG;
   bool drop = false;
   for (int i = 0; i < nw; ++i) drop = drop || in[i].dp.on;
-  if (M <= VMAXM && !drop) return launch_gemv_valu(nw, in, k, X, M, r, rp, s, part, st);
+  if (M <= VMAXM && !drop)
+    return launch_gemv_valu(nw, in, k, X, M, r, rp, s, part, st, ad, scale);
   const int ncu = ql_num_cus();
   const int64_t S = gemv_splits(k);
   int64_t dtot = 0, ngroups = 0, eblocks = 0;
@@ -998,6 +1173,7 @@ qlora_status launch_gemv_fwd(int nw, const GemvIn *in, int64_t k, const uint16_t
       ngroups, std::max<int64_t>(std::max<int64_t>(1, ncu / S), ql_cdiv(ngroups, 2 * GW)));
   const int64_t rpw = ql_cdiv(ngroups, G);
   if (S > 65535 || G > (int64_t(1) << 30) || eblocks > 0x7fffffff) return QLORA_ERR_UNSUPPORTED;
+  if (ad) g.ad = *ad;
   g.nw = nw;
   g.k = k;
   g.X = X;
@@ -1008,17 +1184,19 @@ qlora_status launch_gemv_fwd(int nw, const GemvIn *in, int64_t k, const uint16_t
   g.part = part;
   g.dtot = dtot;
   g.rp = rp;
-  dim3 grid((unsigned)G, (unsigned)S);
+  dim3 grid((unsigned)(G + (ad ? M * (rp / 16) : 0)), (unsigned)S);
   {
     QlProf prof(QLORA_K_GEMV, st);
     const int tp = (int)ql_cdiv(M, 4);
     // every slice is full when k is a multiple of 1024
     const bool full = (k % (64 * GB)) == 0;
-#define QL_GEMV5(DQV, TPV, FV, QAV)                                     \
-  if (nw > 1)                                                           \
-    nf4_gemv_kernel<DQV, TPV, FV, true, QAV><<<grid, GT, 0, st>>>(g);   \
-  else                                                                  \
-    nf4_gemv_kernel<DQV, TPV, FV, false, QAV><<<grid, GT, 0, st>>>(g);
+#define QL_GEMV5(DQV, TPV, FV, QAV)                                            \
+  if (ad)                                                                      \
+    nf4_gemv_kernel<DQV, TPV, FV, false, QAV, true><<<grid, GT, 0, st>>>(g);   \
+  else if (nw > 1)                                                             \
+    nf4_gemv_kernel<DQV, TPV, FV, true, QAV, false><<<grid, GT, 0, st>>>(g);   \
+  else                                                                         \
+    nf4_gemv_kernel<DQV, TPV, FV, false, QAV, false><<<grid, GT, 0, st>>>(g);
 #define QL_GEMV4(DQV, TPV, FV)                                          \
   if (DQV && (k % 256) == 0) {                                          \
     QL_GEMV5(DQV, TPV, FV, DQV)                                         \
@@ -1043,6 +1221,10 @@ qlora_status launch_gemv_fwd(int nw, const GemvIn *in, int64_t k, const uint16_t
 #undef QL_GEMV4
 #undef QL_GEMV5
   }
+  if (ad) {
+    QL_LAUNCH_CHECK();
+    return launch_epilogue_adapters(in[0], M, S, rp, *ad, scale, part, g.w[0].hpart, st);
+  }
   {
     e.nw = nw;
     e.part = part;
@@ -1059,4 +1241,16 @@ qlora_status launch_gemv_fwd(int nw, const GemvIn *in, int64_t k, const uint16_t
   }
   QL_LAUNCH_CHECK();
   return QLORA_OK;
+}
+
+qlora_status launch_gemv_fwd(int nw, const GemvIn *in, int64_t k, const uint16_t *X, int64_t M,
+                             int r, int rp, float s, float *part, hipStream_t st) {
+  return launch_gemv(nw, in, k, X, M, r, rp, s, part, st, nullptr, nullptr);
+}
+
+qlora_status launch_gemv_adapters(const GemvIn &in, int64_t k, const uint16_t *X, int64_t M,
+                                  int r, int rp, const int *tok, int n, const float *scale,
+                                  float *part, hipStream_t st) {
+  const GemvAd ad{tok, n, r};
+  return launch_gemv(1, &in, k, X, M, r, rp, 0.0f, part, st, &ad, scale);
 }

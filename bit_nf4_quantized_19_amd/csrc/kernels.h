@@ -40,6 +40,30 @@ qlora_status launch_loftq(const uint16_t *W, const float *omega, int64_t d, int6
 qlora_status launch_dequantize(const uint8_t *codes, ql::ScaleSrc sc, int64_t n,
                                uint16_t *out, hipStream_t st);
 
+// adapters.hip : the plan of a batch whose tokens use different adapters.
+// A plan is one device buffer of int32, all indices into the batch:
+//   tok   [M]     adapter of token m (-1: none)
+//   perm  [M]     token at position p: by adapter, none last, batch order inside
+//   sid   [M]     adapter of position p (-1: none)
+//   off   [n+2]   first position of adapter a; off[n]: of none; off[n+1] = M
+//   num   [4]     groups, splits
+//   grp   [2 g]   (adapter or n for none, first position): up to AD_TOK positions
+//   split [8 s]   (adapter, lo, hi, first slot or -1, index, count, 0, 0): positions
+//                 lo .. hi of one adapter; an adapter with one split has no slot
+// Every adapter has at least one split (an empty one when it has no token).
+constexpr int AD_TOK = 8;          // tokens of a group
+constexpr int AD_SPLITS = 6;       // splits of a batch that one adapter fills
+struct AdapterPlan {
+  int64_t M = 0;
+  int n = 0;
+  int *tok, *perm, *sid, *off, *num, *grp, *split;
+  int64_t max_groups, max_splits, max_slots;
+  int64_t split_tok;   // tokens of a split
+  size_t bytes;
+  AdapterPlan(void *data, int64_t M, int n);
+};
+qlora_status launch_adapter_plan(const int32_t *ids, const AdapterPlan &p, hipStream_t st);
+
 // lora_small.hip : small LoRA contractions and layout helpers
 // Up to four zero-padded / transposed bf16 copies in one launch:
 // dst (drows x dcols) [i][j] = src[i][j] (or src[j][i] when transpose), zero
@@ -74,6 +98,15 @@ struct SkinnyOut {
 qlora_status launch_skinny(const uint16_t *In, int64_t M, int64_t C, int nw, const SkinnyOut *o,
                            bool p_col, int r, int rp, int out2_ld, float s, hipStream_t st,
                            int *zero = nullptr, int64_t nzero = 0);
+// The same for a plan's batch: per group of the plan, out[m][t] = sum_c
+// In[m][c] P_a[t][c] with a's matrix at P + a * r * C; s_a * out as bf16 hi/lo
+// in plan order (M x rp). out (M x rp) and out2 (M x r) are in token order,
+// either may be NULL. p_col takes any r.
+qlora_status launch_skinny_adapters(const uint16_t *In, int64_t C, const uint16_t *P,
+                                    const float *scale, const AdapterPlan &plan, bool p_col,
+                                    int r, int rp, float *out, float *out2, uint16_t *hi,
+                                    uint16_t *lo, hipStream_t st, int *zero = nullptr,
+                                    int64_t nzero = 0);
 // Two problems out = s * sum_m In[m][c] * Q[m][t] rounded to bf16 (In M x C,
 // Q M x rp fp32) in one launch, including the reduction of its token splits.
 // transpose_out == 0: out is C x r (ld r); == 1: out is r x C (ld C).
@@ -96,20 +129,42 @@ size_t colacc_part_bytes(int64_t M, int64_t C0, int64_t C1, int rp);
 int64_t colacc_counter_count(int64_t C0, int64_t C1);
 int *colacc_counters(float *part, int64_t M, int64_t C0, int64_t C1, int rp);
 
+// The same per adapter of a plan: out_a = s_a * sum over a's tokens. Q is in
+// token order with leading dimension ldq (a.ldq = r or rp; 16-byte aligned).
+struct ColaccAdReq {
+  const uint16_t *In;
+  int64_t C;
+  const float *Q;
+  int ldq;
+  uint16_t *out;      // n matrices, C x r each (transpose_out: r x C)
+  int transpose_out;
+};
+qlora_status launch_colacc2_adapters(const ColaccAdReq &a, const ColaccAdReq &b,
+                                     const AdapterPlan &plan, int rp, int r, const float *scale,
+                                     float *part, hipStream_t st);
+size_t colacc_adapters_part_bytes(const AdapterPlan &plan, int64_t C0, int64_t C1, int rp);
+int64_t colacc_adapters_counter_count(const AdapterPlan &plan, int64_t C0, int64_t C1);
+int *colacc_adapters_counters(float *part, const AdapterPlan &plan, int64_t C0, int64_t C1,
+                              int rp);
+
 // gemm.hip : fused dequant-GEMM, forward (Y) and input-gradient (dX) forms.
-// The rank-r epilogue reads B (d x r) resp. A (r x k) in place.
+// The rank-r epilogue reads B (d x r) resp. A (r x k) in place. With a plan's
+// perm and sid (both or neither), rows run in plan order: B (A) holds one
+// matrix per adapter, hi and lo are in plan order, X and Y in token order.
 qlora_status launch_gemm_fwd(const uint8_t *codes, ql::ScaleSrc sc, int64_t d,
                              int64_t k, const uint16_t *X, int64_t M,
                              const uint16_t *B, int r, const uint16_t *Hs_hi,
                              const uint16_t *Hs_lo, int rp, uint16_t *Y,
-                             hipStream_t st);
+                             hipStream_t st, const int *perm = nullptr,
+                             const int *sid = nullptr);
 // keep (M x k/4 keep nibbles, or NULL): adapter-input dropout of the forward;
 // the rank-r term of dX is then kept per element and scaled by inv_keep.
 qlora_status launch_gemm_dx(const uint8_t *codes, ql::ScaleSrc sc, int64_t d,
                             int64_t k, const uint16_t *dY, int64_t M,
                             const uint16_t *A, int r, const uint16_t *Gs_hi,
                             const uint16_t *Gs_lo, int rp, uint16_t *dX,
-                            const uint8_t *keep, float inv_keep, hipStream_t st);
+                            const uint8_t *keep, float inv_keep, hipStream_t st,
+                            const int *perm = nullptr, const int *sid = nullptr);
 
 // gemv.hip : memory-bound forward for M <= 16, including the LoRA down
 // projection, for nw (1..4) weights that read the same X (sibling
@@ -129,6 +184,11 @@ struct GemvIn {
 qlora_status launch_gemv_fwd(int nw, const GemvIn *in, int64_t k, const uint16_t *X, int64_t M,
                              int r, int rp, float s, float *part, hipStream_t st);
 size_t gemv_part_bytes(int64_t dtot, int64_t k, int64_t M, int rp, int nw);
+// The same for one weight whose tokens use different adapters: in.Ap is
+// [n][r][k], in.Bp [n][d][r] (no padding), tok the adapter of each token.
+qlora_status launch_gemv_adapters(const GemvIn &in, int64_t k, const uint16_t *X, int64_t M,
+                                  int r, int rp, const int *tok, int n, const float *scale,
+                                  float *part, hipStream_t st);
 
 // merge.hip
 qlora_status launch_merge(const uint8_t *codes, ql::ScaleSrc sc, int64_t d,

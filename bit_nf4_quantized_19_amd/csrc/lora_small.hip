@@ -93,6 +93,10 @@ struct SkinnyArgs {
   float s;
   int *zero;        // counters a later launch of the same call needs zeroed (or NULL)
   int64_t nzero;
+  // many adapters: the plan's groups, token order and per-adapter scales
+  const int *perm, *off, *num, *grp;
+  const float *scale;
+  int n;
 };
 template <class T>
 QL_DEV T pick4s(int i, T a0, T a1, T a2, T a3) {
@@ -101,26 +105,56 @@ QL_DEV T pick4s(int i, T a0, T a1, T a2, T a3) {
 #define QL_SKPICK(f) pick4s(wi, a.w[0].f, a.w[1].f, a.w[2].f, a.w[3].f)
 
 constexpr int SK_TOK = 8;   // tokens per workgroup (of the 16 MFMA rows)
-template <bool PCOL>
+static_assert(SK_TOK == AD_TOK, "a plan's group is one workgroup's tokens");
+
+// B[row][t .. t + 7] of a C x r matrix as 16 bytes, ranks past r as zeros: one
+// load when rows are whole 16-byte pieces, else element by element.
+QL_DEV uint4 rank_piece(const uint16_t *row, int t, int r) {
+  if (t >= r) return ql::zero4();
+  if ((r & 7) == 0) return *(const uint4 *)(row + t);
+  uint32_t e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = row[t + i < r ? t + i : r - 1];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = t + i < r ? e[i] : 0u;
+  return make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
+                    e[6] | (e[7] << 16));
+}
+
+// AD (many adapters): workgroup x takes group x of the plan, up to SK_TOK
+// tokens of one adapter, whose matrix is at Pm + adapter * r * C; hi and lo go
+// to plan positions, out and out2 to tokens. Tokens without an adapter get
+// zeros and read nothing.
+template <bool PCOL, bool AD>
 __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
   if (a.zero && blockIdx.x == 0 && blockIdx.y == 0)
     for (int64_t i = threadIdx.x; i < a.nzero; i += 64 * SK_W) a.zero[i] = 0;
+  int ad = 0, ntok = SK_TOK;   // AD: adapter and token count of the group
+  int64_t pos0 = 0;            // AD: its first plan position
+  bool none = false;
+  if (AD) {
+    if ((int)blockIdx.x >= a.num[0]) return;
+    ad = min(a.grp[2 * blockIdx.x], a.n);
+    pos0 = a.grp[2 * blockIdx.x + 1];
+    ntok = (int)min<int64_t>(SK_TOK, min<int64_t>(a.off[ad + 1], a.M) - pos0);
+    none = ad == a.n;
+  }
   const int wi = (int)blockIdx.y / a.tbw;   // uniform: fields picked by selects
   const uint16_t *__restrict__ In = a.In;
-  const uint16_t *__restrict__ Pm = QL_SKPICK(P);
+  const uint16_t *__restrict__ Pm = QL_SKPICK(P) + (AD && !none ? (int64_t)ad * a.r * a.C : 0);
   float *__restrict__ out = QL_SKPICK(out);
   float *__restrict__ out2 = QL_SKPICK(out2);
   uint16_t *__restrict__ hi = QL_SKPICK(hi);
   uint16_t *__restrict__ lo = QL_SKPICK(lo);
   const int64_t M = a.M, C = a.C, cpw = a.cpw;
   const int r = a.r, rp = a.rp, out2_ld = a.out2_ld;
-  const float s = a.s;
+  const float s = !AD ? a.s : none ? 0.0f : a.scale[ad];
   DropParams dp;
   dp.k0 = QL_SKPICK(dp.k0);
   dp.k1 = QL_SKPICK(dp.k1);
   dp.thr = QL_SKPICK(dp.thr);
   dp.inv_keep = QL_SKPICK(dp.inv_keep);
-  dp.on = !PCOL && QL_SKPICK(dp.on);
+  dp.on = !PCOL && !AD && QL_SKPICK(dp.on);
   dp.mask_write = QL_SKPICK(dp.mask_write);
   dp.mask = QL_SKPICK(dp.mask);
   constexpr int PQ = 272;   // bytes per lane group in the transposition slot (256 + pad)
@@ -133,10 +167,14 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
   const int r16 = lane & 15, kq = lane >> 4;
   const int64_t mb = blockIdx.x;
   const int t0 = 16 * ((int)blockIdx.y % a.tbw);
-  const int64_t m = mb * SK_TOK + r16;
-  const bool m_ok = r16 < SK_TOK && m < M;   // MFMA rows past SK_TOK stay zero
+  int64_t m = mb * SK_TOK + r16;
+  bool m_ok = r16 < SK_TOK && m < M;   // MFMA rows past SK_TOK stay zero
+  if (AD) {
+    m_ok = r16 < ntok;
+    m = m_ok ? min<int64_t>((uint32_t)a.perm[pos0 + r16], M - 1) : 0;
+  }
   const uint16_t *inr = In + (m_ok ? m : 0) * C + 8 * kq;
-  const int64_t c_lo = wave * cpw, c_hi = min(C, c_lo + cpw);
+  const int64_t c_lo = wave * cpw, c_hi = none ? c_lo : min(C, c_lo + cpw);
   // !PCOL: A rows are loaded whole (lane -> row ra = lane / 4, 16-byte piece
   // pa = lane % 4 of the slice's 64 bytes, so a quarter-wave reads 4 rows of
   // 64 contiguous bytes) and re-laid out through the slot; rows past r read 0
@@ -168,7 +206,9 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
       }
       if (PCOL) {
         const int64_t row = cc + 8 * kq + rho;   // B row, t = t0 + 8 hf .. +7
-        if (row < c_hi) b[u] = *(const uint4 *)(Pm + row * r + t0 + 8 * hf);
+        if (row < c_hi)
+          b[u] = AD ? rank_piece(Pm + row * r, t0 + 8 * hf, r)
+                    : *(const uint4 *)(Pm + row * r + t0 + 8 * hf);
       }
     }
     if (!PCOL) {
@@ -216,16 +256,23 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
   const int t = t0 + r16;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t mm = mb * SK_TOK + 4 * kq + i;
-    if (4 * kq + i >= SK_TOK || mm >= M) continue;
+    int64_t mm = mb * SK_TOK + 4 * kq + i;
+    int64_t hl = mm;   // row of hi and lo
+    if (AD) {
+      if (4 * kq + i >= ntok) continue;
+      hl = pos0 + 4 * kq + i;
+      mm = min<int64_t>((uint32_t)a.perm[hl], M - 1);
+    } else if (4 * kq + i >= SK_TOK || mm >= M) {
+      continue;
+    }
     if (dp.on) v[i] *= dp.inv_keep;   // inverted dropout: kept elements scaled by 1/(1-p)
-    out[mm * rp + t] = v[i];
+    if (!AD || out) out[mm * rp + t] = v[i];
     if (out2 && t < out2_ld) out2[mm * out2_ld + t] = v[i];
     if (hi) {
       const float sv = s * v[i];
       const uint16_t hb = ql::f_to_bf16(sv);
-      hi[mm * rp + t] = hb;
-      lo[mm * rp + t] = ql::f_to_bf16(sv - ql::bf16_to_f(hb));
+      hi[hl * rp + t] = hb;
+      lo[hl * rp + t] = ql::f_to_bf16(sv - ql::bf16_to_f(hb));
     }
   }
 }
@@ -262,6 +309,15 @@ struct ColaccProb {
   float scale;         // s, times 1/(1-p) for a dropped input
   DropParams dp;       // dropout of In's elements (dp.on == 0: none)
   uint8_t *keep;       // M x C/4 keep nibbles written when drawing them (or NULL)
+  int ldq;             // AD: leading dimension of Q
+};
+
+// Many adapters: the plan's splits and token order, per-adapter scales.
+struct ColaccAd {
+  const int *perm, *num, *split;
+  const float *scale;
+  int64_t M;
+  int n, max_slots;
 };
 
 // Chunk staged through registers: this thread's 8 columns of one token row
@@ -273,13 +329,16 @@ struct CmRegs {
 };
 
 // Rows at or past M (here: the end of this workgroup's token range) read as 0.
-template <bool MK, int RPM, int KS>
+// AD: rows are plan positions of tokens perm[m].
+template <bool MK, int RPM, int KS, bool AD>
 QL_DEV void cm_load(CmRegs<RPM, KS> &R, const ColaccProb &P, int64_t M, int rp, int64_t m0, int64_t c0,
-                    int tid) {
+                    int tid, const ColaccAd &ad) {
 #pragma unroll
   for (int j = 0; j < KS; ++j) {
-    const int64_t m = m0 + 32 * j + (tid >> 3), c = c0 + 8 * (tid & 7);
+    int64_t m = m0 + 32 * j + (tid >> 3);
+    const int64_t c = c0 + 8 * (tid & 7);
     const bool ok = m < M && c < P.C;   // C % 8 == 0: the 8 columns are all in or all out
+    if (AD && ok) m = min<int64_t>((uint32_t)ad.perm[m], ad.M - 1);
     R.x[j] = ok ? *(const uint4 *)(P.In + m * P.C + c) : ql::zero4();
     if (P.dp.on && ok) {
       const uint64_t e = (uint64_t)m * (uint64_t)P.C + (uint64_t)c;
@@ -300,6 +359,21 @@ QL_DEV void cm_load(CmRegs<RPM, KS> &R, const ColaccProb &P, int64_t M, int rp, 
     const int f = tid + 256 * u;
     if (f >= nq) break;
     const int64_t mq = m0 + f / (rp / 4);
+    if (AD) {
+      const int t = 4 * (f % (rp / 4));
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mq < M && t < P.ldq) {
+        const float *q = P.Q + min<int64_t>((uint32_t)ad.perm[mq], ad.M - 1) * P.ldq + t;
+        if ((P.ldq & 3) == 0) {
+          v = *(const float4 *)q;
+        } else {
+          const int left = P.ldq - t;
+          v = make_float4(q[0], left > 1 ? q[1] : 0.f, left > 2 ? q[2] : 0.f, left > 3 ? q[3] : 0.f);
+        }
+      }
+      R.q[u] = v;
+      continue;
+    }
     R.q[u] = mq < M ? *(const float4 *)(P.Q + mq * rp + 4 * (f % (rp / 4)))
                     : make_float4(0.f, 0.f, 0.f, 0.f);
   }
@@ -375,11 +449,13 @@ size_t cm_lds_bytes(int rp) {
 }
 
 // RPM: the largest padded rank this instance handles (32, 64 or 128), which
-// sizes its registers.
-template <bool MK, int RPM, int KS>
+// sizes its registers. AD: grid row y is split y of the plan, which gives the
+// adapter, its positions and the slot of the split's partial sums; an adapter
+// with one split (or no token) writes its result from the accumulators.
+template <bool MK, int RPM, int KS, bool AD>
 __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p1, int64_t M,
                                                      int rp, int r, int64_t mps, int S,
-                                                     int *cnt) {
+                                                     int *cnt, ColaccAd ad) {
   extern __shared__ __align__(16) unsigned char cm_lds[];
   constexpr int TOK = 32 * KS, QS = cm_qs<KS>();
   uint32_t *s_in0 = (uint32_t *)cm_lds, *s_in1 = s_in0 + TOK * CM_INS;
@@ -394,8 +470,23 @@ __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p
   const ColaccProb &P = second ? p1 : p0;
   if (second) bx -= p0.blocks;
   const int64_t c0 = bx * CM_COLS;
-  const int split = blockIdx.y;
-  const int64_t m_lo = split * mps, m_hi = min(M, m_lo + mps);
+  int split = blockIdx.y;
+  int64_t m_lo = split * mps, m_hi = min(M, m_lo + mps);
+  int slot0 = 0;   // AD: first slot of the adapter's splits
+  uint16_t *out = P.out;
+  float scale = P.scale;
+  if (AD) {
+    if (split >= ad.num[1]) return;
+    const int *e = ad.split + 8 * split;
+    const int a = min(e[0], ad.n - 1);
+    m_lo = e[1];
+    m_hi = min<int64_t>(e[2], ad.M);
+    S = e[5];
+    slot0 = S > 1 ? min(e[3], ad.max_slots - S) : 0;
+    split = slot0 + e[4];
+    out += (int64_t)a * r * P.C;
+    scale = ad.scale[a];
+  }
   const int tbs = rp / 16;
   f32x4 acc[RPM / 16];
 #pragma unroll
@@ -409,21 +500,37 @@ __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p
   CmRegs<RPM, KS> R[CM_PF];
 #pragma unroll
   for (int i = 0; i < CM_PF - 1; ++i)
-    if (i < nch) cm_load<MK, RPM, KS>(R[i], P, m_hi, rp, m_lo + (int64_t)i * TOK, c0, tid);
+    if (i < nch) cm_load<MK, RPM, KS, AD>(R[i], P, m_hi, rp, m_lo + (int64_t)i * TOK, c0, tid, ad);
   for (int ch0 = 0; ch0 < nch; ch0 += CM_PF) {
 #pragma unroll
     for (int u = 0; u < CM_PF; ++u) {
       const int ch = ch0 + u;
       if (ch >= nch) break;
       if (ch + CM_PF - 1 < nch)
-        cm_load<MK, RPM, KS>(R[(u + CM_PF - 1) % CM_PF], P, m_hi, rp,
-                             m_lo + (int64_t)(ch + CM_PF - 1) * TOK, c0, tid);
+        cm_load<MK, RPM, KS, AD>(R[(u + CM_PF - 1) % CM_PF], P, m_hi, rp,
+                                 m_lo + (int64_t)(ch + CM_PF - 1) * TOK, c0, tid, ad);
       uint32_t *sin = (u & 1) ? s_in1 : s_in0;
       uint16_t *sqh = (u & 1) ? s_qh1 : s_qh0, *sql = (u & 1) ? s_ql1 : s_ql0;
       cm_store<RPM, KS>(R[u], sin, sqh, sql, rp, tid);
       __syncthreads();
       cm_compute<RPM, KS>(acc, sin, sqh, sql, tbs, wave, cl, g);
     }
+  }
+  if (AD && S == 1) {   // the adapter's only split: uniform over the workgroup
+    const int64_t cc = c0 + 16 * wave + cl;
+    if (cc >= P.C) return;
+#pragma unroll
+    for (int b = 0; b < RPM / 16; ++b) {
+      if (b >= tbs) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * b + 4 * g + i;
+        if (t < r)
+          out[P.transpose_out ? (int64_t)t * P.C + cc : cc * r + t] =
+              ql::f_to_bf16(scale * acc[b][i]);
+      }
+    }
+    return;
   }
   // lane holds out^T[16 b + 4 g + i][c0 + 16 wave + cl]. The partials are
   // published with agent-scope stores (written through to the level every
@@ -447,6 +554,7 @@ __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p
   }
   // the last workgroup of this column block adds the S partials in order
   int *ctr = cnt + (second ? p0.blocks : 0) + bx;
+  if (AD) ctr += slot0 * (p0.blocks + p1.blocks);   // one counter set per adapter with splits
   __builtin_amdgcn_s_waitcnt(0);   // this thread's stores have completed
   __syncthreads();
   if (tid == 0)
@@ -469,7 +577,7 @@ __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p
         const uint64_t *src[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int sp = s0 + u < S ? s0 + u : s0;
+          const int sp = slot0 + (s0 + u < S ? s0 + u : s0);
           src[u] = (const uint64_t *)(P.part + ((int64_t)sp * P.C + ccl) * rp + 16 * b + 4 * q4);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -493,15 +601,15 @@ __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p
       // four ranks are consecutive and aligned in out)
       uint32_t ob[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ob[i] = ql::f_to_bf16(P.scale * v[i]);
+      for (int i = 0; i < 4; ++i) ob[i] = ql::f_to_bf16(scale * v[i]);
       const int t4 = 16 * b + 4 * q4;
       if (cok && !P.transpose_out && (r & 3) == 0 && t4 < r) {
-        *(uint2 *)(P.out + cc * r + t4) = make_uint2(ob[0] | (ob[1] << 16), ob[2] | (ob[3] << 16));
+        *(uint2 *)(out + cc * r + t4) = make_uint2(ob[0] | (ob[1] << 16), ob[2] | (ob[3] << 16));
       } else if (cok) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (t4 + i < r)
-            P.out[P.transpose_out ? (int64_t)(t4 + i) * P.C + cc : cc * r + t4 + i] = (uint16_t)ob[i];
+            out[P.transpose_out ? (int64_t)(t4 + i) * P.C + cc : cc * r + t4 + i] = (uint16_t)ob[i];
       }
     }
   }
@@ -565,9 +673,42 @@ qlora_status launch_skinny(const uint16_t *In, int64_t M, int64_t C, int nw, con
   dim3 grid((unsigned)mbs, (unsigned)(nw * a.tbw));
   QlProf prof(QLORA_K_LORA_DOWN, st);
   if (p_col)
-    skinny_kernel<true><<<grid, 64 * SK_W, 0, st>>>(a);
+    skinny_kernel<true, false><<<grid, 64 * SK_W, 0, st>>>(a);
   else
-    skinny_kernel<false><<<grid, 64 * SK_W, 0, st>>>(a);
+    skinny_kernel<false, false><<<grid, 64 * SK_W, 0, st>>>(a);
+  QL_LAUNCH_CHECK();
+  return QLORA_OK;
+}
+
+qlora_status launch_skinny_adapters(const uint16_t *In, int64_t C, const uint16_t *P,
+                                    const float *scale, const AdapterPlan &plan, bool p_col,
+                                    int r, int rp, float *out, float *out2, uint16_t *hi,
+                                    uint16_t *lo, hipStream_t st, int *zero, int64_t nzero) {
+  SkinnyArgs a{};
+  for (int i = 0; i < 4; ++i)
+    a.w[i] = SkW{P, out, out2, hi, lo, DropParams{0u, 0u, 0u, 1.0f, 0}};
+  a.In = In;
+  a.M = plan.M;
+  a.C = C;
+  a.cpw = ql_rup(ql_cdiv(C, SK_W), 32);
+  a.r = r;
+  a.rp = rp;
+  a.tbw = rp / 16;
+  a.out2_ld = r;
+  a.zero = zero;
+  a.nzero = nzero;
+  a.perm = plan.perm;
+  a.off = plan.off;
+  a.num = plan.num;
+  a.grp = plan.grp;
+  a.scale = scale;
+  a.n = plan.n;
+  dim3 grid((unsigned)plan.max_groups, (unsigned)a.tbw);
+  QlProf prof(QLORA_K_LORA_DOWN, st);
+  if (p_col)
+    skinny_kernel<true, true><<<grid, 64 * SK_W, 0, st>>>(a);
+  else
+    skinny_kernel<false, true><<<grid, 64 * SK_W, 0, st>>>(a);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
@@ -610,20 +751,61 @@ qlora_status launch_colacc2(const ColaccReq &a, const ColaccReq &b, int64_t M, i
   QlProf prof(QLORA_K_LORA_COLACC, st);
   // MK: the adapter input's keep bits come from the mask the forward stored
   const bool mk = p1.dp.on && p1.dp.mask && !p1.dp.mask_write;
+  const ColaccAd none{};
   // chunk depth per rank bound: the LDS of two chunks stays within 64 KB
 #define QL_CM(RPV, KSV)                                                                   \
   {                                                                                       \
     const size_t lds = cm_lds_bytes<KSV>(rp);                                             \
     if (mk)                                                                               \
-      colacc_kernel<true, RPV, KSV><<<grid, 256, lds, st>>>(p0, p1, M, rp, r, mps, (int)S, cnt); \
+      colacc_kernel<true, RPV, KSV, false><<<grid, 256, lds, st>>>(p0, p1, M, rp, r, mps, (int)S, cnt, none); \
     else                                                                                  \
-      colacc_kernel<false, RPV, KSV><<<grid, 256, lds, st>>>(p0, p1, M, rp, r, mps, (int)S, cnt); \
+      colacc_kernel<false, RPV, KSV, false><<<grid, 256, lds, st>>>(p0, p1, M, rp, r, mps, (int)S, cnt, none); \
   }
   if (rp <= 16) QL_CM(16, 4)
   else if (rp <= 32) QL_CM(32, 2)
   else if (rp <= 64) QL_CM(64, 2)
   else QL_CM(128, 1)
 #undef QL_CM
+  QL_LAUNCH_CHECK();
+  return QLORA_OK;
+}
+
+size_t colacc_adapters_part_bytes(const AdapterPlan &plan, int64_t C0, int64_t C1, int rp) {
+  return (size_t)ql_rup(plan.max_slots * (C0 + C1) * rp * 4, 256) +
+         colacc_adapters_counter_count(plan, C0, C1) * 4;
+}
+
+int64_t colacc_adapters_counter_count(const AdapterPlan &plan, int64_t C0, int64_t C1) {
+  return plan.max_slots * colacc_counter_count(C0, C1);
+}
+
+int *colacc_adapters_counters(float *part, const AdapterPlan &plan, int64_t C0, int64_t C1,
+                              int rp) {
+  return (int *)((char *)part + ql_rup(plan.max_slots * (C0 + C1) * rp * 4, 256));
+}
+
+qlora_status launch_colacc2_adapters(const ColaccAdReq &a, const ColaccAdReq &b,
+                                     const AdapterPlan &plan, int rp, int r, const float *scale,
+                                     float *part, hipStream_t st) {
+  if (rp % 16 || rp > CM_MAXRP) return QLORA_ERR_UNSUPPORTED;
+  int *cnt = colacc_adapters_counters(part, plan, a.C, b.C, rp);   // zeroed by the launch before
+  const DropParams nodrop{0u, 0u, 0u, 1.0f, 0};
+  ColaccProb p0{a.In, a.C, a.Q, part, ql_cdiv(a.C, CM_COLS), a.out, a.transpose_out, 0.0f, nodrop,
+                nullptr, a.ldq};
+  ColaccProb p1{b.In, b.C, b.Q, part + plan.max_slots * a.C * rp, ql_cdiv(b.C, CM_COLS), b.out,
+                b.transpose_out, 0.0f, nodrop, nullptr, b.ldq};
+  const ColaccAd ad{plan.perm, plan.num, plan.split, scale, plan.M, plan.n,
+                    (int)plan.max_slots};
+  dim3 grid((unsigned)(p0.blocks + p1.blocks), (unsigned)plan.max_splits);
+  QlProf prof(QLORA_K_LORA_COLACC, st);
+#define QL_CMA(RPV, KSV)                                                                 \
+  colacc_kernel<false, RPV, KSV, true><<<grid, 256, cm_lds_bytes<KSV>(rp), st>>>(        \
+      p0, p1, plan.M, rp, r, 0, 1, cnt, ad);
+  if (rp <= 16) { QL_CMA(16, 4) }
+  else if (rp <= 32) { QL_CMA(32, 2) }
+  else if (rp <= 64) { QL_CMA(64, 2) }
+  else { QL_CMA(128, 1) }
+#undef QL_CMA
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }

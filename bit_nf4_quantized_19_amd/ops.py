@@ -52,7 +52,8 @@ _vp, _i64, _i32, _f32, _sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
                               ctypes.c_float, ctypes.c_size_t)
 _PW = ctypes.POINTER(NF4WeightC)
 
-#: exported symbol -> (restype, argtypes); mirrors include/qlora_nf4.h
+#: exported symbol -> (restype, argtypes); mirrors include/qlora_nf4.h and the
+#: headers named below
 SIGNATURES = {
     "qlora_nf4_quantize": (ctypes.c_int, [_vp, _PW, _vp, _sz, _vp]),
     "qlora_nf4_dequantize": (ctypes.c_int, [_PW, _vp, _vp]),
@@ -81,6 +82,18 @@ SIGNATURES = {
     "qlora_adamw_step": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
     "qlora_adamw_page_out": (ctypes.c_int, [_vp, _vp, _i32, _i64, _vp]),
     "qlora_adamw_page_in": (ctypes.c_int, [_vp, _vp, _i32, _i64, _vp]),
+    # include/qlora_adapters.h
+    "qlora_adapter_plan_bytes": (_sz, [_i64, _i32]),
+    "qlora_adapter_plan_build": (ctypes.c_int, [_vp, _vp, _vp]),
+    "qlora_adapters_workspace_bytes": (_sz, [_i32, _i64, _i64, _i64, _i32, _i32]),
+    "qlora_linear_fwd_adapters": (ctypes.c_int, [_PW, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_linear_bwd_adapters": (ctypes.c_int, [_PW, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                 _sz, _vp]),
+    # include/qlora_logprobs.h
+    "qlora_token_logprobs_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32]),
+    "qlora_token_logprobs": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _sz,
+                                            _vp]),
+    "qlora_token_logprobs_bwd": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 
 #: the timing build's extra symbols; mirrors include/qlora_nf4_timing.h
@@ -96,7 +109,8 @@ TIMING_SIGNATURES = {
 #: ids 8 and 10 are reserved and never recorded
 KERNELS = ["quantize", "double_quant", "dequantize", "gemm_fwd", "gemm_dx", "gemv",
            "gemv_epilogue", "lora_down", "lora_reduce", "lora_colacc", "lora_colacc_reduce",
-           "merge", "layout", "adamw", "loftq_product", "loftq_small", "residual"]
+           "merge", "layout", "adamw", "loftq_product", "loftq_small", "residual", "adapter_plan",
+           "logprobs", "logprobs_grad"]
 
 
 def _load(path: str, signatures: dict) -> ctypes.CDLL:
@@ -507,6 +521,271 @@ def adamw_page_in(dev, host, stream=None):
     _page("qlora_adamw_page_in", dev, host, stream)
 
 
+# ---------------------------------------------------------------------------
+# many adapters on one base weight (include/qlora_adapters.h)
+def _device_tensors(*named):
+    """Every (tensor, name, dtype, shape) contiguous, of that type and shape,
+    and on the current device (the one the stream belongs to)."""
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t, name, dtype, shape in named:
+        if not t.is_cuda or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape "
+                             f"{tuple(shape)}")
+        if t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, not on the current device {cur}")
+
+
+def _on(stream):
+    """Context in which what a call allocates belongs to its stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+class AdapterPlanC(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("n", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("data", ctypes.c_void_p), ("bytes", ctypes.c_size_t)]
+
+
+class AdaptersC(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("r", ctypes.c_int32), ("A", ctypes.c_void_p),
+                ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+@dataclass
+class AdapterPlan:
+    """Which of ``n`` adapters each of ``M`` tokens uses, laid out on the
+    device for the many-adapter linears of one batch (``adapter_plan``)."""
+    M: int
+    n: int
+    data: torch.Tensor
+
+    def c_struct(self) -> AdapterPlanC:
+        return AdapterPlanC(self.M, self.n, 0, self.data.data_ptr(), self.data.numel())
+
+
+def adapter_plan(ids: torch.Tensor, n: int, out: AdapterPlan | None = None,
+                 stream=None) -> AdapterPlan:
+    """Plan of a batch: ids (int32, one per token) is the adapter of each
+    token, any value outside [0, n) meaning none. Built on the device in one
+    launch; every linear the batch passes takes the same plan. ``out`` (a plan
+    of the same M and n) is rebuilt in place."""
+    M = ids.numel()
+    _device_tensors((ids, "ids", torch.int32, (M,)))
+    if out is None:
+        nbytes = int(lib().qlora_adapter_plan_bytes(M, n))
+        if nbytes == 0:
+            raise QLoRAError(QLORA_ERR_UNSUPPORTED if M and n > 0 else QLORA_ERR_INVALID_ARG,
+                             "adapter_plan")
+        with _on(stream):
+            out = AdapterPlan(M, n, torch.empty(nbytes, dtype=torch.uint8, device=ids.device))
+    elif out.M != M or out.n != n:
+        raise ValueError(f"out is a plan of {out.M} tokens and {out.n} adapters, not {M} and {n}")
+    c = out.c_struct()
+    _check(lib().qlora_adapter_plan_build(ids.data_ptr(), ctypes.addressof(c), _stream(stream)),
+           "qlora_adapter_plan_build")
+    return out
+
+
+def adapters_workspace_bytes(op: int, d: int, k: int, M: int, n: int, r: int) -> int:
+    b = lib().qlora_adapters_workspace_bytes(op, d, k, M, n, r)
+    if b == ctypes.c_size_t(-1).value:
+        raise QLoRAError(QLORA_ERR_UNSUPPORTED, "adapters_workspace_bytes")
+    return int(b)
+
+
+def adapters_workspace(plan: AdapterPlan, d: int, k: int, r: int,
+                       backward: bool = False) -> torch.Tensor:
+    """Workspace of the forward (and of the backward too, when asked) of a
+    d x k weight for the plan's batch; calls on one stream can share it."""
+    b = adapters_workspace_bytes(OP_FWD, d, k, plan.M, plan.n, r)
+    if backward:
+        b = max(b, adapters_workspace_bytes(OP_BWD, d, k, plan.M, plan.n, r))
+    return _workspace(b, plan.data.device, None)[0]
+
+
+def _adapter_args(w: NF4Weight, X, A, B, scale, plan: AdapterPlan):
+    if A.dim() != 3:
+        raise ValueError("A must be n x r x k")
+    n, r = A.shape[0], A.shape[1]
+    if plan.n != n:
+        raise ValueError(f"the plan is for {plan.n} adapters, A holds {n}")
+    _device_tensors((X, "X", torch.bfloat16, (plan.M, w.k)), (A, "A", torch.bfloat16, (n, r, w.k)),
+                    (B, "B", torch.bfloat16, (n, w.d, r)), (scale, "scale", torch.float32, (n,)))
+    return r, AdaptersC(n, r, A.data_ptr(), B.data_ptr(), scale.data_ptr())
+
+
+def linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                        scale: torch.Tensor, plan: AdapterPlan, save_h: bool = True,
+                        Y: torch.Tensor | None = None, H: torch.Tensor | None = None,
+                        ws: torch.Tensor | None = None, stream=None):
+    """Y[m] = X[m] W'^T + s_a (X[m] A_a^T) B_a^T with a the adapter of token m
+    in ``plan``: A (n x r x k), B (n x d x r) bf16, scale (n) float32 holding
+    s_a. Returns (Y, H or None); H (M x r float32) is what the backward needs."""
+    r, ad = _adapter_args(w, X, A, B, scale, plan)
+    with _on(stream):
+        if Y is None:
+            Y = torch.empty(plan.M, w.d, dtype=torch.bfloat16, device=X.device)
+        if save_h and H is None:
+            H = torch.empty(plan.M, r, dtype=torch.float32, device=X.device)
+        if ws is None:
+            ws = _workspace(adapters_workspace_bytes(OP_FWD, w.d, w.k, plan.M, plan.n, r),
+                            X.device, None)[0]
+    _device_tensors((Y, "Y", torch.bfloat16, (plan.M, w.d)))
+    if save_h:
+        _device_tensors((H, "H", torch.float32, (plan.M, r)))
+    cw, cp = w.c_struct(), plan.c_struct()
+    _check(lib().qlora_linear_fwd_adapters(ctypes.byref(cw), X.data_ptr(), ctypes.addressof(ad),
+                                           ctypes.addressof(cp), Y.data_ptr(),
+                                           H.data_ptr() if save_h else None, ws.data_ptr(),
+                                           ws.numel() * ws.element_size(), _stream(stream)),
+           "qlora_linear_fwd_adapters")
+    return Y, (H if save_h else None)
+
+
+def linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                        scale: torch.Tensor, plan: AdapterPlan, dY: torch.Tensor,
+                        H: torch.Tensor | None = None, need_dx: bool = True, dX=None, dA=None,
+                        dB=None, ws: torch.Tensor | None = None, stream=None):
+    """Backward of ``linear_fwd_adapters``: (dX or None, dA (n x r x k), dB
+    (n x d x r)); adapters without tokens get zero gradients. H as the forward
+    returned it, or None to recompute it."""
+    r, ad = _adapter_args(w, X, A, B, scale, plan)
+    with _on(stream):
+        if need_dx and dX is None:
+            dX = torch.empty_like(X)
+        if dA is None:
+            dA = torch.empty_like(A)
+        if dB is None:
+            dB = torch.empty_like(B)
+        if ws is None:
+            ws = _workspace(adapters_workspace_bytes(OP_BWD, w.d, w.k, plan.M, plan.n, r),
+                            X.device, None)[0]
+    _device_tensors((dY, "dY", torch.bfloat16, (plan.M, w.d)), (dA, "dA", torch.bfloat16, A.shape),
+                    (dB, "dB", torch.bfloat16, B.shape))
+    if need_dx:
+        _device_tensors((dX, "dX", torch.bfloat16, X.shape))
+    if H is not None:
+        _device_tensors((H, "H", torch.float32, (plan.M, r)))
+    cw, cp = w.c_struct(), plan.c_struct()
+    _check(lib().qlora_linear_bwd_adapters(ctypes.byref(cw), X.data_ptr(), ctypes.addressof(ad),
+                                           ctypes.addressof(cp), dY.data_ptr(), _ptr(H),
+                                           dX.data_ptr() if need_dx else None, dA.data_ptr(),
+                                           dB.data_ptr(), ws.data_ptr(),
+                                           ws.numel() * ws.element_size(), _stream(stream)),
+           "qlora_linear_bwd_adapters")
+    return (dX if need_dx else None), dA, dB
+
+
+# ---------------------------------------------------------------------------
+# log probabilities of given tokens (include/qlora_logprobs.h)
+class LogitsC(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("N", ctypes.c_int64), ("V", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+MAX_TOP = 32
+_LOGITS_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+@dataclass
+class TokenLogprobs:
+    """What ``token_logprobs`` computes for N rows of logits."""
+    logprob: torch.Tensor                       # float32 [N]
+    entropy: torch.Tensor                       # float32 [N]
+    stats: torch.Tensor                         # float32 [N, 2]: row maximum, log of the sum
+    top_logprobs: torch.Tensor | None = None    # float32 [N, top]
+    top_ids: torch.Tensor | None = None         # int64 [N, top]
+
+    @staticmethod
+    def empty(N: int, top: int = 0, device="cuda") -> "TokenLogprobs":
+        f = dict(dtype=torch.float32, device=device)
+        out = TokenLogprobs(torch.empty(N, **f), torch.empty(N, **f), torch.empty(N, 2, **f))
+        if top:
+            out.top_logprobs = torch.empty(N, top, **f)
+            out.top_ids = torch.empty(N, top, dtype=torch.int64, device=device)
+        return out
+
+
+def _logits(t: torch.Tensor, name: str) -> LogitsC:
+    if t.dim() != 2 or t.dtype not in _LOGITS_DTYPES or not t.is_cuda:
+        raise ValueError(f"{name} must be a two-dimensional bfloat16 or float32 CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    N, V = t.shape
+    ld = t.stride(0) if N > 1 else max(V, t.stride(0))
+    if (V > 1 and t.stride(1) != 1) or ld < V:
+        raise ValueError(f"{name} must have rows of consecutive elements that do not overlap")
+    return LogitsC(t.data_ptr(), N, V, ld, _LOGITS_DTYPES[t.dtype], 0)
+
+
+def logprobs_workspace(logits: torch.Tensor, top: int = 0) -> torch.Tensor | None:
+    """Workspace of ``token_logprobs`` for logits of this shape (None: none needed)."""
+    b = lib().qlora_token_logprobs_workspace_bytes(logits.shape[0], logits.shape[1],
+                                                   _LOGITS_DTYPES.get(logits.dtype, -1), top)
+    if b == ctypes.c_size_t(-1).value:
+        raise QLoRAError(QLORA_ERR_UNSUPPORTED, "logprobs_workspace")
+    return _workspace(int(b), logits.device, None)[0]
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0,
+                   out: TokenLogprobs | None = None, ws: torch.Tensor | None = None,
+                   stream=None) -> TokenLogprobs:
+    """Per row of logits (N x V bf16 or float32, rows at any stride): the log
+    probability of its target (int64; outside [0, V): ignored, 0), the
+    entropy, and the ``top`` (0..32) best alternatives by value, then index."""
+    c = _logits(logits, "logits")
+    N = c.N
+    if not 0 <= top <= min(c.V, MAX_TOP):
+        raise QLoRAError(QLORA_ERR_UNSUPPORTED, f"token_logprobs(top={top})")
+    with _on(stream):
+        if out is None:
+            out = TokenLogprobs.empty(N, top, logits.device)
+        if ws is None:
+            ws = logprobs_workspace(logits, top)
+    _device_tensors((targets, "targets", torch.int64, (N,)),
+                    (out.logprob, "out.logprob", torch.float32, (N,)),
+                    (out.entropy, "out.entropy", torch.float32, (N,)),
+                    (out.stats, "out.stats", torch.float32, (N, 2)))
+    if top:
+        _device_tensors((out.top_logprobs, "out.top_logprobs", torch.float32, (N, top)),
+                        (out.top_ids, "out.top_ids", torch.int64, (N, top)))
+    _check(lib().qlora_token_logprobs(ctypes.addressof(c), targets.data_ptr(),
+                                      out.logprob.data_ptr(), out.stats.data_ptr(),
+                                      out.entropy.data_ptr(), top,
+                                      _ptr(out.top_logprobs) if top else None,
+                                      _ptr(out.top_ids) if top else None, _ptr(ws),
+                                      0 if ws is None else ws.numel() * ws.element_size(),
+                                      _stream(stream)), "qlora_token_logprobs")
+    return out
+
+
+def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lp: TokenLogprobs,
+                       dlogprob: torch.Tensor, dentropy: torch.Tensor | None = None,
+                       dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of the logits for upstream gradients of ``lp.logprob`` and
+    (optional) ``lp.entropy``, with ``lp`` as the forward returned it.
+    ``dlogits`` may be ``logits`` itself, which is then overwritten."""
+    c = _logits(logits, "logits")
+    N = c.N
+    if dlogits is None:
+        with _on(stream):
+            dlogits = torch.empty(N, c.V, dtype=logits.dtype, device=logits.device)
+    co = _logits(dlogits, "dlogits")
+    if (co.N, co.V, co.dtype) != (N, c.V, c.dtype):
+        raise ValueError("dlogits must have the shape and type of logits")
+    _device_tensors((targets, "targets", torch.int64, (N,)),
+                    (lp.stats, "lp.stats", torch.float32, (N, 2)),
+                    (lp.entropy, "lp.entropy", torch.float32, (N,)),
+                    (dlogprob, "dlogprob", torch.float32, (N,)))
+    if dentropy is not None:
+        _device_tensors((dentropy, "dentropy", torch.float32, (N,)))
+    _check(lib().qlora_token_logprobs_bwd(ctypes.addressof(c), targets.data_ptr(),
+                                          lp.stats.data_ptr(), lp.entropy.data_ptr(),
+                                          dlogprob.data_ptr(), _ptr(dentropy),
+                                          ctypes.addressof(co), _stream(stream)),
+           "qlora_token_logprobs_bwd")
+    return dlogits
+
+
 def profile_begin(cap: int = 4096, kernels=None):
     """Start bracketing kernel launches of the timing build with HIP events
     (include/qlora_nf4_timing.h); only calls made inside ``timing_build()``
@@ -535,4 +814,6 @@ __all__ = ["NF4Weight", "QLoRAError", "quantize", "dequantize", "linear_fwd", "l
            "merge", "storage_bytes", "workspace_bytes", "codebook", "lib",
            "OP_QUANTIZE", "OP_FWD", "OP_BWD", "SIGNATURES", "LIB_PATH", "KERNELS",
            "profile_begin", "profile_end", "profile_query", "timing_build", "timing_lib",
-           "TIMING_LIB_PATH"]
+           "TIMING_LIB_PATH", "AdapterPlan", "adapter_plan", "adapters_workspace",
+           "adapters_workspace_bytes", "linear_fwd_adapters", "linear_bwd_adapters",
+           "TokenLogprobs", "token_logprobs", "token_logprobs_bwd", "logprobs_workspace"]

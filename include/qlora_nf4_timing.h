@@ -35,7 +35,8 @@ enum {
   QLORA_K_LORA_DOWN = 7, QLORA_K_LORA_REDUCE = 8, QLORA_K_LORA_COLACC = 9,
   QLORA_K_LORA_COLACC_REDUCE = 10, QLORA_K_MERGE = 11, QLORA_K_LAYOUT = 12,
   QLORA_K_ADAMW = 13, QLORA_K_LOFTQ_PRODUCT = 14, QLORA_K_LOFTQ_SMALL = 15,
-  QLORA_K_RESIDUAL = 16, QLORA_K_COUNT = 17
+  QLORA_K_RESIDUAL = 16, QLORA_K_ADAPTER_PLAN = 17, QLORA_K_LOGPROBS = 18,
+  QLORA_K_LOGPROBS_GRAD = 19, QLORA_K_COUNT = 20
 };
 QLORA_API qlora_status qlora_profile_begin(int32_t cap, uint32_t mask);
 QLORA_API qlora_status qlora_profile_end(void);

@@ -22,6 +22,10 @@ Modules
 ``oracle.loftq`` LoftQ initialisation: randomized rank-r SVD (float64,
                  numpy QR/SVD as steps), LoRA factors, the float32 residual
                  W - s B A rounded to bf16, and the alternation with NF4.
+``oracle.adapters`` The LoRA linear with an adapter per token (many adapters on
+                 one base): ``oracle.lora`` on each adapter's tokens.
+``oracle.logprobs`` Log probabilities of given tokens, entropy, the best
+                 alternatives and the gradient of the logits, in float64.
 
 Every function cites the page passage it follows. A page is cited by its
 title and section, e.g. "QLoRA glossary (Ultralytics), 'QLoRA 的工作原理'".

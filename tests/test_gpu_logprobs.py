@@ -1,0 +1,264 @@
+"""Token log probabilities, entropy, alternatives and the logits' gradient
+against the float64 oracle.
+
+Bounds. t = x - m is one float32 subtraction (2^-24 |t|). A term of
+z = sum exp(t) is off by 2^-22 (the exponential) + 2^-23 |t| (its argument's
+rounding and scaling) of itself; weighted by p that is 2^-22 + 2^-23 T with
+T = sum p |t|. A float32 sum in which no addend passes more than V / 64 + 64
+additions adds (V / 64 + 64) 2^-24. So l = log z is off by
+ez = 2^-22 + 2^-23 T + (V / 64 + 64) 2^-24, plus 2^-22 |l|; the entropy, whose
+second sum has the same relative errors on its magnitude T, by
+2 (1 + T) ez + 2^-22 |l|. p = exp(logp) is off by the error of logp plus
+2^-21 + 2^-23 |logp| of itself. Gradients are rounded once to their type."""
+
+import numpy as np
+import pytest
+
+from oracle import logprobs as olp
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from bit_nf4_quantized_19_amd import ops as o
+    o.lib()
+    return o
+
+
+def errors(x):
+    """Per row: bound on l, bound on the entropy, T."""
+    N, V = x.shape
+    el, ee = np.zeros(N), np.zeros(N)
+    for i in range(N):
+        logp, p, ent = olp.row(x[i])
+        fin = np.isfinite(x[i])
+        if not np.isfinite(ent) or not fin.any():
+            continue
+        l = (x[i].max() - x[i][fin] + logp[fin])[0] * -1     # noqa: E741
+        T = (p[fin] * (x[i].max() - x[i][fin])).sum()
+        ez = 4 * U + 2 * U * T + (V / 64 + 64) * U
+        el[i] = ez + 4 * U * abs(l)
+        ee[i] = 2 * (1 + T) * ez + 4 * U * abs(l)
+    return el, ee
+
+
+def logits_of(N, V, ld, dtype, seed, std=2.0):
+    g = torch.Generator().manual_seed(seed)
+    buf = torch.randn(N, ld, generator=g) * std
+    return buf.to(dtype).cuda()
+
+
+def check(ops, buf, V, targets, top, dent=True, ws=None):
+    """Forward and backward of buf[:, :V]; the rest of buf and of the gradient's
+    buffer has to stay as it is."""
+    N = buf.shape[0]
+    x = buf[:, :V]
+    before = buf.clone()
+    t = torch.from_numpy(targets).cuda()
+    lp = ops.token_logprobs(x, t, top=top)
+    rng = np.random.default_rng(5)
+    g, e = rng.standard_normal(N).astype(np.float32), rng.standard_normal(N).astype(np.float32)
+    g[N // 2] = e[N // 2] = 0.0       # a row that takes no part
+    gd, ed = torch.from_numpy(g).cuda(), torch.from_numpy(e).cuda()
+    out = torch.full((N, V + 9), 5.0, dtype=buf.dtype, device="cuda")
+    dx = ops.token_logprobs_bwd(x, t, lp, gd, dentropy=ed if dent else None, dlogits=out[:, :V])
+    torch.cuda.synchronize()
+    assert torch.equal(buf.view(torch.int16), before.view(torch.int16))
+    assert bool((out[:, V:] == 5.0).all())
+
+    xh = x.double().cpu().numpy()
+    wl, we, wt, wi = olp.forward(xh, targets, top)
+    el, ee = errors(xh)
+    m = np.where(np.isfinite(xh), xh, -np.inf).max(1)
+    has = (targets >= 0) & (targets < V)
+
+    def near(got, want, tol, what):
+        got = got.double().cpu().numpy()
+        same = (got == want) | (np.isnan(got) & np.isnan(want))
+        with np.errstate(invalid="ignore"):
+            ok = same | (abs(got - want) <= tol)
+        assert ok.all(), (what, np.argwhere(~ok)[:4].tolist(), got[~ok][:4], want[~ok][:4])
+
+    with np.errstate(invalid="ignore"):
+        xt = np.where(has, xh[np.arange(N), np.clip(targets, 0, V - 1)], m)
+        near(lp.logprob, wl, el + 2 * U * (abs(m - xt) + abs(wl)), "logprob")
+        near(lp.entropy, we, ee, "entropy")
+        if top:
+            assert (lp.top_ids.cpu().numpy() == wi).all()
+            near(lp.top_logprobs, wt, el[:, None] + 2 * U * (abs(wt) * 2 + 1e-30) +
+                 4 * U * abs(m[:, None] - np.take_along_axis(xh, wi, 1)), "top")
+    want = olp.backward(xh, targets, g, e if dent else None)
+    tol = np.zeros_like(want)
+    for i in range(N):
+        logp, p, ent = olp.row(xh[i])
+        if not np.isfinite(ent):
+            continue
+        gi, ei = (g[i] if has[i] else 0.0), (e[i] if dent else 0.0)
+        lf = np.where(p > 0, logp, 0.0)
+        dl = el[i] + 2 * U * abs(lf) + 2 * U * abs(np.where(p > 0, xh[i] - m[i], 0.0))
+        dp = dl + 8 * U + 2 * U * abs(lf)
+        mag = abs(gi) + abs(ei) * (abs(lf) + abs(ent))
+        tol[i] = p * (mag * (dp + 4 * U) + abs(ei) * (dl + ee[i])) + 4 * U * abs(want[i])
+        if has[i]:
+            tol[i][targets[i]] += 4 * U * abs(gi)
+        tol[i] += 1e-37       # results below the smallest normal number
+    half = 2.0 ** -8 if buf.dtype == torch.bfloat16 else U
+    near(dx, want, tol + half * (abs(want) + tol), "gradient")
+    return lp, dx
+
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("N,V,ld,dtype,top", [
+    (1, 1, 1, BF, 1), (3, 2, 2, F32, 2), (2, 7, 7, BF, 5), (5, 63, 64, F32, 32),
+    (1, 255, 300, BF, 20), (4, 2048, 2048, BF, 20), (3, 2049, 2049, F32, 32),
+    (2, 4097, 4099, BF, 32), (1, 32000, 32000, BF, 5), (40, 32000, 32000, BF, 0),
+    (3, 50257, 50304, BF, 1), (2, 50257, 50257, F32, 20), (1, 131072, 131072, F32, 32),
+    (2, 131073, 131080, BF, 20), (1, 300007, 300007, BF, 32), (600, 1000, 1001, BF, 3),
+    (700, 257, 257, F32, 0), (1100, 33000, 33000, BF, 2),
+])
+def test_matches_the_oracle(ops, N, V, ld, dtype, top):
+    print(f"[logprobs] N={N} V={V} ld={ld} {dtype} top={top}", flush=True)
+    buf = logits_of(N, V, ld, dtype, N + V)
+    rng = np.random.default_rng(V)
+    t = rng.integers(0, V, N)
+    t[::5] = rng.choice([-100, -1, V, 1 << 40])
+    t[0] = V - 1
+    check(ops, buf, V, t, top, dent=V % 2 == 1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [100, 40000])
+def test_special_rows(ops, V, dtype):
+    print(f"[logprobs special] V={V} {dtype}", flush=True)
+    buf = logits_of(17, V, V, dtype, 3)
+    lowest, inf = torch.finfo(dtype).min, float("inf")
+    buf[0] = -inf                              # nothing allowed
+    buf[1] = lowest                            # a mask of the type's lowest value everywhere
+    buf[2, : V - 1] = lowest                   # one word left
+    buf[3, 1:] = -inf                          # one word left, the rest banned
+    buf[4, V // 2] = inf
+    buf[5, V // 3] = float("nan")
+    buf[6] = -inf
+    buf[6, 9] = float("nan")                   # banned but for a NaN
+    buf[7] = 1.5                               # all equal: ties by index
+    buf[8] = 0.0
+    buf[8, 1::2] = -0.0                        # the two zeros are equal
+    buf[9] = torch.finfo(dtype).max
+    buf[10] = 1000.0 + buf[10]
+    buf[11] = -1000.0 + buf[11]
+    buf[12, ::2] = -inf
+    buf[13, 5] = 300.0                         # all of the probability on one word
+    buf[14] = torch.arange(V, device="cuda").to(dtype)        # ascending
+    buf[15] = -torch.arange(V, device="cuda").float().to(dtype)
+    buf[16] = float("nan")
+    t = np.arange(17) % V
+    t[3], t[8], t[12] = 0, -100, 1             # row 12's target is banned
+    check(ops, buf, V, t, 20)
+    check(ops, buf, V, np.full(17, -100), 3, dent=False)      # nothing to learn: zeros
+
+
+def test_gradient_in_place_strides_and_repeats(ops):
+    for dtype, V, ld in ((BF, 1001, 1001), (F32, 4096, 5000), (BF, 32001, 32064)):
+        buf = logits_of(37, V, ld, dtype, 9)
+        x = buf[:, :V]
+        t = torch.randint(0, V, (37,), device="cuda")
+        g, e = torch.randn(37, device="cuda"), torch.randn(37, device="cuda")
+        lp = ops.token_logprobs(x, t, top=4)
+        lp2 = ops.token_logprobs(x, t, top=4)
+        dx = ops.token_logprobs_bwd(x, t, lp, g, dentropy=e)
+        assert dx.is_contiguous()
+        tail = buf[:, V:].clone()
+        same = ops.token_logprobs_bwd(x, t, lp, g, dentropy=e, dlogits=x)
+        torch.cuda.synchronize()
+        assert same.data_ptr() == buf.data_ptr() and torch.equal(x, dx)
+        assert torch.equal(buf[:, V:], tail)
+        for n in ("logprob", "entropy", "stats", "top_logprobs", "top_ids"):
+            assert torch.equal(getattr(lp, n), getattr(lp2, n)), n
+
+
+def test_long_offsets(ops):
+    # rows whose start passes 2^31 elements
+    V, ld, N = 1000, (1 << 31) + 64, 2
+    buf = torch.empty(N * ld - 64, dtype=BF, device="cuda")
+    x = buf.as_strided((N, V), (ld, 1))
+    x.copy_(logits_of(N, V, V, BF, 1))
+    t = torch.tensor([3, 999], device="cuda")
+    lp = ops.token_logprobs(x, t, top=3)
+    near = ops.token_logprobs(x.contiguous(), t, top=3)
+    g = torch.ones(N, device="cuda")
+    dx = ops.token_logprobs_bwd(x, t, lp, g)
+    dn = ops.token_logprobs_bwd(x, t, lp, g, dlogits=x)
+    torch.cuda.synchronize()
+    assert torch.equal(lp.logprob, near.logprob) and torch.equal(lp.top_ids, near.top_ids)
+    assert torch.equal(dx, dn)
+
+
+def test_graph_replay_and_other_stream(ops):
+    for N, V, top in ((1, 32000, 5), (64, 33000, 20), (2000, 500, 0)):
+        x = logits_of(N, V, V, BF, 31)
+        t = torch.randint(0, V, (N,), device="cuda")
+        g = torch.randn(N, device="cuda")
+        want = ops.token_logprobs(x, t, top=top)
+        dwant = ops.token_logprobs_bwd(x, t, want, g)
+        out = ops.TokenLogprobs.empty(N, top)
+        ws = ops.logprobs_workspace(x, top)
+        dx = torch.empty_like(x)
+
+        def step(stream=None):
+            ops.token_logprobs(x, t, top=top, out=out, ws=ws, stream=stream)
+            ops.token_logprobs_bwd(x, t, out, g, dlogits=dx, stream=stream)
+
+        def same():
+            torch.cuda.synchronize()
+            return (torch.equal(out.logprob, want.logprob) and torch.equal(dx, dwant)
+                    and torch.equal(out.entropy, want.entropy)
+                    and (not top or torch.equal(out.top_ids, want.top_ids)))
+
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        step(s)
+        assert same()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for i in range(4):
+            for b in (out.logprob, out.entropy, dx):
+                b.fill_(7.0)
+            if ws is not None:
+                ws.fill_(255)
+            graph.replay()
+            assert same(), (N, V, i)
+            ops.token_logprobs(x, t, top=top)
+
+
+def test_refusals(ops):
+    x = torch.zeros(4, 64, dtype=BF, device="cuda")
+    t = torch.zeros(4, dtype=torch.int64, device="cuda")
+    lp = ops.token_logprobs(x, t)
+    g = torch.zeros(4, device="cuda")
+    for bad in (dict(logits=x.half()), dict(logits=x[0]), dict(logits=x.t()),
+                dict(targets=t.int()), dict(targets=t[:3]),
+                dict(logits=x[:1].expand(4, 64))):
+        with pytest.raises(ValueError):
+            ops.token_logprobs(**{**dict(logits=x, targets=t), **bad})
+        with pytest.raises(ValueError):
+            ops.token_logprobs_bwd(**{**dict(logits=x, targets=t, lp=lp, dlogprob=g), **bad})
+    with pytest.raises(ValueError):
+        ops.token_logprobs_bwd(x, t, lp, g, dlogits=torch.empty(4, 63, dtype=BF, device="cuda"))
+    with pytest.raises(ValueError):
+        ops.token_logprobs_bwd(x, t, lp, g, dlogits=torch.empty(4, 64, device="cuda"))
+    with pytest.raises(ValueError):
+        ops.token_logprobs_bwd(x, t, lp, g.double())
+    for top in (-1, 33, 65):
+        with pytest.raises(ops.QLoRAError):
+            ops.token_logprobs(x, t, top=top)
+    with pytest.raises(ops.QLoRAError):      # a view that starts off 16 bytes
+        ops.token_logprobs(x[:, 1:33], t)
