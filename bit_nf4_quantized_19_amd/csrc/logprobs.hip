@@ -6,12 +6,14 @@
 //   dx_j = g (delta - p_j) - e p_j (logp_j + entropy),  logp_j = t_j - l.
 // Differences from the maximum keep every quantity near zero where the
 // logits themselves are large. Sums are float32.
+#include <algorithm>
+
 #include "../../include/qlora_logprobs.h"
 #include "capi_util.h"
 
 namespace {
 
-constexpr int LT = 256;
+constexpr int LT = 256, LW = LT / 64;
 
 struct LpArgs {
   const void *x;
@@ -21,6 +23,10 @@ struct LpArgs {
   int top;
   float *top_lp;
   int64_t *top_ids;
+  int64_t chunk;       // logits of a row per workgroup, a multiple of 8
+  int nchunk;
+  float4 *part;        // [N][nchunk]: m, z, sum exp(t) t of a chunk (nchunk > 1)
+  uint64_t *keys;      // [N][nchunk][top]: its best, in order; 0 past its end
 };
 
 template <bool F32>
@@ -32,73 +38,329 @@ QL_DEV const void *row_of(const void *x, int64_t i, int64_t ld) {
   return (const char *)x + i * ld * (F32 ? 4 : 2);
 }
 
+// 16 bytes of a row: 4 float32 or 8 bf16. Rows start at any element, so the
+// accesses are declared with the element's alignment only (the hardware takes
+// them at any).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+template <bool F32> constexpr int lp_elems() { return F32 ? 4 : 8; }
+template <bool F32>
+QL_DEV u32x4 load16(const void *row, int64_t j) {
+  if (F32) return *(const u32x4_a4 *)((const float *)row + j);
+  return *(const u32x4_a2 *)((const uint16_t *)row + j);
+}
+template <bool F32>
+QL_DEV float elem(const u32x4 &v, int e) {
+  if (F32) return __uint_as_float(v[e]);
+  return (e & 1) ? ql::bf16hi(v[e >> 1]) : ql::bf16lo(v[e >> 1]);
+}
+
 // Order of the alternatives as one integer: value (NaN above +inf, the two
-// zeros equal) in the upper half, complement of the index in the lower.
+// zeros equal) in the upper half, complement of the index in the lower. Never
+// 0 (what is past the end) nor all ones.
 QL_DEV uint64_t order_key(float v, uint32_t j) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   const uint32_t k = v != v ? 0xff800001u : u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
   return ((uint64_t)k << 32) | (0xffffffffu - j);
 }
+QL_DEV float key_value(uint64_t key) {
+  const uint32_t k = (uint32_t)(key >> 32);
+  return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
+}
 
+QL_DEV float fast_exp(float t) { return __builtin_amdgcn_exp2f(t * 1.44269504088896340736f); }
+
+struct OpMax {
+  template <class T> QL_DEV T operator()(T a, T b) const { return a > b ? a : b; }
+  QL_DEV float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct OpAdd {
+  QL_DEV float operator()(float a, float b) const { return a + b; }
+};
 template <class T, class Op>
 QL_DEV T block_reduce(T v, T *tmp, Op op) {
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = op(v, __shfl_xor(v, d));
+  for (int d = 32; d >= 1; d >>= 1) v = op(v, (T)__shfl_xor(v, d));
   __syncthreads();
   if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
   __syncthreads();
   v = tmp[0];
 #pragma unroll
-  for (int w = 1; w < LT / 64; ++w) v = op(v, tmp[w]);
+  for (int w = 1; w < LW; ++w) v = op(v, tmp[w]);
   return v;
 }
 
-// One workgroup per row: a pass for the maximum, one for the sums, one per
-// alternative.
+// The row's results from its sums (one thread).
 template <bool F32>
-__global__ __launch_bounds__(LT) void logprobs_kernel(LpArgs g) {
-  __shared__ float tf[LT / 64];
-  __shared__ uint64_t tk[LT / 64];
-  const int64_t i = blockIdx.x;
-  const void *row = row_of<F32>(g.x, i, g.ld);
-  const int tid = threadIdx.x;
-  float m = -INFINITY;
-  for (int64_t j = tid; j < g.V; j += LT) m = fmaxf(m, load1<F32>(row, j));
-  m = block_reduce(m, tf, [](float a, float b) { return fmaxf(a, b); });
-  const float mm = m == -INFINITY ? 0.0f : m;
-  float z = 0.0f, s = 0.0f;
-  for (int64_t j = tid; j < g.V; j += LT) {
-    const float t = load1<F32>(row, j) - mm;
-    const float e = expf(t);
-    z += e;
-    s += e * fmaxf(t, -1e30f);
+QL_DEV void finish_row(const LpArgs &g, int64_t i, const void *row, float m, float l, float z,
+                       float s, bool empty) {
+  const int64_t t = g.targets[i];
+  float lp = 0.0f;
+  if (t >= 0 && t < g.V)
+    lp = empty ? -INFINITY : (load1<F32>(row, t) - m) - l;
+  g.logprob[i] = lp;
+  g.stats[2 * i] = m;
+  g.stats[2 * i + 1] = l;
+  if (g.entropy) g.entropy[i] = empty ? 0.0f : l - s / z;
+}
+QL_DEV void put_top(const LpArgs &g, int64_t i, int q, uint64_t key, float m, float l,
+                    bool empty) {
+  g.top_ids[i * g.top + q] = (int64_t)(0xffffffffu - (uint32_t)key);
+  g.top_lp[i * g.top + q] = empty ? -INFINITY : (key_value(key) - m) - l;
+}
+
+// The `top` largest of `count` distinct keys in LDS, by counting the larger
+// ones of each; emit(q, key) in order.
+template <class Emit>
+QL_DEV void emit_ranked(const uint64_t *list, int count, int top, Emit emit) {
+  for (int c = threadIdx.x; c < count; c += LT) {
+    const uint64_t k = list[c];
+    int rank = 0;
+    for (int o = 0; o < count; ++o) rank += list[o] > k ? 1 : 0;
+    if (rank < top) emit(rank, k);
   }
-  z = block_reduce(z, tf, [](float a, float b) { return a + b; });
-  s = block_reduce(s, tf, [](float a, float b) { return a + b; });
-  const bool empty = z == 0.0f;          // every logit -inf
+}
+
+constexpr int LP_LIST = 1024;   // candidates of a chunk held in LDS
+constexpr int LP_GROUPS = 64;   // groups of threads whose maxima give the threshold
+
+// A workgroup holds one chunk of a row (the whole row where it fits) in
+// registers, R 16-byte pieces a thread, all loaded before the first is used:
+// the row is read once from memory, its exact maximum is known before the
+// first exponential (one per logit, none to rescale), and the alternatives
+// are found in the same registers. Chunks of a split row leave (m, z, s) and
+// their best for logprobs_join_kernel.
+//
+// Alternatives: the top-th largest of 64 disjoint groups' maxima is a lower
+// bound of the top-th largest logit (that many groups hold one at least as
+// large), so only logits that reach it are listed, typically little more than
+// top of them, and ranked among themselves. Keys of value and index are
+// distinct, so ties need no further rule. A chunk with NaN or +inf, or one
+// whose list would overflow (its largest logits crowded into few threads),
+// takes one workgroup maximum per alternative instead.
+template <bool F32, int R, bool TOP>
+__global__ __launch_bounds__(LT) void logprobs_kernel(LpArgs g) {
+  constexpr int E = lp_elems<F32>();
+  constexpr uint32_t FILL = F32 ? 0xff800000u : 0xff80ff80u;   // -inf
+  __shared__ float tf[LW];
+  __shared__ uint64_t tk[LW];
+  const int tid = threadIdx.x;
+  const int64_t i = blockIdx.x / (uint32_t)g.nchunk;
+  const int c = (int)(blockIdx.x % (uint32_t)g.nchunk);
+  const void *row = row_of<F32>(g.x, i, g.ld);
+  const int64_t j0 = c * g.chunk;
+  const int len = (int)min(g.chunk, g.V - j0);
+  const int nvec = len / E, rem = len % E;   // rem: the row's end only
+  u32x4 x[R];
+  if (nvec) {
+    // pieces past the end re-read the last one (no branch around a load)
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = load16<F32>(row, j0 + E * min(r * LT + tid, nvec - 1));
+  }
+  float xt = load1<F32>(row, j0 + min(nvec * E + tid, len - 1));
+  xt = tid < rem ? xt : -INFINITY;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if ((r + 1) * LT > nvec) {   // uniform
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[r][q] = r * LT + tid < nvec ? x[r][q] : FILL;
+    }
+  float tm = xt;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      tm = fmaxf(tm, fmaxf(elem<F32>(x[r], e), elem<F32>(x[r], e + 1)));
+  const float m = block_reduce(tm, tf, OpMax());
+  const float mm = m == -INFINITY ? 0.0f : m;
+  // each pass unpacks the pieces again: kept unpacked they would fill the registers
+  auto repack = [&]() {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w = x[r][q];
+        asm("" : "+v"(w));
+        x[r][q] = w;
+      }
+  };
+  repack();
+  float z = 0.0f, s = 0.0f;
+  auto add = [&](float v) {
+    const float t = v - mm, e = fast_exp(t);
+    z += e;
+    s = fmaf(e, fmaxf(t, -1000.0f), s);   // e is 0 below that; keeps 0 * -inf out of s
+  };
+  add(xt);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (r * LT < nvec) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) add(elem<F32>(x[r], e));
+    }
+  }
+  z = block_reduce(z, tf, OpAdd());
+  s = block_reduce(s, tf, OpAdd());
+  const bool whole = g.nchunk == 1;
+  const bool empty = z == 0.0f;              // every logit -inf
   const float l = empty ? 0.0f : logf(z);
   if (tid == 0) {
-    const int64_t t = g.targets[i];
-    float lp = 0.0f;
-    if (t >= 0 && t < g.V) lp = empty ? -INFINITY : (load1<F32>(row, t) - mm) - l;
-    g.logprob[i] = lp;
-    g.stats[2 * i] = m;
-    g.stats[2 * i + 1] = l;
-    if (g.entropy) g.entropy[i] = empty ? 0.0f : l - s / z;
+    if (whole)
+      finish_row<F32>(g, i, row, m, l, z, s, empty);
+    else
+      g.part[i * g.nchunk + c] = make_float4(m, z, s, 0.0f);
+  }
+  if (!TOP) return;
+
+  __shared__ uint64_t list[LP_LIST];
+  __shared__ uint64_t grp[LP_GROUPS];
+  __shared__ int count;
+  const int top = g.top;
+  uint64_t *keys = whole ? nullptr : g.keys + (i * g.nchunk + c) * top;
+  auto emit = [&](int q, uint64_t key) {
+    if (whole)
+      put_top(g, i, q, key, m, l, empty);
+    else
+      keys[q] = key;
+  };
+  const uint32_t jt = (uint32_t)(j0 + nvec * E + tid);
+  uint32_t jb = (uint32_t)(j0 + E * tid);   // index of the thread's first logit
+  auto index = [&](int r, int e) { return jb + (uint32_t)(E * LT * r + e); };
+  bool plain = z == z;
+  repack();
+  if (plain) {   // uniform
+    // first index of the thread's maximum; what is past the end comes last
+    uint32_t at = tid < rem && xt == tm ? jt : 0xffffffffu;
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r)
+#pragma unroll
+      for (int e = E - 1; e >= 0; --e)
+        if (elem<F32>(x[r], e) == tm && r * LT + tid < nvec) at = index(r, e);
+    const uint64_t mine = at == 0xffffffffu ? 0 : order_key(tm, at);
+    uint64_t gm = mine;
+#pragma unroll
+    for (int d = 1; d < LT / LP_GROUPS; d <<= 1) gm = OpMax()(gm, (uint64_t)__shfl_xor(gm, d));
+    if (tid % (LT / LP_GROUPS) == 0) grp[tid / (LT / LP_GROUPS)] = gm;
+    if (tid == 0) count = 0;
+    __syncthreads();
+    // every wave ranks the 64 maxima, one per lane; empty groups are all last
+    const uint64_t own = grp[tid & 63];
+    int rank = 0;
+#pragma unroll 16
+    for (int o = 0; o < LP_GROUPS; ++o) rank += grp[o] > own ? 1 : 0;
+    const uint64_t hit = __ballot(rank == top - 1 && own != 0);
+    const uint64_t floor_key = hit ? __shfl(own, __builtin_ctzll(hit)) : 1;
+    repack();
+    asm("" : "+v"(jb));   // indices are formed where they are used, too
+    if (mine >= floor_key) {
+      auto offer = [&](float v, uint32_t j) {
+        const uint64_t k = order_key(v, j);
+        if (k < floor_key) return;
+        const int at2 = atomicAdd(&count, 1);
+        if (at2 < LP_LIST) list[at2] = k;
+      };
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r * LT + tid < nvec) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) offer(elem<F32>(x[r], e), index(r, e));
+        }
+      if (tid < rem) offer(xt, jt);
+    }
+    __syncthreads();
+    plain = count <= LP_LIST;
+    if (plain) {
+      emit_ranked(list, count, top, emit);
+      for (int q = count + tid; q < top; q += LT) emit(q, 0);   // a chunk of fewer logits
+    }
+  }
+  if (!plain) {
+    uint64_t last = ~0ull;
+    for (int q = 0; q < top; ++q) {
+      uint64_t best = 0;
+      repack();
+      asm("" : "+v"(jb));
+      auto offer = [&](float v, uint32_t j) {
+        const uint64_t k = order_key(v, j);
+        if (k < last && k > best) best = k;
+      };
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r * LT + tid < nvec) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) offer(elem<F32>(x[r], e), index(r, e));
+        }
+      if (tid < rem) offer(xt, jt);
+      last = block_reduce(best, tk, OpMax());
+      if (tid == 0) emit(q, last);
+    }
+  }
+}
+
+// Joins the chunks of a row: sums rescaled to the row's maximum, in a fixed
+// order; of the chunks' ordered lists, those keys that reach the smallest
+// ceil(top / nchunk)-th entry (at least top keys do) are ranked as above.
+template <bool F32>
+__global__ __launch_bounds__(LT) void logprobs_join_kernel(LpArgs g) {
+  __shared__ float tf[LW];
+  __shared__ uint64_t tk[LW];
+  const int tid = threadIdx.x;
+  const int64_t i = blockIdx.x;
+  const void *row = row_of<F32>(g.x, i, g.ld);
+  const float4 *part = g.part + i * g.nchunk;
+  float m = -INFINITY;
+  for (int c = tid; c < g.nchunk; c += LT) m = fmaxf(m, part[c].x);
+  m = block_reduce(m, tf, OpMax());
+  float z = 0.0f, s = 0.0f;
+  for (int c = tid; c < g.nchunk; c += LT) {
+    const float4 p = part[c];
+    if (p.y == 0.0f) continue;                     // nothing but -inf
+    const float t = p.x == -INFINITY ? 0.0f : p.x - m;   // -inf: a chunk of -inf and NaN
+    const float e = expf(t);
+    z += e * p.y;
+    s += e * (p.z + fmaxf(t, -1000.0f) * p.y);
+  }
+  z = block_reduce(z, tf, OpAdd());
+  s = block_reduce(s, tf, OpAdd());
+  const bool empty = z == 0.0f;
+  const float l = empty ? 0.0f : logf(z);
+  if (tid == 0) finish_row<F32>(g, i, row, m, l, z, s, empty);
+  const int top = g.top;
+  if (!top) return;
+
+  __shared__ uint64_t list[LP_LIST];
+  __shared__ int count;
+  const int total = g.nchunk * top;                // at most 2^16 chunks of 32
+  const uint64_t *keys = g.keys + i * total;
+  const int depth = (top + g.nchunk - 1) / g.nchunk;
+  uint64_t low = ~0ull;
+  for (int c = tid; c < g.nchunk; c += LT) low = min(low, keys[c * top + depth - 1]);
+  low = ~block_reduce(~low, tk, OpMax());
+  if (low == 0) low = 1;                           // a short last chunk: every key
+  if (tid == 0) count = 0;
+  __syncthreads();
+  for (int o = tid; o < total; o += LT) {
+    const uint64_t k = keys[o];
+    if (k < low) continue;
+    const int at = atomicAdd(&count, 1);
+    if (at < LP_LIST) list[at] = k;
+  }
+  __syncthreads();
+  if (count <= LP_LIST) {
+    emit_ranked(list, count, top,
+                [&](int q, uint64_t key) { put_top(g, i, q, key, m, l, empty); });
+    return;
   }
   uint64_t last = ~0ull;
-  for (int q = 0; q < g.top; ++q) {
+  for (int q = 0; q < top; ++q) {
     uint64_t best = 0;
-    for (int64_t j = tid; j < g.V; j += LT) {
-      const uint64_t k = order_key(load1<F32>(row, j), (uint32_t)j);
+    for (int o = tid; o < total; o += LT) {
+      const uint64_t k = keys[o];
       if (k < last && k > best) best = k;
     }
-    last = block_reduce(best, tk, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-    if (tid == 0) {
-      const int64_t j = 0xffffffffu - (uint32_t)last;
-      g.top_ids[i * g.top + q] = j;
-      g.top_lp[i * g.top + q] = empty ? -INFINITY : (load1<F32>(row, j) - mm) - l;
-    }
+    last = block_reduce(best, tk, OpMax());
+    if (tid == 0) put_top(g, i, q, last, m, l, empty);
   }
 }
 
@@ -108,31 +370,84 @@ struct LpGradArgs {
   const int64_t *targets;
   const float *stats, *entropy, *dlp, *dent;
   void *dx;
+  int nchunk;
 };
 
 template <bool F32>
+QL_DEV void store16(void *row, int64_t j, const u32x4 &v) {
+  if (F32)
+    *(u32x4_a4 *)((float *)row + j) = v;
+  else
+    *(u32x4_a2 *)((uint16_t *)row + j) = v;
+}
+template <bool F32>
+QL_DEV void store1(void *row, int64_t j, float v) {
+  if (F32)
+    ((float *)row)[j] = v;
+  else
+    ((uint16_t *)row)[j] = ql::f_to_bf16(v);
+}
+
+constexpr int LG_R = 4;   // pieces a thread of the gradient kernel holds
+
+// One read and one write of each logit; the time is that of the bytes. A
+// thread loads its pieces before it writes any, and owns what it writes, so
+// the gradient may replace the logits. The target's element is written once
+// more by the thread that owns it (stores of a thread to one address keep
+// their order), which keeps a comparison out of every other element.
+template <bool F32, bool ENT>
 __global__ __launch_bounds__(LT) void logprobs_grad_kernel(LpGradArgs g) {
-  const int64_t i = blockIdx.x;
+  constexpr int E = lp_elems<F32>();
+  const int tid = threadIdx.x;
+  const int64_t i = blockIdx.x / (uint32_t)g.nchunk;
+  const int c = (int)(blockIdx.x % (uint32_t)g.nchunk);
   const void *row = row_of<F32>(g.x, i, g.ld);
-  char *out = (char *)g.dx + i * g.ldo * (F32 ? 4 : 2);
+  void *out = (void *)row_of<F32>(g.dx, i, g.ldo);
+  const int64_t j0 = (int64_t)c * (LT * E * LG_R);
+  const int len = (int)min<int64_t>(LT * E * LG_R, g.V - j0);
+  const int nvec = len / E, rem = len % E;
   const int64_t t = g.targets[i];
   const float gl = (t >= 0 && t < g.V) ? g.dlp[i] : 0.0f;
-  const float ge = g.dent ? g.dent[i] : 0.0f;
-  const float ent = g.dent ? g.entropy[i] : 0.0f;
+  const float ge = ENT ? g.dent[i] : 0.0f;
+  const float ent = ENT ? g.entropy[i] : 0.0f;
   const float m = g.stats[2 * i], l = g.stats[2 * i + 1];
-  const bool zero = (gl == 0.0f && ge == 0.0f) || (m == -INFINITY && l == 0.0f);
-  for (int64_t j = threadIdx.x; j < g.V; j += LT) {
-    float d = 0.0f;
-    if (!zero) {
-      const float lp = (load1<F32>(row, j) - m) - l;
-      const float p = expf(lp);
-      d = -p * (gl + ge * (fmaxf(lp, -1e30f) + ent)) + (j == t ? gl : 0.0f);
-    }
-    if (F32)
-      ((float *)out)[j] = d;
-    else
-      ((uint16_t *)out)[j] = ql::f_to_bf16(d);
+  if ((gl == 0.0f && ge == 0.0f) || (m == -INFINITY && l == 0.0f)) {
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int r = 0; r < LG_R; ++r)
+      if (r * LT + tid < nvec) store16<F32>(out, j0 + E * (r * LT + tid), zero);
+    if (tid < rem) store1<F32>(out, j0 + nvec * E + tid, 0.0f);
+    return;
   }
+  u32x4 x[LG_R];
+  if (nvec) {
+#pragma unroll
+    for (int r = 0; r < LG_R; ++r) x[r] = load16<F32>(row, j0 + E * min(r * LT + tid, nvec - 1));
+  }
+  const float xt = load1<F32>(row, j0 + min(nvec * E + tid, len - 1));   // used if tid < rem
+  const int64_t tl = t - j0;   // the target's place in the chunk, if it has one
+  const bool owner = gl != 0.0f && tl >= 0 && tl < len &&
+                     tid == (tl < nvec * E ? (int)(tl / E) % LT : (int)tl - nvec * E);
+  const float xo = load1<F32>(row, owner ? t : j0);
+  auto grad = [&](float v) {   // without the target's own term
+    const float lp = (v - m) - l;
+    const float p = fast_exp(lp);
+    return ENT ? -p * (gl + ge * (fmaxf(lp, -1000.0f) + ent)) : -p * gl;
+  };
+#pragma unroll
+  for (int r = 0; r < LG_R; ++r) {
+    const int v = r * LT + tid;
+    if (v >= nvec) continue;
+    u32x4 o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      o[q] = F32 ? __float_as_uint(grad(elem<F32>(x[r], q)))
+                 : ql::pack_bf16x2(grad(elem<F32>(x[r], 2 * q % E)),
+                                   grad(elem<F32>(x[r], (2 * q + 1) % E)));
+    store16<F32>(out, j0 + E * v, o);
+  }
+  if (tid < rem) store1<F32>(out, j0 + nvec * E + tid, grad(xt));
+  if (owner) store1<F32>(out, t, grad(xo) + gl);
 }
 
 constexpr int64_t kMaxV = (int64_t(1) << 31) - (1 << 16);
@@ -146,6 +461,51 @@ qlora_status check_logits(const qlora_logits *x) {
   return QLORA_OK;
 }
 
+// How a row is cut: pieces per thread and workgroups per row.
+struct Split {
+  int R;
+  int64_t chunk, nchunk;
+};
+
+// The largest pieces that still give the chip two workgroups per compute
+// unit: few rows are spread, many rows are not cut where they fit.
+Split split_of(int64_t N, int64_t V, bool f32) {
+  const int64_t unit = LT * (f32 ? 4 : 8);
+  static const int kR[] = {1, 2, 4, 6, 8, 12, 16};
+  int64_t most = std::min<int64_t>(16, ql_cdiv(V, unit));
+  while (most > 1 && N * ql_cdiv(V, most * unit) < 512) most = (most + 1) / 2;
+  Split p;
+  p.nchunk = ql_cdiv(V, most * unit);
+  p.chunk = ql_rup(ql_cdiv(V, p.nchunk), 8);
+  p.nchunk = ql_cdiv(V, p.chunk);
+  p.R = 16;
+  for (int i = 6; i >= 0; --i)
+    if (kR[i] * unit >= p.chunk) p.R = kR[i];
+  return p;
+}
+
+template <bool F32, int R>
+void launch_rows(const LpArgs &g, unsigned grid, hipStream_t st) {
+  if (g.top)
+    logprobs_kernel<F32, R, true><<<grid, LT, 0, st>>>(g);
+  else
+    logprobs_kernel<F32, R, false><<<grid, LT, 0, st>>>(g);
+}
+template <bool F32>
+void launch_split(const LpArgs &g, int R, hipStream_t st) {
+  const unsigned grid = (unsigned)(g.N * g.nchunk);
+  switch (R) {
+    case 1: launch_rows<F32, 1>(g, grid, st); break;
+    case 2: launch_rows<F32, 2>(g, grid, st); break;
+    case 4: launch_rows<F32, 4>(g, grid, st); break;
+    case 6: launch_rows<F32, 6>(g, grid, st); break;
+    case 8: launch_rows<F32, 8>(g, grid, st); break;
+    case 12: launch_rows<F32, 12>(g, grid, st); break;
+    default: launch_rows<F32, 16>(g, grid, st); break;
+  }
+  if (g.nchunk > 1) logprobs_join_kernel<F32><<<(unsigned)g.N, LT, 0, st>>>(g);
+}
+
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 bool aligned8(const void *p) { return ((uintptr_t)p & 7u) == 0; }
 
@@ -157,7 +517,9 @@ size_t qlora_token_logprobs_workspace_bytes(int64_t N, int64_t V, int32_t dtype,
   if (N < 1 || V < 1 || V >= kMaxV || N > 0x7fffffff || top < 0 || top > QLORA_MAX_TOP ||
       top > V || (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_F32))
     return (size_t)-1;
-  return 0;
+  const Split p = split_of(N, V, dtype == QLORA_DTYPE_F32);
+  if (N * p.nchunk > 0x7fffffff) return (size_t)-1;
+  return p.nchunk == 1 ? 0 : (size_t)(N * p.nchunk) * (16 + 8 * (size_t)top);
 }
 
 qlora_status qlora_token_logprobs(const qlora_logits *x, const int64_t *targets, float *logprob,
@@ -172,15 +534,19 @@ qlora_status qlora_token_logprobs(const qlora_logits *x, const int64_t *targets,
   if (top && (!top_logprobs || !top_ids || !aligned4(top_logprobs) || !aligned8(top_ids)))
     return QLORA_ERR_INVALID_ARG;
   const size_t need = qlora_token_logprobs_workspace_bytes(x->N, x->V, x->dtype, top);
+  if (need == (size_t)-1) return QLORA_ERR_UNSUPPORTED;
   if (!ws_ok(ws, ws_bytes, (int64_t)need)) return QLORA_ERR_WORKSPACE;
+  const Split p = split_of(x->N, x->V, x->dtype == QLORA_DTYPE_F32);
+  float4 *part = (float4 *)ws;
   const LpArgs g{x->data, x->N, x->V, x->ld, targets, logprob, stats, entropy, top, top_logprobs,
-                 top_ids};
+                 top_ids, p.chunk, (int)p.nchunk, part,
+                 p.nchunk > 1 ? (uint64_t *)(part + x->N * p.nchunk) : nullptr};
   hipStream_t st = (hipStream_t)stream;
   QlProf prof(QLORA_K_LOGPROBS, st);
   if (x->dtype == QLORA_DTYPE_F32)
-    logprobs_kernel<true><<<(unsigned)x->N, LT, 0, st>>>(g);
+    launch_split<true>(g, p.R, st);
   else
-    logprobs_kernel<false><<<(unsigned)x->N, LT, 0, st>>>(g);
+    launch_split<false>(g, p.R, st);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
@@ -197,14 +563,22 @@ qlora_status qlora_token_logprobs_bwd(const qlora_logits *x, const int64_t *targ
       !aligned4(dlogprob) || !aligned4(dentropy) || !aligned4(entropy))
     return QLORA_ERR_INVALID_ARG;
   if (dentropy && !entropy) return QLORA_ERR_INVALID_ARG;
-  const LpGradArgs g{x->data, x->N,    x->V,     x->ld,    dx->ld,  targets,
-                     stats,   entropy, dlogprob, dentropy, dx->data};
+  const bool f32 = x->dtype == QLORA_DTYPE_F32;
+  const int64_t nchunk = ql_cdiv(x->V, LT * LG_R * (f32 ? 4 : 8));
+  if (x->N * nchunk > 0x7fffffff) return QLORA_ERR_UNSUPPORTED;
+  const LpGradArgs g{x->data, x->N,    x->V,     x->ld,    dx->ld,   targets,
+                     stats,   entropy, dlogprob, dentropy, dx->data, (int)nchunk};
   hipStream_t st = (hipStream_t)stream;
+  const unsigned grid = (unsigned)(x->N * nchunk);
   QlProf prof(QLORA_K_LOGPROBS_GRAD, st);
-  if (x->dtype == QLORA_DTYPE_F32)
-    logprobs_grad_kernel<true><<<(unsigned)x->N, LT, 0, st>>>(g);
+  if (f32 && dentropy)
+    logprobs_grad_kernel<true, true><<<grid, LT, 0, st>>>(g);
+  else if (f32)
+    logprobs_grad_kernel<true, false><<<grid, LT, 0, st>>>(g);
+  else if (dentropy)
+    logprobs_grad_kernel<false, true><<<grid, LT, 0, st>>>(g);
   else
-    logprobs_grad_kernel<false><<<(unsigned)x->N, LT, 0, st>>>(g);
+    logprobs_grad_kernel<false, false><<<grid, LT, 0, st>>>(g);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }

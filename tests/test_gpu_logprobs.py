@@ -262,3 +262,23 @@ def test_refusals(ops):
             ops.token_logprobs(x, t, top=top)
     with pytest.raises(ops.QLoRAError):      # a view that starts off 16 bytes
         ops.token_logprobs(x[:, 1:33], t)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [32768, 131000])
+def test_alternatives_crowded_into_few_pieces(ops, V, dtype):
+    # the row's largest logits lie where few threads hold them: in half of the
+    # groups of 32 (16) consecutive logits out of every 64, one group's being
+    # the least of them; and in descending and constant runs
+    per = 32 if dtype == BF else 16
+    buf = logits_of(4, V, V, dtype, 5)
+    j = torch.arange(V, device="cuda")
+    g = (j // per) % 64
+    big = (20 + (j * 2654435761 % 4096).float() / 64).to(dtype)
+    buf[0] = torch.where(g < 31, big, torch.where(g == 31, torch.full_like(big, 10), buf[0]))
+    buf[1, : 5 * per] = torch.arange(5 * per, 0, -1, device="cuda").to(dtype)
+    buf[2] = torch.where(g < 32, torch.full_like(big, 9), buf[2])
+    buf[3, V - 40:] = 30.0
+    t = np.array([0, 1, 2, V - 1])
+    for top in (1, 20, 32):
+        check(ops, buf, V, t, top, dent=False)
