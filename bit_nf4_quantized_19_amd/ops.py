@@ -166,8 +166,8 @@ def _check(status: int, what: str):
 
 
 def _stream(stream=None) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the handle itself, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -526,13 +526,21 @@ def adamw_page_in(dev, host, stream=None):
 def _device_tensors(*named):
     """Every (tensor, name, dtype, shape) contiguous, of that type and shape,
     and on the current device (the one the stream belongs to)."""
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    dev = named[0][0].get_device()
     for t, name, dtype, shape in named:
-        if not t.is_cuda or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                or t.get_device() != dev or dev < 0):
             raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape "
-                             f"{tuple(shape)}")
-        if t.device.index != cur:
-            raise ValueError(f"{name} is on {t.device}, not on the current device {cur}")
+                             f"{tuple(shape)} on the device of {named[0][1]}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{named[0][1]} is on cuda:{dev}, not on the current device")
+
+
+def _same_device(t, name, named):
+    """``_device_tensors`` of named, and t on the same device."""
+    _device_tensors(*named)
+    if t.get_device() != named[0][0].get_device():
+        raise ValueError(f"{name} and {named[0][1]} must be on one device")
 
 
 def _on(stream):
@@ -559,7 +567,7 @@ class AdapterPlan:
     data: torch.Tensor
 
     def c_struct(self) -> AdapterPlanC:
-        return AdapterPlanC(self.M, self.n, 0, self.data.data_ptr(), self.data.numel())
+        return AdapterPlanC(self.M, self.n, 0, self.data.data_ptr(), self.data.nbytes)
 
 
 def adapter_plan(ids: torch.Tensor, n: int, out: AdapterPlan | None = None,
@@ -621,24 +629,26 @@ def linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch
     in ``plan``: A (n x r x k), B (n x d x r) bf16, scale (n) float32 holding
     s_a. Returns (Y, H or None); H (M x r float32) is what the backward needs."""
     r, ad = _adapter_args(w, X, A, B, scale, plan)
-    with _on(stream):
-        if Y is None:
-            Y = torch.empty(plan.M, w.d, dtype=torch.bfloat16, device=X.device)
-        if save_h and H is None:
-            H = torch.empty(plan.M, r, dtype=torch.float32, device=X.device)
-        if ws is None:
-            ws = _workspace(adapters_workspace_bytes(OP_FWD, w.d, w.k, plan.M, plan.n, r),
-                            X.device, None)[0]
-    _device_tensors((Y, "Y", torch.bfloat16, (plan.M, w.d)))
+    if Y is None or ws is None or (save_h and H is None):
+        with _on(stream):
+            if Y is None:
+                Y = torch.empty(plan.M, w.d, dtype=torch.bfloat16, device=X.device)
+            if save_h and H is None:
+                H = torch.empty(plan.M, r, dtype=torch.float32, device=X.device)
+            if ws is None:
+                ws = adapters_workspace(plan, w.d, w.k, r)
     if save_h:
-        _device_tensors((H, "H", torch.float32, (plan.M, r)))
+        _device_tensors((Y, "Y", torch.bfloat16, (plan.M, w.d)),
+                        (H, "H", torch.float32, (plan.M, r)))
+    else:
+        H = None
+        _device_tensors((Y, "Y", torch.bfloat16, (plan.M, w.d)))
     cw, cp = w.c_struct(), plan.c_struct()
     _check(lib().qlora_linear_fwd_adapters(ctypes.byref(cw), X.data_ptr(), ctypes.addressof(ad),
-                                           ctypes.addressof(cp), Y.data_ptr(),
-                                           H.data_ptr() if save_h else None, ws.data_ptr(),
-                                           ws.numel() * ws.element_size(), _stream(stream)),
+                                           ctypes.addressof(cp), Y.data_ptr(), _ptr(H),
+                                           ws.data_ptr(), ws.nbytes, _stream(stream)),
            "qlora_linear_fwd_adapters")
-    return Y, (H if save_h else None)
+    return Y, H
 
 
 def linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
@@ -657,8 +667,7 @@ def linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch
         if dB is None:
             dB = torch.empty_like(B)
         if ws is None:
-            ws = _workspace(adapters_workspace_bytes(OP_BWD, w.d, w.k, plan.M, plan.n, r),
-                            X.device, None)[0]
+            ws = adapters_workspace(plan, w.d, w.k, r, backward=True)
     _device_tensors((dY, "dY", torch.bfloat16, (plan.M, w.d)), (dA, "dA", torch.bfloat16, A.shape),
                     (dB, "dB", torch.bfloat16, B.shape))
     if need_dx:
@@ -669,9 +678,8 @@ def linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch
     _check(lib().qlora_linear_bwd_adapters(ctypes.byref(cw), X.data_ptr(), ctypes.addressof(ad),
                                            ctypes.addressof(cp), dY.data_ptr(), _ptr(H),
                                            dX.data_ptr() if need_dx else None, dA.data_ptr(),
-                                           dB.data_ptr(), ws.data_ptr(),
-                                           ws.numel() * ws.element_size(), _stream(stream)),
-           "qlora_linear_bwd_adapters")
+                                           dB.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                           _stream(stream)), "qlora_linear_bwd_adapters")
     return (dX if need_dx else None), dA, dB
 
 
@@ -706,15 +714,16 @@ class TokenLogprobs:
 
 
 def _logits(t: torch.Tensor, name: str) -> LogitsC:
-    if t.dim() != 2 or t.dtype not in _LOGITS_DTYPES or not t.is_cuda:
+    dtype = _LOGITS_DTYPES.get(t.dtype)
+    if t.dim() != 2 or dtype is None or not t.is_cuda:
         raise ValueError(f"{name} must be a two-dimensional bfloat16 or float32 CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
     N, V = t.shape
-    ld = t.stride(0) if N > 1 else max(V, t.stride(0))
-    if (V > 1 and t.stride(1) != 1) or ld < V:
+    ld, step = t.stride()
+    if N == 1:
+        ld = max(V, ld)
+    if (V > 1 and step != 1) or ld < V:
         raise ValueError(f"{name} must have rows of consecutive elements that do not overlap")
-    return LogitsC(t.data_ptr(), N, V, ld, _LOGITS_DTYPES[t.dtype], 0)
+    return LogitsC(t.data_ptr(), N, V, ld, dtype, 0)
 
 
 def logprobs_workspace(logits: torch.Tensor, top: int = 0) -> torch.Tensor | None:
@@ -736,25 +745,26 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0,
     N = c.N
     if not 0 <= top <= min(c.V, MAX_TOP):
         raise QLoRAError(QLORA_ERR_UNSUPPORTED, f"token_logprobs(top={top})")
-    with _on(stream):
-        if out is None:
-            out = TokenLogprobs.empty(N, top, logits.device)
-        if ws is None:
-            ws = logprobs_workspace(logits, top)
-    _device_tensors((targets, "targets", torch.int64, (N,)),
-                    (out.logprob, "out.logprob", torch.float32, (N,)),
-                    (out.entropy, "out.entropy", torch.float32, (N,)),
-                    (out.stats, "out.stats", torch.float32, (N, 2)))
+    if out is None or ws is None:
+        with _on(stream):
+            if out is None:
+                out = TokenLogprobs.empty(N, top, logits.device)
+            if ws is None:
+                ws = logprobs_workspace(logits, top)
+    f32 = torch.float32
+    checks = ((targets, "targets", torch.int64, (N,)), (out.logprob, "out.logprob", f32, (N,)),
+              (out.entropy, "out.entropy", f32, (N,)), (out.stats, "out.stats", f32, (N, 2)))
     if top:
-        _device_tensors((out.top_logprobs, "out.top_logprobs", torch.float32, (N, top)),
-                        (out.top_ids, "out.top_ids", torch.int64, (N, top)))
+        checks += ((out.top_logprobs, "out.top_logprobs", f32, (N, top)),
+                   (out.top_ids, "out.top_ids", torch.int64, (N, top)))
+    _same_device(logits, "logits", checks)
     _check(lib().qlora_token_logprobs(ctypes.addressof(c), targets.data_ptr(),
                                       out.logprob.data_ptr(), out.stats.data_ptr(),
                                       out.entropy.data_ptr(), top,
-                                      _ptr(out.top_logprobs) if top else None,
-                                      _ptr(out.top_ids) if top else None, _ptr(ws),
-                                      0 if ws is None else ws.numel() * ws.element_size(),
-                                      _stream(stream)), "qlora_token_logprobs")
+                                      out.top_logprobs.data_ptr() if top else None,
+                                      out.top_ids.data_ptr() if top else None, _ptr(ws),
+                                      0 if ws is None else ws.nbytes, _stream(stream)),
+           "qlora_token_logprobs")
     return out
 
 
@@ -772,12 +782,15 @@ def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lp: TokenLog
     co = _logits(dlogits, "dlogits")
     if (co.N, co.V, co.dtype) != (N, c.V, c.dtype):
         raise ValueError("dlogits must have the shape and type of logits")
-    _device_tensors((targets, "targets", torch.int64, (N,)),
-                    (lp.stats, "lp.stats", torch.float32, (N, 2)),
-                    (lp.entropy, "lp.entropy", torch.float32, (N,)),
-                    (dlogprob, "dlogprob", torch.float32, (N,)))
+    checks = ((targets, "targets", torch.int64, (N,)),
+              (lp.stats, "lp.stats", torch.float32, (N, 2)),
+              (lp.entropy, "lp.entropy", torch.float32, (N,)),
+              (dlogprob, "dlogprob", torch.float32, (N,)))
     if dentropy is not None:
-        _device_tensors((dentropy, "dentropy", torch.float32, (N,)))
+        checks += ((dentropy, "dentropy", torch.float32, (N,)),)
+    _same_device(logits, "logits", checks)
+    if dlogits.get_device() != logits.get_device():
+        raise ValueError("dlogits must be on the device of logits")
     _check(lib().qlora_token_logprobs_bwd(ctypes.addressof(c), targets.data_ptr(),
                                           lp.stats.data_ptr(), lp.entropy.data_ptr(),
                                           dlogprob.data_ptr(), _ptr(dentropy),
