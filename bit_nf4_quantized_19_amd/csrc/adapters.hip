@@ -26,7 +26,7 @@ constexpr int PB = QLORA_MAX_ADAPTERS + 1;   // buckets: adapters, then none
 
 struct PlanArgs {
   const int32_t *ids;
-  int64_t M, split_tok;
+  int64_t M, split_tok, max_groups;
   int n;
   int *tok, *perm, *sid, *off, *num, *grp, *split;
 };
@@ -137,10 +137,10 @@ __global__ __launch_bounds__(PT) void adapter_plan_kernel(PlanArgs g) {
   }
   if (tid == 0) {
     s_off[nb] = g.off[nb] = (int)g.M;
-    g.num[0] = tot[1];
-    g.num[1] = tot[2];
-    g.num[2] = g.num[3] = 0;
+    g.num[0] = tot[2];
+    g.num[1] = g.num[2] = g.num[3] = 0;
   }
+  for (int64_t i = tot[1] + tid; i < g.max_groups; i += PT) g.grp[AD_GRP * i + 2] = 0;
   __syncthreads();
 
   for (int64_t m0 = lo; m0 < hi; m0 += 64) {
@@ -155,10 +155,12 @@ __global__ __launch_bounds__(PT) void adapter_plan_kernel(PlanArgs g) {
     g.perm[p] = (int)(m0 + lane);
     g.sid[p] = b < n ? b : -1;
     const int q = p - s_off[b], end = s_off[b + 1];
+    int *e = g.grp + AD_GRP * (int64_t)(s_grp[b] + q / AD_TOK);
+    e[4 + q % AD_TOK] = (int)(m0 + lane);
     if (q % AD_TOK == 0) {
-      int *e = g.grp + 2 * (int64_t)(s_grp[b] + q / AD_TOK);
       e[0] = b;
       e[1] = p;
+      e[2] = min(AD_TOK, end - p);
     }
     if (b < n && q % (int)g.split_tok == 0) {
       const int i = q / (int)g.split_tok;
@@ -196,13 +198,13 @@ AdapterPlan::AdapterPlan(void *data, int64_t M_, int n_) : M(M_), n(n_) {
   sid = take(M);
   off = take(n + 2);
   num = take(4);
-  grp = take(2 * max_groups);
+  grp = take(AD_GRP * max_groups);
   split = take(8 * max_splits);
   bytes = (size_t)at * 4;
 }
 
 qlora_status launch_adapter_plan(const int32_t *ids, const AdapterPlan &p, hipStream_t st) {
-  PlanArgs g{ids, p.M, p.split_tok, p.n, p.tok, p.perm, p.sid, p.off, p.num, p.grp, p.split};
+  PlanArgs g{ids, p.M, p.split_tok, p.max_groups, p.n, p.tok, p.perm, p.sid, p.off, p.num, p.grp, p.split};
   QlProf prof(QLORA_K_ADAPTER_PLAN, st);
   adapter_plan_kernel<<<1, PT, 0, st>>>(g);
   QL_LAUNCH_CHECK();

@@ -94,6 +94,8 @@ template <int S> QL_DEV uint4 *sC() { return S == 0 ? s_C0 : S == 1 ? s_C1 : s_C
 template <int S> QL_DEV uint32_t *sQ() { return S == 0 ? s_Q0 : S == 1 ? s_Q1 : s_Q2; }
 template <int S> QL_DEV float *sS() { return S == 0 ? s_S0 : S == 1 ? s_S1 : s_S2; }
 
+typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
+
 QL_DEV int swz(int row, int chunk) { return row * 8 + (chunk ^ ((row ^ (row >> 2)) & 7)); }
 
 QL_DEV uint32_t lds_addr(const void *p) {
@@ -145,7 +147,9 @@ QL_DEV float scale_of(uint32_t qd, float s2, int64_t blk, float mu) {
 // codes (waves 0-3) or scale words (waves 4-7).
 constexpr int kLoadsPerStep = 5;
 
-template <int MODE, bool DQ, bool AD>
+// AD: 0 one adapter; else many, taking 16 |AD| ranks at a time,
+// the matrices' rows (forward) being whole 16-byte pieces (AD > 0) or not
+template <int MODE, bool DQ, int AD>
 struct Tile {
   GemmArgs g;
   int tid, lane, wave, r32, h, wn, wm;
@@ -173,7 +177,7 @@ struct Tile {
   // the rank-r epilogue's operands of rank chunk 0 (L rows of the forward's
   // whole-piece path, and the S hi/lo parts), loaded before the last K-steps
   uint4 pre_a[2], pre_b[2][2];
-  int ad0, pre_id[2];   // AD: adapter of the wave's first row; of this lane's two rows
+  int pre_id[4];   // AD: adapters of rows lane, 64 + lane, ... of the tile
 
   // tile (tm, tn): token rows tm*BM.., output columns tn*BN..
   QL_DEV void init(const GemmArgs &ga, int64_t tm, int64_t tn) {
@@ -241,11 +245,6 @@ struct Tile {
         const uint32_t rb = (uint32_t)((4 * h2 + 2 + bsel + rot) & 7) * 32u;
         roff[h2] = ra | (ra << 8) | (rb << 16) | (rb << 24);
       }
-    }
-    if (AD) {
-      const int64_t p0 = m0 + 64 * wm;
-      ad0 = __builtin_amdgcn_readfirstlane(g.sid[p0 < g.M ? p0 : g.M - 1]);
-      if (ad0 < 0) ad0 = 0;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -328,6 +327,7 @@ struct Tile {
   // 4 rows (8 bytes). Neighbouring lanes take the two halves of one 16-byte
   // fragment slot, so the 8-byte writes of 16 lanes fall on 16 distinct
   // slots (the row permutation alone gives 8).
+  static constexpr int NC = AD < 0 ? -AD : AD;   // rank chunks of the many-adapter epilogue
   static constexpr int kParts = MODE == 0 ? 2 : 4;
   struct DecIn {
     uint32_t c[4];   // forward: 2 code words; dX: the table-address bytes ev[0..1], od[0..1]
@@ -522,7 +522,7 @@ struct Tile {
   // block goes to an accumulator of its own and is added where the input
   // element was kept, times 1/(1-p): dX = dY W' + s (G A) * keep / (1 - p).
   QL_DEV void epilogue() {
-    if (MODE == 1 && g.keep) {
+    if (MODE == 1 && !AD && g.keep) {
       // keep bits of the lane's two token rows: byte (n - bc) / 4 of the
       // wave's 64-column block bc (bit n % 4), one 16-byte load per row,
       // issued before the rank-r products (Ntot % 64 == 0, so a block is
@@ -541,47 +541,200 @@ struct Tile {
       keep_block<1, 0>(kw);
       keep_block<1, 1>(kw);
     } else {
-      if (AD)
+      if constexpr (AD != 0)
         adapter_terms();
       else
-        lora_term<0, 2, 0, 2>(acc, g.L, true);
+        lora_term<0, 2, 0, 2>(acc);
     }
     store();
   }
 
-  // Many adapters: rows are ordered by adapter, so a wave's 64 rows hold a
-  // few runs. For each adapter present, the rank-r term with that adapter's
-  // matrix is added to a copy of the accumulators, and each lane keeps the
-  // copy where its row (one per 32 x 32 block: column l % 32 of D) belongs to
-  // the adapter. Selecting results, rather than zeroing the other rows'
-  // operands, keeps an infinity or NaN in one adapter's matrix out of the
-  // others' rows.
+  // Many adapters: rows are ordered by adapter, so the tile's 256 rows are a
+  // sequence of runs. The part of each run's matrix that the tile's 128
+  // columns need is 256 r bytes in both modes (forward: 128 whole rows of
+  // B_a, one contiguous block; dX: 256 bytes of each of A_a's r rows) and
+  // comes by LDS DMA into the In stages, which are free by now, half of them
+  // while the runs in the other half are computed: the matrices of many
+  // adapters do not stay in L2, and a tile of many adapters would otherwise
+  // wait for memory once a run and rank chunk. The wave takes its two blocks
+  // of 32 rows in turn, with 16 NC ranks of the block's S in registers.
+  // A run's term is added to a copy of the accumulators, and each lane keeps
+  // the copy where its row (column l % 32 of a block of D) lies in the run.
+  // Selecting results, rather than zeroing the other rows' operands, keeps an
+  // infinity or NaN in one adapter's matrix out of the others' rows.
   QL_DEV void adapter_terms() {
-    int id[2];
-    uint64_t pend[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t m = m0 + wm * 64 + 32 * j + r32;
-      id[j] = m < g.M ? pre_id[j] : -1;
-      pend[j] = __ballot(id[j] >= 0);
+    // opaque, or the selects among them below become indexed reads of a scratch copy
+    int id0 = pre_id[0], id1 = pre_id[1], id2 = pre_id[2], id3 = pre_id[3];
+    asm("" : "+v"(id0), "+v"(id1), "+v"(id2), "+v"(id3));
+    const int64_t left = g.M - m0;
+    int live = 0;
+    const uint64_t st0 = run_starts(id0, -1, left, live);
+    const uint64_t st1 = run_starts(id1, __builtin_amdgcn_readlane(id0, 63), left - 64, live);
+    const uint64_t st2 = run_starts(id2, __builtin_amdgcn_readlane(id1, 63), left - 128, live);
+    const uint64_t st3 = run_starts(id3, __builtin_amdgcn_readlane(id2, 63), left - 192, live);
+    if (live == 0) return;
+    const auto next = [=](int p) { return next_start(p, st0, st1, st2, st3, live); };
+    const int blk = 256 * ((g.r + 3) & ~3);     // bytes of a run's block
+    const int per = (BM * 128) / blk;           // blocks of a stage
+    const int half = 3 * per / 2;               // runs in flight together
+    const uint32_t x0 = lds_addr(s_X0), x1 = lds_addr(s_X1), x2 = lds_addr(s_X2);
+    // runs from row p on, `half` of them at most, into the blocks from slot on
+    const auto fetch = [=](int p, int slot) {
+      for (int n = 0; n < half && p < live; ++n, p = next(p + 1)) {
+        const int ad = __builtin_amdgcn_readlane(p < 64 ? id0 : p < 128 ? id1 : p < 192 ? id2 : id3,
+                                                 p & 63);
+        fetch_run(g.L + (int64_t)ad * g.r * g.Ntot, run_block(slot + n, per, blk, x0, x1, x2));
+      }
+      return p;
+    };
+    int row = 0, slot = 0;
+    int ahead = fetch(0, 0);
+#pragma clang loop unroll(disable)
+    while (row < live) {
+      __builtin_amdgcn_s_waitcnt(0);
+      block_sync();   // this batch has landed; the other half's readers are done
+      const int end = ahead;
+      ahead = fetch(end, half - slot);
+      batch_runs<0>(row, end, slot, per, blk, x0, x1, x2, next);
+      batch_runs<1>(row, end, slot, per, blk, x0, x1, x2, next);
+      row = end;
+      slot = half - slot;
     }
-    while (pend[0] | pend[1]) {
-      const int a = pend[0] ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(pend[0]))
-                            : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(pend[1]));
+  }
+
+  // The runs of rows row .. end - 1, in the blocks from slot on, for the wave's
+  // row block J.
+  template <int J, class Next>
+  QL_DEV void batch_runs(int row, int end, int slot, int per, int blk, uint32_t x0, uint32_t x1,
+                         uint32_t x2, const Next &next) {
+    const int first = 64 * wm + 32 * J;
+    if (row >= first + 32 || end <= first) return;
+    int rr = r32, hh = h;   // opaque: the addresses below are not formed before the last K-steps
+    asm volatile("" : "+v"(rr), "+v"(hh));
+#pragma clang loop unroll(disable)
+    for (int t0 = 0; t0 < g.rp; t0 += 16 * NC) {
+      // hi and lo of S of this lane's row, ranks t0 .. t0 + 16 NC - 1 (chunks
+      // past rp re-read the last one, and meet a zero)
+      uint4 b[NC][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) pend[j] &= ~__ballot(id[j] == a);
-      f32x16 t[2][2];
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int part = 0; part < 2; ++part) {
+          const int64_t m = m0 + first + rr;
+          const int t = t0 + 16 * c < g.rp ? t0 + 16 * c : g.rp - 16;
+          b[c][part] = *(const uint4 *)((part ? g.Slo : g.Shi) +
+                                        (m < g.M ? m : g.M - 1) * g.rp + t + 8 * hh);
+        }
+      int q0 = row;
+#pragma clang loop unroll(disable)
+      for (int n = 0; q0 < end; ++n) {
+        const int q1 = next(q0 + 1);
+        if (q1 > first && q0 < first + 32)
+          adapter_run<J>(run_block(slot + n, per, blk, x0, x1, x2), t0, b, q0, q1, rr, hh);
+        q0 = q1;
+      }
+    }
+  }
+
+  // Forward blocks with a power of two of 16-byte pieces a row: the pieces of
+  // a row are permuted so that equal pieces of neighbouring rows lie in
+  // different banks (rows of 32 bytes need none).
+  QL_DEV int piece_swz(int row) const {
+    const int np = g.r >> 3;
+    if (MODE != 0 || AD < 0 || (np & (np - 1)) || np < 4) return 0;
+    return (np == 4 ? row >> 1 : row) & (np - 1);
+  }
+
+  // LDS DMA of one run's block, shared by the eight waves.
+  QL_DEV void fetch_run(const uint16_t *L, uint32_t base) const {
+    for (int i = wave; 4 * i < g.r; i += 8) {
+      const int c = 64 * i + lane;              // 16-byte piece of the block
+      int64_t e;
+      if (MODE == 0) {
+        int src = c;
+        if (AD > 0) {
+          const int np = g.r >> 3, row = c / np;
+          src = row * np + ((c - row * np) ^ piece_swz(row));
+        }
+        e = n0 * g.r + 8 * src;
+        const int64_t last = g.Ntot * g.r - 8;
+        e = e < last ? e : last;                // columns past Ntot: not stored
+      } else {
+        const int t = c >> 4 < g.r ? c >> 4 : g.r - 1;
+        const int64_t n = n0 + 8 * (c & 15);
+        e = t * g.Ntot + (n < g.Ntot ? n : g.Ntot - 8);
+      }
+      dma16(L + e, __builtin_amdgcn_readfirstlane(base + 1024 * i));
+    }
+  }
+
+  // Lanes whose row starts a run, given the previous 64 rows' last adapter and
+  // the rows left in the batch; adds the rows with an adapter to live.
+  QL_DEV uint64_t run_starts(int id, int before, int64_t left, int &live) const {
+    int prev = __shfl_up(id, 1);
+    if (lane == 0) prev = before;
+    const bool on = lane < left && id >= 0;
+    live += __popcll(__ballot(on));
+    return __ballot(on && id != prev);
+  }
+  // LDS address of a run's block: per blocks of blk bytes in each stage.
+  static QL_DEV uint32_t run_block(int slot, int per, int blk, uint32_t x0, uint32_t x1,
+                                   uint32_t x2) {
+    const int st = slot / per;   // 0, 1 or 2
+    return x0 + (st > 0) * (x1 - x0) + (st > 1) * (x2 - x1) + (uint32_t)((slot - st * per) * blk);
+  }
+  // First start at or after row p (live: none).
+  static QL_DEV int next_start(int p, uint64_t a, uint64_t b, uint64_t c, uint64_t d, int live) {
+    const int w = p >> 6, k = p & 63;
+    if (w == 0) a &= ~0ull << k;
+    if (w == 1) b &= ~0ull << k;
+    if (w == 2) c &= ~0ull << k;
+    if (w == 3) d &= ~0ull << k;
+    if (w < 1 && a) return __builtin_ctzll(a);
+    if (w < 2 && b) return 64 + __builtin_ctzll(b);
+    if (w < 3 && c) return 128 + __builtin_ctzll(c);
+    if (w < 4 && d) return 192 + __builtin_ctzll(d);
+    return live;
+  }
+
+  // Ranks t0 .. t0 + 16 NC - 1 of the run of rows q0 .. q1 - 1 for row block J, the
+  // run's matrix at LDS address base, S in b; rr and hh: the lane's r32 and h.
+  template <int J>
+  QL_DEV void adapter_run(uint32_t base, int t0, const uint4 (&b)[NC][2], int q0, int q1, int rr,
+                          int hh) {
+    typedef const __attribute__((address_space(3))) uint16_t lds16;
+    typedef const __attribute__((address_space(3))) u32v4 lds128;
+    const int row = 64 * wm + 32 * J + rr;
+    const bool mine = row >= q0 && row < q1;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) t[i][j] = acc[i][j];
-      lora_term<0, 2, 0, 2>(t, g.L + (int64_t)a * g.r * g.Ntot, a == ad0);
+    for (int i = 0; i < 2; ++i) {
+      const int nl = wn * 64 + 32 * i + rr;
+      f32x16 v = acc[i][J];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int c = 0; c < NC; ++c) {
+        const int t = t0 + 16 * c + 8 * hh;
+        uint4 a;
+        if (MODE == 0 && AD > 0) {
+          const int pc = (t < g.r ? t >> 3 : 0) ^ piece_swz(nl);
+          const u32v4 w = *(lds128 *)(uintptr_t)(base + 2 * nl * g.r + 16 * pc);
+          a = t < g.r ? make_uint4(w[0], w[1], w[2], w[3]) : ql::zero4();
+        } else {
+          uint32_t e[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+          for (int x = 0; x < 8; ++x) {
+            const int tc = t + x < g.r ? t + x : g.r - 1;
+            e[x] = *(lds16 *)(uintptr_t)(base +
+                                         (MODE == 0 ? 2 * (nl * g.r + tc) : 256 * tc + 2 * nl));
+            e[x] = t + x < g.r ? e[x] : 0u;
+          }
+          a = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
+                         e[6] | (e[7] << 16));
+        }
+        v = ql::mfma32(a, b[c][0], v);
+        v = ql::mfma32(a, b[c][1], v);
+      }
 #pragma unroll
-          for (int q = 0; q < 16; ++q) acc[i][j][q] = id[j] == a ? t[i][j][q] : acc[i][j][q];
+      for (int q = 0; q < 16; ++q) acc[i][J][q] = mine ? v[q] : acc[i][J][q];
     }
   }
 
@@ -592,7 +745,7 @@ struct Tile {
     f32x16 lacc[1][1];
 #pragma unroll
     for (int q = 0; q < 16; ++q) lacc[0][0][q] = 0.0f;
-    lora_term<I, 1, J, 1>(lacc, g.L, true);
+    lora_term<I, 1, J, 1>(lacc);
     const uint32_t w4[4] = {kw[J].x, kw[J].y, kw[J].z, kw[J].w};
 #pragma unroll
     for (int q4 = 0; q4 < 4; ++q4) {
@@ -607,25 +760,24 @@ struct Tile {
   // Unconditional loads from clamped addresses (their latency then runs
   // under the last K-steps); out-of-range lanes are zeroed where used.
   QL_DEV void lora_prefetch() {
-    if (MODE == 0 && g.r % 8 == 0) {
+    if (!AD && MODE == 0 && g.r % 8 == 0) {
       const int tq = 8 * h < g.r ? 8 * h : g.r - 8;
-      const uint16_t *L = AD ? g.L + (int64_t)ad0 * g.r * g.Ntot : g.L;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int64_t n = n0 + wn * 64 + 32 * i + r32;
         const int64_t nc = n < g.Ntot ? n : g.Ntot - 1;
-        pre_a[i] = *(const uint4 *)(L + nc * g.r + tq);
+        pre_a[i] = *(const uint4 *)(g.L + nc * g.r + tq);
       }
     }
     if (AD) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t m = m0 + wm * 64 + 32 * j + r32;
-        pre_id[j] = g.sid[m < g.M ? m : g.M - 1];
+      for (int q = 0; q < 4; ++q) {
+        const int64_t m = m0 + 64 * q + lane;
+        pre_id[q] = g.sid[m < g.M ? m : g.M - 1];
       }
     }
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
+    for (int part = 0; !AD && part < 2; ++part) {
       const uint16_t *S = part ? g.Slo : g.Shi;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -636,10 +788,9 @@ struct Tile {
     }
   }
 
-  // the rank-r term of the 32 x 32 blocks (I0 .., J0 ..), NI x NJ of them,
-  // with L rows from `L` (pre: pre_a holds its first rank chunk)
+  // the rank-r term of the 32 x 32 blocks (I0 .., J0 ..), NI x NJ of them
   template <int I0, int NI, int J0, int NJ>
-  QL_DEV void lora_term(f32x16 (&dst)[NI][NJ], const uint16_t *L, bool pre) {
+  QL_DEV void lora_term(f32x16 (&dst)[NI][NJ]) {
     for (int t0 = 0; t0 < g.rp; t0 += 16) {
       // L[n][t0 + 8h .. +7] read in place (ranks past r and n past Ntot: 0);
       // loads from clamped addresses, the zeroing applied afterwards
@@ -651,9 +802,8 @@ struct Tile {
         for (int ii = 0; ii < NI; ++ii) {
           const int64_t n = n0 + wn * 64 + 32 * (I0 + ii) + r32;
           const int64_t nc = n < g.Ntot ? n : g.Ntot - 1;
-          const uint4 v = (t0 == 0 && pre)
-                              ? pre_a[I0 + ii]
-                              : *(const uint4 *)(L + nc * g.r + (tq < g.r ? tq : g.r - 8));
+          const uint4 v = t0 == 0 ? pre_a[I0 + ii]
+                                  : *(const uint4 *)(g.L + nc * g.r + (tq < g.r ? tq : g.r - 8));
           a[ii] = (n < g.Ntot && tq < g.r) ? v : ql::zero4();
         }
       } else {
@@ -666,7 +816,7 @@ struct Tile {
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             const int t = t0 + 8 * h + x, tc = t < g.r ? t : g.r - 1;
-            e[ii][x] = L[MODE == 0 ? nc * g.r + tc : (int64_t)tc * g.Ntot + nc];
+            e[ii][x] = g.L[MODE == 0 ? nc * g.r + tc : (int64_t)tc * g.Ntot + nc];
           }
         }
 #pragma unroll
@@ -735,7 +885,7 @@ QL_DEV void tile_of(int64_t ntn, int64_t ntm, int64_t &tm, int64_t &tn) {
   tn = tile % ntn;
 }
 
-template <int MODE, bool DQ, bool AD>
+template <int MODE, bool DQ, int AD>
 __global__ __launch_bounds__(NT, 1) void nf4_gemm_kernel(GemmArgs g) {
   if (threadIdx.x < 16) s_lv[threadIdx.x] = __uint_as_float(c_levels_g[threadIdx.x]);
   int64_t tm, tn;
@@ -753,16 +903,20 @@ static qlora_status launch_gemm(int mode, GemmArgs g, hipStream_t st) {
   const int64_t tiles = ql_cdiv(g.Ntot, BN) * ql_cdiv(g.M, BM);
   QlProf prof(mode == 0 ? QLORA_K_GEMM_FWD : QLORA_K_GEMM_DX, st);
   const unsigned grid = (unsigned)tiles;
-#define QL_GEMM(MODEV, DQV)                                        \
-  if (g.perm)                                                      \
-    nf4_gemm_kernel<MODEV, DQV, true><<<grid, NT, 0, st>>>(g);     \
-  else                                                             \
-    nf4_gemm_kernel<MODEV, DQV, false><<<grid, NT, 0, st>>>(g);
-  if (mode == 0) {
-    if (g.sc.dq) { QL_GEMM(0, true) } else { QL_GEMM(0, false) }
-  } else {
-    if (g.sc.dq) { QL_GEMM(1, true) } else { QL_GEMM(1, false) }
+#define QL_GEMM(MODEV, DQV, ADV) nf4_gemm_kernel<MODEV, DQV, ADV><<<grid, NT, 0, st>>>(g);
+#define QL_GEMM_AD(MODEV, DQV)                                                          \
+  if (!g.perm) { QL_GEMM(MODEV, DQV, 0) }                                               \
+  else if (MODEV == 1 || g.r % 8 == 0) {                                                \
+    if (g.rp == 16) { QL_GEMM(MODEV, DQV, 1) } else { QL_GEMM(MODEV, DQV, 4) }          \
+  } else {                                                                              \
+    if (g.rp == 16) { QL_GEMM(0, DQV, -1) } else { QL_GEMM(0, DQV, -2) }                \
   }
+  if (mode == 0) {
+    if (g.sc.dq) { QL_GEMM_AD(0, true) } else { QL_GEMM_AD(0, false) }
+  } else {
+    if (g.sc.dq) { QL_GEMM_AD(1, true) } else { QL_GEMM_AD(1, false) }
+  }
+#undef QL_GEMM_AD
 #undef QL_GEMM
   QL_LAUNCH_CHECK();
   return QLORA_OK;

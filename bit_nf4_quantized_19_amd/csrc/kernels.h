@@ -46,12 +46,14 @@ qlora_status launch_dequantize(const uint8_t *codes, ql::ScaleSrc sc, int64_t n,
 //   perm  [M]     token at position p: by adapter, none last, batch order inside
 //   sid   [M]     adapter of position p (-1: none)
 //   off   [n+2]   first position of adapter a; off[n]: of none; off[n+1] = M
-//   num   [4]     groups, splits
-//   grp   [2 g]   (adapter or n for none, first position): up to AD_TOK positions
+//   num   [4]     splits
+//   grp   [16 g]  (adapter or n for none, first position, tokens, 0, the tokens):
+//                 up to AD_TOK positions; records past the last group have 0 tokens
 //   split [8 s]   (adapter, lo, hi, first slot or -1, index, count, 0, 0): positions
 //                 lo .. hi of one adapter; an adapter with one split has no slot
 // Every adapter has at least one split (an empty one when it has no token).
 constexpr int AD_TOK = 8;          // tokens of a group
+constexpr int AD_GRP = 16;         // ints of a group's record: one load for all a workgroup needs
 constexpr int AD_SPLITS = 6;       // splits of a batch that one adapter fills
 struct AdapterPlan {
   int64_t M = 0;

@@ -93,8 +93,8 @@ struct SkinnyArgs {
   float s;
   int *zero;        // counters a later launch of the same call needs zeroed (or NULL)
   int64_t nzero;
-  // many adapters: the plan's groups, token order and per-adapter scales
-  const int *perm, *off, *num, *grp;
+  // many adapters: the plan's groups and per-adapter scales
+  const int *grp;
   const float *scale;
   int n;
 };
@@ -107,37 +107,57 @@ QL_DEV T pick4s(int i, T a0, T a1, T a2, T a3) {
 constexpr int SK_TOK = 8;   // tokens per workgroup (of the 16 MFMA rows)
 static_assert(SK_TOK == AD_TOK, "a plan's group is one workgroup's tokens");
 
-// B[row][t .. t + 7] of a C x r matrix as 16 bytes, ranks past r as zeros: one
-// load when rows are whole 16-byte pieces, else element by element.
-QL_DEV uint4 rank_piece(const uint16_t *row, int t, int r) {
-  if (t >= r) return ql::zero4();
-  if ((r & 7) == 0) return *(const uint4 *)(row + t);
-  uint32_t e[8];
+// B[row][t .. t + 7] of a C x r matrix as 16 bytes, ranks past r as zeros.
+// W8: r % 8 == 0, rows of whole aligned pieces. Otherwise the piece is read
+// where it starts, at any element, and may run into the next row, whose part
+// is masked off; a piece that would pass the end of the matrix is read up to
+// that end and shifted.
+typedef uint32_t sk_u32x4 __attribute__((ext_vector_type(4)));
+typedef sk_u32x4 sk_u32x4_a2 __attribute__((aligned(2)));
+template <bool W8>
+QL_DEV uint4 rank_piece(const uint16_t *P, int64_t row, int t, int r, int64_t total) {
+  if (W8) {
+    const uint4 v = *(const uint4 *)(P + row * r + min(t, r - 8));
+    return t < r ? v : ql::zero4();
+  }
+  const int64_t off = row * r + t, safe = min(off, total - 8);
+  sk_u32x4 v = *(const sk_u32x4_a2 *)(P + safe);
+  if (off != safe) {   // the matrix's last rows
+    const int sh = (int)min<int64_t>(off - safe, 8);
+    uint32_t e[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = row[t + i < r ? t + i : r - 1];
+    for (int i = 0; i < 8; ++i)
+      e[i] = i + sh < 8 ? P[safe + i + sh] : 0u;
+    v = sk_u32x4{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
+                 e[6] | (e[7] << 16)};
+  }
+  const int left = r - t;   // ranks of the piece that exist
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = t + i < r ? e[i] : 0u;
-  return make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
-                    e[6] | (e[7] << 16));
+  for (int q = 0; q < 4; ++q)
+    w[q] = v[q] & ((2 * q < left ? 0x0000ffffu : 0u) | (2 * q + 1 < left ? 0xffff0000u : 0u));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // AD (many adapters): workgroup x takes group x of the plan, up to SK_TOK
 // tokens of one adapter, whose matrix is at Pm + adapter * r * C; hi and lo go
 // to plan positions, out and out2 to tokens. Tokens without an adapter get
 // zeros and read nothing.
-template <bool PCOL, bool AD>
+template <bool PCOL, bool AD, bool W8>
 __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
   if (a.zero && blockIdx.x == 0 && blockIdx.y == 0)
     for (int64_t i = threadIdx.x; i < a.nzero; i += 64 * SK_W) a.zero[i] = 0;
   int ad = 0, ntok = SK_TOK;   // AD: adapter and token count of the group
   int64_t pos0 = 0;            // AD: its first plan position
   bool none = false;
+  const int *gr = nullptr;
   if (AD) {
-    if ((int)blockIdx.x >= a.num[0]) return;
-    ad = min(a.grp[2 * blockIdx.x], a.n);
-    pos0 = a.grp[2 * blockIdx.x + 1];
-    ntok = (int)min<int64_t>(SK_TOK, min<int64_t>(a.off[ad + 1], a.M) - pos0);
+    gr = a.grp + AD_GRP * (int64_t)blockIdx.x;
+    ad = min(gr[0], a.n);
+    pos0 = gr[1];
+    ntok = min(gr[2], SK_TOK);
     none = ad == a.n;
+    if (ntok <= 0) return;   // past the last group
   }
   const int wi = (int)blockIdx.y / a.tbw;   // uniform: fields picked by selects
   const uint16_t *__restrict__ In = a.In;
@@ -171,7 +191,7 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
   bool m_ok = r16 < SK_TOK && m < M;   // MFMA rows past SK_TOK stay zero
   if (AD) {
     m_ok = r16 < ntok;
-    m = m_ok ? min<int64_t>((uint32_t)a.perm[pos0 + r16], M - 1) : 0;
+    m = min<int64_t>((uint32_t)gr[4 + (m_ok ? r16 : 0)], M - 1);
   }
   const uint16_t *inr = In + (m_ok ? m : 0) * C + 8 * kq;
   const int64_t c_lo = wave * cpw, c_hi = none ? c_lo : min(C, c_lo + cpw);
@@ -207,7 +227,7 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
       if (PCOL) {
         const int64_t row = cc + 8 * kq + rho;   // B row, t = t0 + 8 hf .. +7
         if (row < c_hi)
-          b[u] = AD ? rank_piece(Pm + row * r, t0 + 8 * hf, r)
+          b[u] = AD ? rank_piece<W8>(Pm, row, t0 + 8 * hf, r, C * r)
                     : *(const uint4 *)(Pm + row * r + t0 + 8 * hf);
       }
     }
@@ -261,7 +281,7 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
     if (AD) {
       if (4 * kq + i >= ntok) continue;
       hl = pos0 + 4 * kq + i;
-      mm = min<int64_t>((uint32_t)a.perm[hl], M - 1);
+      mm = min<int64_t>((uint32_t)gr[4 + 4 * kq + i], M - 1);
     } else if (4 * kq + i >= SK_TOK || mm >= M) {
       continue;
     }
@@ -476,7 +496,7 @@ __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p
   uint16_t *out = P.out;
   float scale = P.scale;
   if (AD) {
-    if (split >= ad.num[1]) return;
+    if (split >= ad.num[0]) return;
     const int *e = ad.split + 8 * split;
     const int a = min(e[0], ad.n - 1);
     m_lo = e[1];
@@ -673,9 +693,9 @@ qlora_status launch_skinny(const uint16_t *In, int64_t M, int64_t C, int nw, con
   dim3 grid((unsigned)mbs, (unsigned)(nw * a.tbw));
   QlProf prof(QLORA_K_LORA_DOWN, st);
   if (p_col)
-    skinny_kernel<true, false><<<grid, 64 * SK_W, 0, st>>>(a);
+    skinny_kernel<true, false, true><<<grid, 64 * SK_W, 0, st>>>(a);
   else
-    skinny_kernel<false, false><<<grid, 64 * SK_W, 0, st>>>(a);
+    skinny_kernel<false, false, true><<<grid, 64 * SK_W, 0, st>>>(a);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
@@ -697,18 +717,17 @@ qlora_status launch_skinny_adapters(const uint16_t *In, int64_t C, const uint16_
   a.out2_ld = r;
   a.zero = zero;
   a.nzero = nzero;
-  a.perm = plan.perm;
-  a.off = plan.off;
-  a.num = plan.num;
   a.grp = plan.grp;
   a.scale = scale;
   a.n = plan.n;
   dim3 grid((unsigned)plan.max_groups, (unsigned)a.tbw);
   QlProf prof(QLORA_K_LORA_DOWN, st);
-  if (p_col)
-    skinny_kernel<true, true><<<grid, 64 * SK_W, 0, st>>>(a);
+  if (!p_col)
+    skinny_kernel<false, true, true><<<grid, 64 * SK_W, 0, st>>>(a);
+  else if (r % 8 == 0)
+    skinny_kernel<true, true, true><<<grid, 64 * SK_W, 0, st>>>(a);
   else
-    skinny_kernel<false, true><<<grid, 64 * SK_W, 0, st>>>(a);
+    skinny_kernel<true, true, false><<<grid, 64 * SK_W, 0, st>>>(a);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
