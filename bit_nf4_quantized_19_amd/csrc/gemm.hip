@@ -891,6 +891,9 @@ __global__ __launch_bounds__(NT, 1) void nf4_gemm_kernel(GemmArgs g) {
   int64_t tm, tn;
   tile_of(ql_cdiv(g.Ntot, BN), ql_cdiv(g.M, BM), tm, tn);
   Tile<MODE, DQ, AD> t;
+  // many adapters: the column tiles' second half takes the token blocks in
+  // reverse, so that an XCD with a token block of many runs gets one of few
+  if (AD && 2 * tn >= ql_cdiv(g.Ntot, BN)) tm = ql_cdiv(g.M, BM) - 1 - tm;
   t.init(g, tm, tn);
   __syncthreads();  // level table
   t.run();

@@ -143,8 +143,12 @@ QL_DEV uint4 rank_piece(const uint16_t *P, int64_t row, int t, int r, int64_t to
 // tokens of one adapter, whose matrix is at Pm + adapter * r * C; hi and lo go
 // to plan positions, out and out2 to tokens. Tokens without an adapter get
 // zeros and read nothing.
-template <bool PCOL, bool AD, bool W8>
+// TB: blocks of 16 ranks of one workgroup, which share its reads of In. The
+// K-slices in flight are fewer with more than one, and for rows of B that are
+// not whole pieces (!W8), to stay in 128 registers.
+template <bool PCOL, bool AD, bool W8, int TB>
 __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
+  constexpr int UN = SK_UNROLL / (TB == 1 ? 1 : 2) / (W8 ? 1 : 2);
   if (a.zero && blockIdx.x == 0 && blockIdx.y == 0)
     for (int64_t i = threadIdx.x; i < a.nzero; i += 64 * SK_W) a.zero[i] = 0;
   int ad = 0, ntok = SK_TOK;   // AD: adapter and token count of the group
@@ -159,7 +163,7 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
     none = ad == a.n;
     if (ntok <= 0) return;   // past the last group
   }
-  const int wi = (int)blockIdx.y / a.tbw;   // uniform: fields picked by selects
+  const int wi = AD ? 0 : (int)blockIdx.y / a.tbw;   // uniform: fields picked by selects
   const uint16_t *__restrict__ In = a.In;
   const uint16_t *__restrict__ Pm = QL_SKPICK(P) + (AD && !none ? (int64_t)ad * a.r * a.C : 0);
   float *__restrict__ out = QL_SKPICK(out);
@@ -178,7 +182,7 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
   dp.mask_write = QL_SKPICK(dp.mask_write);
   dp.mask = QL_SKPICK(dp.mask);
   constexpr int PQ = 272;   // bytes per lane group in the transposition slot (256 + pad)
-  __shared__ f32x4 red[SK_W][64];
+  __shared__ f32x4 red[TB][SK_W][64];
   // per-wave slot for re-laying out the P pieces of one K-slice: B's raw
   // pieces (PCOL) or A's 16 rows of 64 bytes at a stride of 80 (!PCOL)
   constexpr int AST = 80;
@@ -186,7 +190,7 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, kq = lane >> 4;
   const int64_t mb = blockIdx.x;
-  const int t0 = 16 * ((int)blockIdx.y % a.tbw);
+  const int t0 = AD ? 16 * TB * (int)blockIdx.y : 16 * ((int)blockIdx.y % a.tbw);
   int64_t m = mb * SK_TOK + r16;
   bool m_ok = r16 < SK_TOK && m < M;   // MFMA rows past SK_TOK stay zero
   if (AD) {
@@ -199,22 +203,32 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
   // pa = lane % 4 of the slice's 64 bytes, so a quarter-wave reads 4 rows of
   // 64 contiguous bytes) and re-laid out through the slot; rows past r read 0
   const int ra = lane >> 2, pa = lane & 3;
-  const bool ta_ok = t0 + ra < r;
-  const uint16_t *prow = Pm + (ta_ok ? t0 + ra : 0) * C + 8 * pa;           // !PCOL
+  bool ta_ok[TB];
+  const uint16_t *prow[TB];                                                 // !PCOL
+#pragma unroll
+  for (int b = 0; b < TB; ++b) {
+    ta_ok[b] = t0 + 16 * b + ra < r;
+    prow[b] = Pm + (ta_ok[b] ? t0 + 16 * b + ra : 0) * C + 8 * pa;
+  }
   const int rho = (lane >> 1) & 7, hf = lane & 1;                           // PCOL raw piece
   unsigned char *slot = pst[wave];
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t c = c_lo; c < c_hi; c += 32 * SK_UNROLL) {
-    uint4 a[SK_UNROLL], b[SK_UNROLL];
+  f32x4 acc[TB];
 #pragma unroll
-    for (int u = 0; u < SK_UNROLL; ++u) {
+  for (int tb = 0; tb < TB; ++tb) acc[tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int64_t c = c_lo; c < c_hi; c += 32 * UN) {
+    uint4 a[UN], b[TB][UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
       const int64_t cc = c + 32 * u;
       a[u] = ql::zero4();
-      b[u] = ql::zero4();
       if (cc + 8 * kq < c_hi) {   // c_hi % 8 == 0: a chunk is all in or all out
         if (m_ok) a[u] = *(const uint4 *)(inr + cc);
       }
-      if (!PCOL && ta_ok && cc + 8 * pa < c_hi) b[u] = *(const uint4 *)(prow + cc);
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) {
+        b[tb][u] = ql::zero4();
+        if (!PCOL && ta_ok[tb] && cc + 8 * pa < c_hi) b[tb][u] = *(const uint4 *)(prow[tb] + cc);
+      }
       if (dp.on) {   // dropped elements of X (token m, columns cc + 8kq ..) read as 0
         const uint64_t e = (uint64_t)(m_ok ? m : 0) * (uint64_t)C + (uint64_t)(cc + 8 * kq);
         const uint32_t k8 = keep4(dp, e) | (keep4(dp, e + 4) << 4);
@@ -225,55 +239,65 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
           *(uint16_t *)(dp.mask + (e >> 2)) = (uint16_t)((k8 & 15u) | ((k8 >> 4) << 8));
       }
       if (PCOL) {
-        const int64_t row = cc + 8 * kq + rho;   // B row, t = t0 + 8 hf .. +7
-        if (row < c_hi)
-          b[u] = AD ? rank_piece<W8>(Pm, row, t0 + 8 * hf, r, C * r)
-                    : *(const uint4 *)(Pm + row * r + t0 + 8 * hf);
+        const int64_t row = cc + 8 * kq + rho;   // B row, t = t0 + 16 tb + 8 hf .. +7
+        if (row < c_hi) {
+#pragma unroll
+          for (int tb = 0; tb < TB; ++tb)
+            b[tb][u] = AD ? rank_piece<W8>(Pm, row, t0 + 16 * tb + 8 * hf, r, C * r)
+                          : *(const uint4 *)(Pm + row * r + t0 + 16 * tb + 8 * hf);
+        }
       }
     }
     if (!PCOL) {
       // lane (t = r16, kq) needs A[t][cc + 8kq .. +7]: row ra's piece pa in,
       // row r16's piece kq out
 #pragma unroll
-      for (int u = 0; u < SK_UNROLL; ++u) {
-        *(uint4 *)(slot + ra * AST + pa * 16) = b[u];
-        b[u] = *(const uint4 *)(slot + r16 * AST + kq * 16);
-      }
+      for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          *(uint4 *)(slot + ra * AST + pa * 16) = b[tb][u];
+          b[tb][u] = *(const uint4 *)(slot + r16 * AST + kq * 16);
+        }
     }
     if (PCOL) {
       // lane (t = r16, kq) needs B rows cc + 8kq .. +7 of column t: write the
       // raw pieces (group kq, row rho, half hf) and read them back by column
 #pragma unroll
-      for (int u = 0; u < SK_UNROLL; ++u) {
-        *(uint4 *)(slot + kq * PQ + rho * 32 + hf * 16) = b[u];
-        uint32_t w[4];
+      for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t e0 = *(const uint16_t *)(slot + kq * PQ + (2 * q) * 32 + 2 * r16);
-          const uint32_t e1 = *(const uint16_t *)(slot + kq * PQ + (2 * q + 1) * 32 + 2 * r16);
-          w[q] = e0 | (e1 << 16);
+        for (int u = 0; u < UN; ++u) {
+          *(uint4 *)(slot + kq * PQ + rho * 32 + hf * 16) = b[tb][u];
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t e0 = *(const uint16_t *)(slot + kq * PQ + (2 * q) * 32 + 2 * r16);
+            const uint32_t e1 = *(const uint16_t *)(slot + kq * PQ + (2 * q + 1) * 32 + 2 * r16);
+            w[q] = e0 | (e1 << 16);
+          }
+          b[tb][u] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        b[u] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
     }
 #pragma unroll
-    for (int u = 0; u < SK_UNROLL; ++u) acc = ql::mfma16(a[u], b[u], acc);
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) acc[tb] = ql::mfma16(a[u], b[tb][u], acc[tb]);
   }
   // lane holds D[4kq + i][r16] = out[token 4kq+i of the block][t0 + r16]
-  red[wave][lane] = acc;
+#pragma unroll
+  for (int tb = 0; tb < TB; ++tb) red[tb][wave][lane] = acc[tb];
   __syncthreads();
-  if (wave != 0) return;
+  if (wave >= TB || t0 + 16 * wave >= rp) return;   // wave tb finishes rank block tb
   // all the waves' partials read first (one LDS latency), then added in wave order
   f32x4 x[SK_W];
 #pragma unroll
-  for (int w = 0; w < SK_W; ++w) x[w] = red[w][lane];
+  for (int w = 0; w < SK_W; ++w) x[w] = red[TB == 1 ? 0 : wave][w][lane];
   __builtin_amdgcn_sched_barrier(0);
   f32x4 v = x[0];
 #pragma unroll
   for (int w = 1; w < SK_W; ++w)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += x[w][i];
-  const int t = t0 + r16;
+  const int t = t0 + 16 * wave + r16;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     int64_t mm = mb * SK_TOK + 4 * kq + i;
@@ -350,15 +374,30 @@ struct CmRegs {
 
 // Rows at or past M (here: the end of this workgroup's token range) read as 0.
 // AD: rows are plan positions of tokens perm[m].
+// A thread's tokens of a chunk (AD), read one chunk ahead of the rows they name.
+template <int RPM, int KS>
+struct CmTok {
+  int x[KS];
+  int q[RPM * KS / 32 > 0 ? RPM * KS / 32 : 1];
+};
+template <int RPM, int KS>
+QL_DEV void cm_tokens(CmTok<RPM, KS> &T, const int *perm, int64_t M, int rp, int64_t m0, int tid) {
+#pragma unroll
+  for (int j = 0; j < KS; ++j) T.x[j] = perm[min(m0 + 32 * j + (tid >> 3), M - 1)];
+#pragma unroll
+  for (int u = 0; u < (RPM * KS + 31) / 32; ++u)
+    T.q[u] = perm[min(m0 + (tid + 256 * u) / (rp / 4), M - 1)];
+}
+
 template <bool MK, int RPM, int KS, bool AD>
 QL_DEV void cm_load(CmRegs<RPM, KS> &R, const ColaccProb &P, int64_t M, int rp, int64_t m0, int64_t c0,
-                    int tid, const ColaccAd &ad) {
+                    int tid, const ColaccAd &ad, const CmTok<RPM, KS> &T) {
 #pragma unroll
   for (int j = 0; j < KS; ++j) {
     int64_t m = m0 + 32 * j + (tid >> 3);
     const int64_t c = c0 + 8 * (tid & 7);
     const bool ok = m < M && c < P.C;   // C % 8 == 0: the 8 columns are all in or all out
-    if (AD && ok) m = min<int64_t>((uint32_t)ad.perm[m], ad.M - 1);
+    if (AD) m = min<int64_t>((uint32_t)T.x[j], ad.M - 1);
     R.x[j] = ok ? *(const uint4 *)(P.In + m * P.C + c) : ql::zero4();
     if (P.dp.on && ok) {
       const uint64_t e = (uint64_t)m * (uint64_t)P.C + (uint64_t)c;
@@ -383,7 +422,7 @@ QL_DEV void cm_load(CmRegs<RPM, KS> &R, const ColaccProb &P, int64_t M, int rp, 
       const int t = 4 * (f % (rp / 4));
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (mq < M && t < P.ldq) {
-        const float *q = P.Q + min<int64_t>((uint32_t)ad.perm[mq], ad.M - 1) * P.ldq + t;
+        const float *q = P.Q + min<int64_t>((uint32_t)T.q[u], ad.M - 1) * P.ldq + t;
         if ((P.ldq & 3) == 0) {
           v = *(const float4 *)q;
         } else {
@@ -518,17 +557,25 @@ __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p
   // named at compile time: chunk ch + CM_PF - 1 is loaded while chunk ch is
   // stored to LDS and computed
   CmRegs<RPM, KS> R[CM_PF];
+  CmTok<RPM, KS> T;
+  if (AD && nch > 0) cm_tokens<RPM, KS>(T, ad.perm, m_hi, rp, m_lo, tid);
 #pragma unroll
   for (int i = 0; i < CM_PF - 1; ++i)
-    if (i < nch) cm_load<MK, RPM, KS, AD>(R[i], P, m_hi, rp, m_lo + (int64_t)i * TOK, c0, tid, ad);
+    if (i < nch) {
+      cm_load<MK, RPM, KS, AD>(R[i], P, m_hi, rp, m_lo + (int64_t)i * TOK, c0, tid, ad, T);
+      if (AD) cm_tokens<RPM, KS>(T, ad.perm, m_hi, rp, m_lo + (int64_t)(i + 1) * TOK, tid);
+    }
   for (int ch0 = 0; ch0 < nch; ch0 += CM_PF) {
 #pragma unroll
     for (int u = 0; u < CM_PF; ++u) {
       const int ch = ch0 + u;
       if (ch >= nch) break;
-      if (ch + CM_PF - 1 < nch)
+      if (ch + CM_PF - 1 < nch) {
         cm_load<MK, RPM, KS, AD>(R[(u + CM_PF - 1) % CM_PF], P, m_hi, rp,
-                                 m_lo + (int64_t)(ch + CM_PF - 1) * TOK, c0, tid, ad);
+                                 m_lo + (int64_t)(ch + CM_PF - 1) * TOK, c0, tid, ad, T);
+        if (AD)
+          cm_tokens<RPM, KS>(T, ad.perm, m_hi, rp, m_lo + (int64_t)(ch + CM_PF) * TOK, tid);
+      }
       uint32_t *sin = (u & 1) ? s_in1 : s_in0;
       uint16_t *sqh = (u & 1) ? s_qh1 : s_qh0, *sql = (u & 1) ? s_ql1 : s_ql0;
       cm_store<RPM, KS>(R[u], sin, sqh, sql, rp, tid);
@@ -693,9 +740,9 @@ qlora_status launch_skinny(const uint16_t *In, int64_t M, int64_t C, int nw, con
   dim3 grid((unsigned)mbs, (unsigned)(nw * a.tbw));
   QlProf prof(QLORA_K_LORA_DOWN, st);
   if (p_col)
-    skinny_kernel<true, false, true><<<grid, 64 * SK_W, 0, st>>>(a);
+    skinny_kernel<true, false, true, 1><<<grid, 64 * SK_W, 0, st>>>(a);
   else
-    skinny_kernel<false, false, true><<<grid, 64 * SK_W, 0, st>>>(a);
+    skinny_kernel<false, false, true, 1><<<grid, 64 * SK_W, 0, st>>>(a);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
@@ -720,14 +767,23 @@ qlora_status launch_skinny_adapters(const uint16_t *In, int64_t C, const uint16_
   a.grp = plan.grp;
   a.scale = scale;
   a.n = plan.n;
-  dim3 grid((unsigned)plan.max_groups, (unsigned)a.tbw);
   QlProf prof(QLORA_K_LORA_DOWN, st);
-  if (!p_col)
-    skinny_kernel<false, true, true><<<grid, 64 * SK_W, 0, st>>>(a);
-  else if (r % 8 == 0)
-    skinny_kernel<true, true, true><<<grid, 64 * SK_W, 0, st>>>(a);
-  else
-    skinny_kernel<true, true, false><<<grid, 64 * SK_W, 0, st>>>(a);
+#define QL_SKA(PC, W8V, TBV)                                                                \
+  skinny_kernel<PC, true, W8V, TBV>                                                         \
+      <<<dim3((unsigned)plan.max_groups, (unsigned)ql_cdiv(a.tbw, TBV)), 64 * SK_W, 0, st>>>(a);
+#define QL_SKT(PC, W8V)                                                                     \
+  if (a.tbw == 1) { QL_SKA(PC, W8V, 1) }                                                    \
+  else if (a.tbw == 2) { QL_SKA(PC, W8V, 2) }                                               \
+  else { QL_SKA(PC, W8V, 4) }
+  if (!p_col) {
+    QL_SKT(false, true)
+  } else if (r % 8 == 0) {
+    if (a.tbw == 1) { QL_SKA(true, true, 1) } else { QL_SKA(true, true, 2) }
+  } else {
+    if (a.tbw == 1) { QL_SKA(true, false, 1) } else { QL_SKA(true, false, 2) }
+  }
+#undef QL_SKT
+#undef QL_SKA
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
@@ -820,8 +876,14 @@ qlora_status launch_colacc2_adapters(const ColaccAdReq &a, const ColaccAdReq &b,
 #define QL_CMA(RPV, KSV)                                                                 \
   colacc_kernel<false, RPV, KSV, true><<<grid, 256, cm_lds_bytes<KSV>(rp), st>>>(        \
       p0, p1, plan.M, rp, r, 0, 1, cnt, ad);
-  if (rp <= 16) { QL_CMA(16, 4) }
+  // few tokens an adapter: chunks of 32 tokens, whose smaller LDS lets eight
+  // workgroups share a compute unit instead of three
+  const bool few = plan.M <= 48 * (int64_t)plan.n;
+  if (rp <= 16 && few) { QL_CMA(16, 1) }
+  else if (rp <= 16) { QL_CMA(16, 4) }
+  else if (rp <= 32 && few) { QL_CMA(32, 1) }
   else if (rp <= 32) { QL_CMA(32, 2) }
+  else if (rp <= 64 && few) { QL_CMA(64, 1) }
   else if (rp <= 64) { QL_CMA(64, 2) }
   else { QL_CMA(128, 1) }
 #undef QL_CMA
