@@ -398,7 +398,12 @@ QL_DEV void cm_load(CmRegs<RPM, KS> &R, const ColaccProb &P, int64_t M, int rp, 
     const int64_t c = c0 + 8 * (tid & 7);
     const bool ok = m < M && c < P.C;   // C % 8 == 0: the 8 columns are all in or all out
     if (AD) m = min<int64_t>((uint32_t)T.x[j], ad.M - 1);
-    R.x[j] = ok ? *(const uint4 *)(P.In + m * P.C + c) : ql::zero4();
+    if (AD) {
+      const uint4 v = *(const uint4 *)(P.In + m * P.C + (c < P.C ? c : 0));
+      R.x[j] = ok ? v : ql::zero4();
+    } else {
+      R.x[j] = ok ? *(const uint4 *)(P.In + m * P.C + c) : ql::zero4();
+    }
     if (P.dp.on && ok) {
       const uint64_t e = (uint64_t)m * (uint64_t)P.C + (uint64_t)c;
       uint32_t k8;
@@ -419,17 +424,21 @@ QL_DEV void cm_load(CmRegs<RPM, KS> &R, const ColaccProb &P, int64_t M, int rp, 
     if (f >= nq) break;
     const int64_t mq = m0 + f / (rp / 4);
     if (AD) {
+      // loads from clamped places, what lies past the batch or the ranks zeroed after
       const int t = 4 * (f % (rp / 4));
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (mq < M && t < P.ldq) {
-        const float *q = P.Q + min<int64_t>((uint32_t)T.q[u], ad.M - 1) * P.ldq + t;
-        if ((P.ldq & 3) == 0) {
-          v = *(const float4 *)q;
-        } else {
-          const int left = P.ldq - t;
-          v = make_float4(q[0], left > 1 ? q[1] : 0.f, left > 2 ? q[2] : 0.f, left > 3 ? q[3] : 0.f);
-        }
+      const float *q = P.Q + min<int64_t>((uint32_t)T.q[u], ad.M - 1) * P.ldq;
+      float4 v;
+      if ((P.ldq & 3) == 0) {
+        v = *(const float4 *)(q + min(t, P.ldq - 4));
+      } else {
+        const int e = P.ldq - 1;
+        v = make_float4(q[min(t, e)], q[min(t + 1, e)], q[min(t + 2, e)], q[min(t + 3, e)]);
       }
+      const int left = mq < M ? P.ldq - t : 0;
+      v.x = left > 0 ? v.x : 0.f;
+      v.y = left > 1 ? v.y : 0.f;
+      v.z = left > 2 ? v.z : 0.f;
+      v.w = left > 3 ? v.w : 0.f;
       R.q[u] = v;
       continue;
     }
@@ -544,6 +553,13 @@ __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p
     slot0 = S > 1 ? min(e[3], ad.max_slots - S) : 0;
     split = slot0 + e[4];
     out += (int64_t)a * r * P.C;
+    if (m_lo >= m_hi) {   // an adapter without tokens: its zeros, 16 bytes a store
+      const int nc = (int)min<int64_t>(CM_COLS, P.C - c0), np = nc >> 3;   // C % 8 == 0
+      for (int i = tid; i < r * np; i += 256)
+        *(uint4 *)(P.transpose_out ? out + (int64_t)(i / np) * P.C + c0 + 8 * (i % np)
+                                   : out + c0 * r + 8 * i) = ql::zero4();
+      return;
+    }
     scale = ad.scale[a];
   }
   const int tbs = rp / 16;
@@ -589,12 +605,18 @@ __global__ __launch_bounds__(256) void colacc_kernel(ColaccProb p0, ColaccProb p
 #pragma unroll
     for (int b = 0; b < RPM / 16; ++b) {
       if (b >= tbs) break;
+      const int t4 = 16 * b + 4 * g;
+      uint32_t ob[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * b + 4 * g + i;
-        if (t < r)
-          out[P.transpose_out ? (int64_t)t * P.C + cc : cc * r + t] =
-              ql::f_to_bf16(scale * acc[b][i]);
+      for (int i = 0; i < 4; ++i) ob[i] = ql::f_to_bf16(scale * acc[b][i]);
+      if (!P.transpose_out && (r & 3) == 0) {
+        if (t4 < r)
+          *(uint2 *)(out + cc * r + t4) = make_uint2(ob[0] | (ob[1] << 16), ob[2] | (ob[3] << 16));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t4 + i < r)
+            out[P.transpose_out ? (int64_t)(t4 + i) * P.C + cc : cc * r + t4 + i] = (uint16_t)ob[i];
       }
     }
     return;
