@@ -27,7 +27,7 @@ qlora_status check_adapters(const qlora_adapters *a, const qlora_adapter_plan *p
 
 struct FwdWs {
   uint16_t *hi, *lo;   // M > 16: s_a H in plan order
-  float *part;         // M <= 16: slice and H partial sums
+  float *part;         // partial sums: M <= 16 of slices and H, larger M of split tiles
   int64_t bytes;
 };
 FwdWs fwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
@@ -37,6 +37,7 @@ FwdWs fwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
   if (M > 16) {
     L.hi = c.take<uint16_t>(M * rp * 2);
     L.lo = c.take<uint16_t>(M * rp * 2);
+    L.part = c.take<float>((int64_t)gemm_adapter_part_bytes(M, d, k));
   } else {
     L.part = c.take<float>((int64_t)gemv_part_bytes(d, k, M, rp, 1));
   }
@@ -45,8 +46,10 @@ FwdWs fwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
 }
 
 struct BwdWs {
-  float *H, *G, *part;
+  float *H, *G;
+  float *part;         // partial sums of the gradients, then of dX's split tiles
   uint16_t *hi, *lo;
+  int *ctr;            // counters of the gradients
   int64_t bytes;
 };
 BwdWs bwd_layout(char *base, int64_t d, int64_t k, const AdapterPlan &plan, int r) {
@@ -57,7 +60,10 @@ BwdWs bwd_layout(char *base, int64_t d, int64_t k, const AdapterPlan &plan, int 
   L.G = c.take<float>(plan.M * rp * 4);
   L.hi = c.take<uint16_t>(plan.M * rp * 2);
   L.lo = c.take<uint16_t>(plan.M * rp * 2);
-  L.part = c.take<float>((int64_t)colacc_adapters_part_bytes(plan, d, k, rp));
+  L.ctr = c.take<int>(4 * colacc_adapters_counter_count(plan, d, k));
+  const size_t pg = colacc_adapters_part_bytes(plan, d, k, rp);
+  const size_t px = gemm_adapter_part_bytes(plan.M, k, d);
+  L.part = c.take<float>((int64_t)(pg > px ? pg : px));
   L.bytes = c.off;
   return L;
 }
@@ -113,8 +119,8 @@ qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight *w, const uint16_t
   if ((s = launch_skinny_adapters(X, k, ad->A, ad->scale, p, false, r, rp, nullptr, H_save, L.hi,
                                   L.lo, st)) != QLORA_OK)
     return s;
-  return launch_gemm_fwd(w->codes, scale_src(w), d, k, X, M, ad->B, r, L.hi, L.lo, rp, Y, st,
-                         p.perm, p.sid);
+  const GemmAdapters ga{p.perm, p.sid, L.part};
+  return launch_gemm_fwd(w->codes, scale_src(w), d, k, X, M, ad->B, r, L.hi, L.lo, rp, Y, st, &ga);
 }
 
 qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight *w, const uint16_t *X,
@@ -142,19 +148,19 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight *w, const uint16_t
     H = L.H;
   }
   // G = dY B_a, which also clears the counters of the gradient launch
-  int *cnt = colacc_adapters_counters(L.part, p, d, k, rp);
   if ((s = launch_skinny_adapters(dY, d, ad->B, ad->scale, p, true, r, rp, L.G, nullptr, L.hi,
-                                  L.lo, st, cnt, colacc_adapters_counter_count(p, d, k))) !=
+                                  L.lo, st, L.ctr, colacc_adapters_counter_count(p, d, k))) !=
       QLORA_OK)
     return s;
   // dB_a = s_a dY^T H and dA_a = s_a G^T X over each adapter's tokens
   if ((s = launch_colacc2_adapters(ColaccAdReq{dY, d, H, r, dB, 0},
                                    ColaccAdReq{X, k, L.G, rp, dA, 1}, p, rp, r, ad->scale, L.part,
-                                   st)) != QLORA_OK)
+                                   L.ctr, st)) != QLORA_OK)
     return s;
   if (!dX) return QLORA_OK;
+  const GemmAdapters ga{p.perm, p.sid, L.part};
   return launch_gemm_dx(w->codes, scale_src(w), d, k, dY, M, ad->A, r, L.hi, L.lo, rp, dX, nullptr,
-                        1.0f, st, p.perm, p.sid);
+                        1.0f, st, &ga);
 }
 
 }  // extern "C"

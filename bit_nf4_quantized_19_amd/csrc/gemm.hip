@@ -49,6 +49,8 @@
 // step, orders everything.
 // Workgroups are mapped XCD-aware: the 32 column tiles of one token block
 // land on the same XCD, whose L2 then holds that In block.
+#include <type_traits>
+
 #include "kernels.h"
 #include "nf4_tables.h"
 
@@ -74,6 +76,14 @@ struct GemmArgs {
   // sid[p] (-1: none); In and Out are addressed by token, S by p, and L holds
   // one r x Ntot (or Ntot x r) matrix per adapter
   const int *perm, *sid;
+};
+
+// Many adapters with few tiles: S workgroups (grid y) share a tile's K-steps
+// and leave their sums in part for the join kernel. Kept apart so that the
+// one-adapter kernels' arguments stay as they are.
+struct GemmArgsAd : GemmArgs {
+  int S;
+  float4 *part;   // [tile][S][16][NT]
 };
 
 // LDS, one object per stage. The level table is the most aligned object, so
@@ -179,8 +189,10 @@ struct Tile {
   uint4 pre_a[2], pre_b[2][2];
   int pre_id[4];   // AD: adapters of rows lane, 64 + lane, ... of the tile
 
+  int64_t k0, nkt;    // AD: first K of this workgroup's steps; all steps (nk: its own)
+
   // tile (tm, tn): token rows tm*BM.., output columns tn*BN..
-  QL_DEV void init(const GemmArgs &ga, int64_t tm, int64_t tn) {
+  QL_DEV void init(const GemmArgs &ga, int64_t tm, int64_t tn, int S = 1) {
     g = ga;
     tid = threadIdx.x;
     lane = tid & 63;
@@ -192,6 +204,12 @@ struct Tile {
     m0 = tm * BM;
     n0 = tn * BN;
     nk = ql_cdiv(g.Ktot, BK);
+    if (AD) {
+      nkt = nk;
+      const int64_t lo = blockIdx.y * nkt / S;
+      nk = (blockIdx.y + 1) * nkt / S - lo;
+      k0 = lo * BK;
+    }
     mu = DQ ? g.sc.mu[0] : 0.0f;
     // In DMA: wave w fetches rows 32w .. 32w+31 in 4 groups of 8 rows; lane l
     // of a group fetches the chunk that the LDS permutation puts at slot l%8
@@ -286,7 +304,7 @@ struct Tile {
   // p/4; entry e = 2r + b is row r, block column b.
   template <int ST>
   QL_DEV void issue_c(int64_t kk) {
-    if (kk >= g.Ktot) kk = (nk - 1) * BK;   // prologue past the end: any valid step
+    if (kk >= g.Ktot) kk = ((AD ? nkt : nk) - 1) * BK;   // prologue past the end: any valid step
     if (wave < 4) {
       const void *src;
       if (MODE == 0) {
@@ -429,7 +447,7 @@ struct Tile {
 
   template <int CS, int WS>
   QL_DEV void decode(int64_t t) {
-    const DecIn di = dec_load<CS>(t * BK);
+    const DecIn di = dec_load<CS>((AD ? k0 : 0) + t * BK);
 #pragma unroll
     for (int i = 0; i < kParts; ++i) dec_part<WS>(di, i);
   }
@@ -456,14 +474,14 @@ struct Tile {
     const bool do_x = !TAIL || s + 2 < nk, do_c = !TAIL || s + 3 < nk;
     const bool do_d = !TAIL || s + 1 < nk;
     DecIn di;
-    if (do_d) di = dec_load<S1>((s + 1) * BK);
+    if (do_d) di = dec_load<S1>((AD ? k0 : 0) + (s + 1) * BK);
     uint4 a[2][2], b[2][2];
     load_slice<ST>(0, a[0], b[0]);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       if (c < 3) load_slice<ST>(c + 1, a[(c + 1) & 1], b[(c + 1) & 1]);
-      if (do_x) issue_x<S2, !TAIL>((s + 2) * BK, c);
-      if (c == 3 && do_c) issue_c<ST>((s + 3) * BK);
+      if (do_x) issue_x<S2, !TAIL>((AD ? k0 : 0) + (s + 2) * BK, c);
+      if (c == 3 && do_c) issue_c<ST>((AD ? k0 : 0) + (s + 3) * BK);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -491,11 +509,11 @@ struct Tile {
     // prologue (unconditional, with clamped addresses, so the loop is entered
     // with the same loads in flight as it carries around its back edge):
     // codes 0, then In 0 + codes 1, In 1 + codes 2; decode codes 0
-    issue_c<0>(0);
-    issue_x_all<0, false>(0);
-    issue_c<1>(BK);
-    issue_x_all<1, false>(BK);
-    issue_c<2>(2 * BK);
+    issue_c<0>(AD ? k0 : 0);
+    issue_x_all<0, false>(AD ? k0 : 0);
+    issue_c<1>(AD ? k0 + BK : BK);
+    issue_x_all<1, false>(AD ? k0 + BK : BK);
+    issue_c<2>(AD ? k0 + 2 * BK : 2 * BK);
     wait_vm_le<2 * kLoadsPerStep>();   // codes 0 landed
     block_sync();
     decode<0, 0>(0);
@@ -513,6 +531,22 @@ struct Tile {
       step<0, true>(s);
       if (s + 1 < nk) step<1, true>(s + 1);
       if (s + 2 < nk) step<2, true>(s + 2);
+    }
+  }
+
+  // Split K (AD): the lane's sums to slot y of the tile's partial sums, 16
+  // bytes a store; rows past the batch are not written.
+  QL_DEV void publish(float4 *dst) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (m0 + wm * 64 + 32 * j + r32 >= g.M) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          dst[((2 * i + j) * 4 + q) * NT + tid] =
+              make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                          acc[i][j][4 * q + 3]);
     }
   }
 
@@ -542,7 +576,7 @@ struct Tile {
       keep_block<1, 1>(kw);
     } else {
       if constexpr (AD != 0)
-        adapter_terms();
+        adapter_terms(0, 1);
       else
         lora_term<0, 2, 0, 2>(acc);
     }
@@ -562,7 +596,8 @@ struct Tile {
   // the copy where its row (column l % 32 of a block of D) lies in the run.
   // Selecting results, rather than zeroing the other rows' operands, keeps an
   // infinity or NaN in one adapter's matrix out of the others' rows.
-  QL_DEV void adapter_terms() {
+  // Of a split tile, split y takes every S-th run from the y-th on.
+  QL_DEV void adapter_terms(int y, int S) {
     // opaque, or the selects among them below become indexed reads of a scratch copy
     int id0 = pre_id[0], id1 = pre_id[1], id2 = pre_id[2], id3 = pre_id[3];
     asm("" : "+v"(id0), "+v"(id1), "+v"(id2), "+v"(id3));
@@ -574,13 +609,17 @@ struct Tile {
     const uint64_t st3 = run_starts(id3, __builtin_amdgcn_readlane(id2, 63), left - 192, live);
     if (live == 0) return;
     const auto next = [=](int p) { return next_start(p, st0, st1, st2, st3, live); };
+    const auto mine = [=](int p) {   // the next run of this split
+      for (int n = 0; n < S && p < live; ++n) p = next(p + 1);
+      return p;
+    };
     const int blk = 256 * ((g.r + 3) & ~3);     // bytes of a run's block
     const int per = (BM * 128) / blk;           // blocks of a stage
     const int half = 3 * per / 2;               // runs in flight together
     const uint32_t x0 = lds_addr(s_X0), x1 = lds_addr(s_X1), x2 = lds_addr(s_X2);
     // runs from row p on, `half` of them at most, into the blocks from slot on
     const auto fetch = [=](int p, int slot) {
-      for (int n = 0; n < half && p < live; ++n, p = next(p + 1)) {
+      for (int n = 0; n < half && p < live; ++n, p = mine(p)) {
         const int ad = __builtin_amdgcn_readlane(p < 64 ? id0 : p < 128 ? id1 : p < 192 ? id2 : id3,
                                                  p & 63);
         fetch_run(g.L + (int64_t)ad * g.r * g.Ntot, run_block(slot + n, per, blk, x0, x1, x2));
@@ -588,15 +627,16 @@ struct Tile {
       return p;
     };
     int row = 0, slot = 0;
-    int ahead = fetch(0, 0);
+    for (int n = 0; n < y && row < live; ++n) row = next(row + 1);
+    int ahead = fetch(row, 0);
 #pragma clang loop unroll(disable)
     while (row < live) {
       __builtin_amdgcn_s_waitcnt(0);
       block_sync();   // this batch has landed; the other half's readers are done
       const int end = ahead;
       ahead = fetch(end, half - slot);
-      batch_runs<0>(row, end, slot, per, blk, x0, x1, x2, next);
-      batch_runs<1>(row, end, slot, per, blk, x0, x1, x2, next);
+      batch_runs<0>(row, end, slot, per, blk, x0, x1, x2, next, mine);
+      batch_runs<1>(row, end, slot, per, blk, x0, x1, x2, next, mine);
       row = end;
       slot = half - slot;
     }
@@ -604,9 +644,9 @@ struct Tile {
 
   // The runs of rows row .. end - 1, in the blocks from slot on, for the wave's
   // row block J.
-  template <int J, class Next>
+  template <int J, class Next, class Mine>
   QL_DEV void batch_runs(int row, int end, int slot, int per, int blk, uint32_t x0, uint32_t x1,
-                         uint32_t x2, const Next &next) {
+                         uint32_t x2, const Next &next, const Mine &mine) {
     const int first = 64 * wm + 32 * J;
     if (row >= first + 32 || end <= first) return;
     int rr = r32, hh = h;   // opaque: the addresses below are not formed before the last K-steps
@@ -631,7 +671,7 @@ struct Tile {
         const int q1 = next(q0 + 1);
         if (q1 > first && q0 < first + 32)
           adapter_run<J>(run_block(slot + n, per, blk, x0, x1, x2), t0, b, q0, q1, rr, hh);
-        q0 = q1;
+        q0 = mine(q0);
       }
     }
   }
@@ -886,7 +926,8 @@ QL_DEV void tile_of(int64_t ntn, int64_t ntm, int64_t &tm, int64_t &tn) {
 }
 
 template <int MODE, bool DQ, int AD>
-__global__ __launch_bounds__(NT, 1) void nf4_gemm_kernel(GemmArgs g) {
+__global__ __launch_bounds__(NT, 1) void nf4_gemm_kernel(
+    std::conditional_t<AD != 0, GemmArgsAd, GemmArgs> g) {
   if (threadIdx.x < 16) s_lv[threadIdx.x] = __uint_as_float(c_levels_g[threadIdx.x]);
   int64_t tm, tn;
   tile_of(ql_cdiv(g.Ntot, BN), ql_cdiv(g.M, BM), tm, tn);
@@ -894,25 +935,106 @@ __global__ __launch_bounds__(NT, 1) void nf4_gemm_kernel(GemmArgs g) {
   // many adapters: the column tiles' second half takes the token blocks in
   // reverse, so that an XCD with a token block of many runs gets one of few
   if (AD && 2 * tn >= ql_cdiv(g.Ntot, BN)) tm = ql_cdiv(g.M, BM) - 1 - tm;
-  t.init(g, tm, tn);
+  if constexpr (AD != 0)
+    t.init(g, tm, tn, g.S);
+  else
+    t.init(g, tm, tn);
   __syncthreads();  // level table
   t.run();
+  if constexpr (AD != 0)
+    if (g.S > 1) {   // the adapters' terms go into the splits' sums
+      t.adapter_terms(blockIdx.y, g.S);
+      t.publish(g.part + ((tm * ql_cdiv(g.Ntot, BN) + tn) * g.S + blockIdx.y) * 16 * NT);
+      return;
+    }
   t.epilogue();
+}
+
+// Split K: adds a tile's S partial sums in split order, rounds and stores
+// them; workgroup 4 tile + 2 i + j takes that 32 x 32 block of every wave's
+// eighth, all of a thread's loads in flight at once. The sums are handed over
+// by a kernel boundary because the XCDs' L2s are not coherent: with the tile's
+// last workgroup adding them inside the GEMM (agent-scope 8-byte stores) the
+// hand-over cost 25 to 40 us at 32 to 128 tiles.
+template <int S>
+__global__ __launch_bounds__(NT) void nf4_gemm_join_kernel(GemmArgsAd g) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, h = lane >> 5;
+  const int wn = wave & 1, wm = wave >> 1;
+  const int64_t tile = blockIdx.x >> 2;
+  const int i = (blockIdx.x >> 1) & 1, j = blockIdx.x & 1;
+  const int64_t tn = tile % ql_cdiv(g.Ntot, BN), tm = tile / ql_cdiv(g.Ntot, BN);
+  const int64_t p = tm * BM + wm * 64 + 32 * j + r32;
+  const int64_t n = tn * BN + wn * 64 + 32 * i + 4 * h;
+  if (p >= g.M) return;
+  const float4 *src = g.part + (tile * S * 16 + (2 * i + j) * 4) * NT + tid;
+  float4 w[S][4];
+#pragma unroll
+  for (int y = 0; y < S; ++y)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[y][q] = src[(y * 16 + q) * NT];
+  const int64_t m = min<int64_t>((uint32_t)g.perm[p], g.M - 1);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float4 v = w[0][q];
+#pragma unroll
+    for (int y = 1; y < S; ++y) {
+      v.x += w[y][q].x;
+      v.y += w[y][q].y;
+      v.z += w[y][q].z;
+      v.w += w[y][q].w;
+    }
+    if (n + 8 * q < g.Ntot)
+      *(uint2 *)(g.Out + m * g.Ntot + n + 8 * q) =
+          make_uint2(ql::pack_bf16x2(v.x, v.y), ql::pack_bf16x2(v.z, v.w));
+  }
+}
+
+static void launch_join(const GemmArgsAd &g, unsigned tiles, hipStream_t st) {
+  switch (g.S) {
+    case 2: nf4_gemm_join_kernel<2><<<4 * tiles, NT, 0, st>>>(g); break;
+    case 3: nf4_gemm_join_kernel<3><<<4 * tiles, NT, 0, st>>>(g); break;
+    case 4: nf4_gemm_join_kernel<4><<<4 * tiles, NT, 0, st>>>(g); break;
+    case 6: nf4_gemm_join_kernel<6><<<4 * tiles, NT, 0, st>>>(g); break;
+    case 8: nf4_gemm_join_kernel<8><<<4 * tiles, NT, 0, st>>>(g); break;
+    default: break;
+  }
 }
 
 }  // namespace
 
-static qlora_status launch_gemm(int mode, GemmArgs g, hipStream_t st) {
-  const int64_t tiles = ql_cdiv(g.Ntot, BN) * ql_cdiv(g.M, BM);
+static qlora_status launch_gemm(int mode, const GemmArgs &ga, const GemmAdapters *ad,
+                                hipStream_t st) {
+  const int64_t tiles = ql_cdiv(ga.Ntot, BN) * ql_cdiv(ga.M, BM);
   QlProf prof(mode == 0 ? QLORA_K_GEMM_FWD : QLORA_K_GEMM_DX, st);
   const unsigned grid = (unsigned)tiles;
-#define QL_GEMM(MODEV, DQV, ADV) nf4_gemm_kernel<MODEV, DQV, ADV><<<grid, NT, 0, st>>>(g);
-#define QL_GEMM_AD(MODEV, DQV)                                                          \
-  if (!g.perm) { QL_GEMM(MODEV, DQV, 0) }                                               \
-  else if (MODEV == 1 || g.r % 8 == 0) {                                                \
-    if (g.rp == 16) { QL_GEMM(MODEV, DQV, 1) } else { QL_GEMM(MODEV, DQV, 4) }          \
-  } else {                                                                              \
-    if (g.rp == 16) { QL_GEMM(0, DQV, -1) } else { QL_GEMM(0, DQV, -2) }                \
+  if (!ad) {
+    if (mode == 0) {
+      if (ga.sc.dq)
+        nf4_gemm_kernel<0, true, 0><<<grid, NT, 0, st>>>(ga);
+      else
+        nf4_gemm_kernel<0, false, 0><<<grid, NT, 0, st>>>(ga);
+    } else {
+      if (ga.sc.dq)
+        nf4_gemm_kernel<1, true, 0><<<grid, NT, 0, st>>>(ga);
+      else
+        nf4_gemm_kernel<1, false, 0><<<grid, NT, 0, st>>>(ga);
+    }
+    QL_LAUNCH_CHECK();
+    return QLORA_OK;
+  }
+  GemmArgsAd g;
+  (GemmArgs &)g = ga;
+  g.perm = ad->perm;
+  g.sid = ad->sid;
+  g.S = gemm_adapter_splits(g.M, g.Ntot, g.Ktot);
+  g.part = (float4 *)ad->part;
+#define QL_GEMM(MODEV, DQV, ADV) \
+  nf4_gemm_kernel<MODEV, DQV, ADV><<<dim3(grid, (unsigned)g.S), NT, 0, st>>>(g);
+#define QL_GEMM_AD(MODEV, DQV)                                                  \
+  if (MODEV == 1 || g.r % 8 == 0) {                                             \
+    if (g.rp == 16) { QL_GEMM(MODEV, DQV, 1) } else { QL_GEMM(MODEV, DQV, 4) }  \
+  } else {                                                                      \
+    if (g.rp == 16) { QL_GEMM(0, DQV, -1) } else { QL_GEMM(0, DQV, -2) }        \
   }
   if (mode == 0) {
     if (g.sc.dq) { QL_GEMM_AD(0, true) } else { QL_GEMM_AD(0, false) }
@@ -921,23 +1043,54 @@ static qlora_status launch_gemm(int mode, GemmArgs g, hipStream_t st) {
   }
 #undef QL_GEMM_AD
 #undef QL_GEMM
+  if (g.S > 1) launch_join(g, grid, st);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
+}
+
+// Workgroups per tile: the count with the least time by what was measured, in
+// 10 ns. A workgroup takes its K-steps plus four for its start and end; a step
+// takes 0.92 us while up to 0.6 of the 256 compute units work and 1.25 us when
+// all do; a split adds 5 us for the join and the partial sums' bytes, written
+// and read, at 6 TB/s. Measured forward times (4096 x 4096, r = 16, eight
+// adapters; one workgroup a tile / the chosen split): 64 tokens 66 / 31 us,
+// 512 69 / 41, 1024 69 / 60; 4096 x 11008, 777 tokens 166 / 115; a split of
+// 2048 tokens would take 111 us instead of 90.
+int gemm_adapter_splits(int64_t M, int64_t Ntot, int64_t Ktot) {
+  const int64_t tn = ql_cdiv(Ntot, BN), tiles = tn * ql_cdiv(M, BM), nk = ql_cdiv(Ktot, BK);
+  int best = 1;
+  int64_t least = 0;
+  for (const int S : {1, 2, 3, 4, 6, 8}) {   // those launch_join knows
+    if (S > nk) break;
+    const int64_t steps = ql_cdiv(nk, S) + 4, rounds = tiles * S / 256, rest = tiles * S % 256;
+    int64_t t = rounds * steps * 125;
+    if (rest) t += steps * (rest <= 154 ? 92 : 92 + (rest - 154) * 33 / 102);
+    if (S > 1) t += 500 + S * tn * M / 59;
+    if (S == 1 || t < least) {
+      least = t;
+      best = S;
+    }
+  }
+  return best;
+}
+size_t gemm_adapter_part_bytes(int64_t M, int64_t Ntot, int64_t Ktot) {
+  const int S = gemm_adapter_splits(M, Ntot, Ktot);
+  return S == 1 ? 0 : (size_t)(ql_cdiv(Ntot, BN) * ql_cdiv(M, BM) * S) * BN * BM * 4;
 }
 
 qlora_status launch_gemm_fwd(const uint8_t *codes, ql::ScaleSrc sc, int64_t d, int64_t k,
                              const uint16_t *X, int64_t M, const uint16_t *B, int r,
                              const uint16_t *Hs_hi, const uint16_t *Hs_lo, int rp,
-                             uint16_t *Y, hipStream_t st, const int *perm, const int *sid) {
-  GemmArgs g{codes, sc, d, k, X, M, d, k, B, Hs_hi, Hs_lo, r, rp, Y, nullptr, 1.0f, perm, sid};
-  return launch_gemm(0, g, st);
+                             uint16_t *Y, hipStream_t st, const GemmAdapters *ad) {
+  GemmArgs g{codes, sc, d, k, X, M, d, k, B, Hs_hi, Hs_lo, r, rp, Y, nullptr, 1.0f};
+  return launch_gemm(0, g, ad, st);
 }
 
 qlora_status launch_gemm_dx(const uint8_t *codes, ql::ScaleSrc sc, int64_t d, int64_t k,
                             const uint16_t *dY, int64_t M, const uint16_t *A, int r,
                             const uint16_t *Gs_hi, const uint16_t *Gs_lo, int rp,
                             uint16_t *dX, const uint8_t *keep, float inv_keep, hipStream_t st,
-                            const int *perm, const int *sid) {
-  GemmArgs g{codes, sc, d, k, dY, M, k, d, A, Gs_hi, Gs_lo, r, rp, dX, keep, inv_keep, perm, sid};
-  return launch_gemm(1, g, st);
+                            const GemmAdapters *ad) {
+  GemmArgs g{codes, sc, d, k, dY, M, k, d, A, Gs_hi, Gs_lo, r, rp, dX, keep, inv_keep};
+  return launch_gemm(1, g, ad, st);
 }

@@ -133,6 +133,7 @@ int *colacc_counters(float *part, int64_t M, int64_t C0, int64_t C1, int rp);
 
 // The same per adapter of a plan: out_a = s_a * sum over a's tokens. Q is in
 // token order with leading dimension ldq (a.ldq = r or rp; 16-byte aligned).
+// cnt: colacc_adapters_counter_count() counters, zero when the launch starts.
 struct ColaccAdReq {
   const uint16_t *In;
   int64_t C;
@@ -143,22 +144,25 @@ struct ColaccAdReq {
 };
 qlora_status launch_colacc2_adapters(const ColaccAdReq &a, const ColaccAdReq &b,
                                      const AdapterPlan &plan, int rp, int r, const float *scale,
-                                     float *part, hipStream_t st);
+                                     float *part, int *cnt, hipStream_t st);
 size_t colacc_adapters_part_bytes(const AdapterPlan &plan, int64_t C0, int64_t C1, int rp);
 int64_t colacc_adapters_counter_count(const AdapterPlan &plan, int64_t C0, int64_t C1);
-int *colacc_adapters_counters(float *part, const AdapterPlan &plan, int64_t C0, int64_t C1,
-                              int rp);
 
 // gemm.hip : fused dequant-GEMM, forward (Y) and input-gradient (dX) forms.
-// The rank-r epilogue reads B (d x r) resp. A (r x k) in place. With a plan's
-// perm and sid (both or neither), rows run in plan order: B (A) holds one
-// matrix per adapter, hi and lo are in plan order, X and Y in token order.
+// The rank-r epilogue reads B (d x r) resp. A (r x k) in place. With
+// GemmAdapters rows run in plan order: B (A) holds one matrix per adapter, hi
+// and lo are in plan order, X and Y in token order.
+struct GemmAdapters {
+  const int *perm, *sid;   // of the plan
+  void *part;              // gemm_adapter_part_bytes(M, Ntot, Ktot), 256-byte aligned
+};
+int gemm_adapter_splits(int64_t M, int64_t Ntot, int64_t Ktot);
+size_t gemm_adapter_part_bytes(int64_t M, int64_t Ntot, int64_t Ktot);
 qlora_status launch_gemm_fwd(const uint8_t *codes, ql::ScaleSrc sc, int64_t d,
                              int64_t k, const uint16_t *X, int64_t M,
                              const uint16_t *B, int r, const uint16_t *Hs_hi,
                              const uint16_t *Hs_lo, int rp, uint16_t *Y,
-                             hipStream_t st, const int *perm = nullptr,
-                             const int *sid = nullptr);
+                             hipStream_t st, const GemmAdapters *ad = nullptr);
 // keep (M x k/4 keep nibbles, or NULL): adapter-input dropout of the forward;
 // the rank-r term of dX is then kept per element and scaled by inv_keep.
 qlora_status launch_gemm_dx(const uint8_t *codes, ql::ScaleSrc sc, int64_t d,
@@ -166,7 +170,7 @@ qlora_status launch_gemm_dx(const uint8_t *codes, ql::ScaleSrc sc, int64_t d,
                             const uint16_t *A, int r, const uint16_t *Gs_hi,
                             const uint16_t *Gs_lo, int rp, uint16_t *dX,
                             const uint8_t *keep, float inv_keep, hipStream_t st,
-                            const int *perm = nullptr, const int *sid = nullptr);
+                            const GemmAdapters *ad = nullptr);
 
 // gemv.hip : memory-bound forward for M <= 16, including the LoRA down
 // projection, for nw (1..4) weights that read the same X (sibling

@@ -868,24 +868,17 @@ qlora_status launch_colacc2(const ColaccReq &a, const ColaccReq &b, int64_t M, i
 }
 
 size_t colacc_adapters_part_bytes(const AdapterPlan &plan, int64_t C0, int64_t C1, int rp) {
-  return (size_t)ql_rup(plan.max_slots * (C0 + C1) * rp * 4, 256) +
-         colacc_adapters_counter_count(plan, C0, C1) * 4;
+  return (size_t)(plan.max_slots * (C0 + C1) * rp) * 4;
 }
 
 int64_t colacc_adapters_counter_count(const AdapterPlan &plan, int64_t C0, int64_t C1) {
   return plan.max_slots * colacc_counter_count(C0, C1);
 }
 
-int *colacc_adapters_counters(float *part, const AdapterPlan &plan, int64_t C0, int64_t C1,
-                              int rp) {
-  return (int *)((char *)part + ql_rup(plan.max_slots * (C0 + C1) * rp * 4, 256));
-}
-
 qlora_status launch_colacc2_adapters(const ColaccAdReq &a, const ColaccAdReq &b,
                                      const AdapterPlan &plan, int rp, int r, const float *scale,
-                                     float *part, hipStream_t st) {
+                                     float *part, int *cnt, hipStream_t st) {
   if (rp % 16 || rp > CM_MAXRP) return QLORA_ERR_UNSUPPORTED;
-  int *cnt = colacc_adapters_counters(part, plan, a.C, b.C, rp);   // zeroed by the launch before
   const DropParams nodrop{0u, 0u, 0u, 1.0f, 0};
   ColaccProb p0{a.In, a.C, a.Q, part, ql_cdiv(a.C, CM_COLS), a.out, a.transpose_out, 0.0f, nodrop,
                 nullptr, a.ldq};

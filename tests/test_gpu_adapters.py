@@ -145,9 +145,10 @@ def test_with_a_real_base(ops, d, k, M, n, r, pattern, dq):
 
 
 def test_one_adapter_is_the_plain_linear(ops):
-    # every token on one adapter, in batch order: the same tiles, sums and
-    # roundings as the single-adapter calls, bit for bit
-    d, k, M, r, alpha = 512, 768, 300, 16, 32.0
+    # every token on one adapter, in batch order, and enough tiles that none is
+    # split over K: the same tiles, sums and roundings as the single-adapter
+    # calls, bit for bit
+    d, k, M, r, alpha = 4096, 4096, 2040, 16, 32.0
     t = inputs(d, k, M, 1, r, "one", 7, False)
     t["scale"][:] = alpha / r
     g = on_device(t)
