@@ -6,6 +6,8 @@
 //   dx_j = g (delta - p_j) - e p_j (logp_j + entropy),  logp_j = t_j - l.
 // Differences from the maximum keep every quantity near zero where the
 // logits themselves are large. Sums are float32.
+#include <float.h>
+
 #include <algorithm>
 
 #include "../../include/qlora_logprobs.h"
@@ -75,9 +77,6 @@ struct OpMax {
   template <class T> QL_DEV T operator()(T a, T b) const { return a > b ? a : b; }
   QL_DEV float operator()(float a, float b) const { return fmaxf(a, b); }
 };
-struct OpAdd {
-  QL_DEV float operator()(float a, float b) const { return a + b; }
-};
 template <class T, class Op>
 QL_DEV T block_reduce(T v, T *tmp, Op op) {
 #pragma unroll
@@ -125,12 +124,49 @@ QL_DEV void emit_ranked(const uint64_t *list, int count, int top, Emit emit) {
 constexpr int LP_LIST = 1024;   // candidates of a chunk held in LDS
 constexpr int LP_GROUPS = 64;   // groups of threads whose maxima give the threshold
 
+// Maximum, sum of exp(x - m) and of exp(x - m)(x - m) over some logits. m
+// starts at the lowest finite number, so that differences from it are never
+// NaN for want of a logit; z is 0 exactly when every logit is -inf.
+struct Sums {
+  float m, z, s;
+};
+QL_DEV Sums sums_at(const Sums &a, float m) {   // a referred to a maximum m >= a.m
+  const float d = a.m - m, e = fast_exp(d);
+  return Sums{m, a.z * e, (a.s + fmaxf(d, -1000.0f) * a.z) * e};
+}
+// The workgroup's sums in every thread: over each wave's lanes, then its waves
+// in order; tmp: LW entries, free for reuse only after a barrier.
+QL_DEV Sums block_sums(Sums a, Sums *tmp) {
+  float m = a.m;
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  a = sums_at(a, m);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    a.z += __shfl_xor(a.z, d);
+    a.s += __shfl_xor(a.s, d);
+  }
+  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = a;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < LW; ++w) m = fmaxf(m, tmp[w].m);
+  Sums t{m, 0.0f, 0.0f};
+#pragma unroll
+  for (int w = 0; w < LW; ++w) {
+    const Sums b = sums_at(tmp[w], m);
+    t.z += b.z;
+    t.s += b.s;
+  }
+  return t;
+}
+
 // A workgroup holds one chunk of a row (the whole row where it fits) in
 // registers, R 16-byte pieces a thread, all loaded before the first is used:
-// the row is read once from memory, its exact maximum is known before the
-// first exponential (one per logit, none to rescale), and the alternatives
-// are found in the same registers. Chunks of a split row leave (m, z, s) and
-// their best for logprobs_join_kernel.
+// the row is read once from memory. The sums are taken piece by piece as the
+// pieces arrive, against the thread's maximum so far (one exponential per
+// logit and one per piece to rescale), and the alternatives are found in the
+// same registers. Chunks of a split row leave (m, z, s) and their best for
+// logprobs_join_kernel.
 //
 // Alternatives: the top-th largest of 64 disjoint groups' maxima is a lower
 // bound of the top-th largest logit (that many groups hold one at least as
@@ -143,7 +179,7 @@ template <bool F32, int R, bool TOP>
 __global__ __launch_bounds__(LT) void logprobs_kernel(LpArgs g) {
   constexpr int E = lp_elems<F32>();
   constexpr uint32_t FILL = F32 ? 0xff800000u : 0xff80ff80u;   // -inf
-  __shared__ float tf[LW];
+  __shared__ Sums ts[LW];
   __shared__ uint64_t tk[LW];
   const int tid = threadIdx.x;
   const int64_t i = blockIdx.x / (uint32_t)g.nchunk;
@@ -153,63 +189,53 @@ __global__ __launch_bounds__(LT) void logprobs_kernel(LpArgs g) {
   const int len = (int)min(g.chunk, g.V - j0);
   const int nvec = len / E, rem = len % E;   // rem: the row's end only
   u32x4 x[R];
+  float xt = load1<F32>(row, j0 + min(nvec * E + tid, len - 1));
   if (nvec) {
     // pieces past the end re-read the last one (no branch around a load)
 #pragma unroll
     for (int r = 0; r < R; ++r) x[r] = load16<F32>(row, j0 + E * min(r * LT + tid, nvec - 1));
   }
-  float xt = load1<F32>(row, j0 + min(nvec * E + tid, len - 1));
-  xt = tid < rem ? xt : -INFINITY;
+  Sums a{-FLT_MAX, 0.0f, 0.0f};
+  auto add = [&](float v) {
+    const float t = v - a.m, e = fast_exp(t);
+    a.z += e;
+    a.s = fmaf(e, fmaxf(t, -1000.0f), a.s);   // e is 0 below that; keeps 0 * -inf out of s
+  };
+  float vm = -INFINITY;   // the pieces' maximum itself,
+  int best_r = 0;         // and the first piece that holds it
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < R; ++r) {
     if ((r + 1) * LT > nvec) {   // uniform
 #pragma unroll
       for (int q = 0; q < 4; ++q) x[r][q] = r * LT + tid < nvec ? x[r][q] : FILL;
     }
-  float tm = xt;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      tm = fmaxf(tm, fmaxf(elem<F32>(x[r], e), elem<F32>(x[r], e + 1)));
-  const float m = block_reduce(tm, tf, OpMax());
-  const float mm = m == -INFINITY ? 0.0f : m;
-  // each pass unpacks the pieces again: kept unpacked they would fill the registers
-  auto repack = [&]() {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t w = x[r][q];
-        asm("" : "+v"(w));
-        x[r][q] = w;
-      }
-  };
-  repack();
-  float z = 0.0f, s = 0.0f;
-  auto add = [&](float v) {
-    const float t = v - mm, e = fast_exp(t);
-    z += e;
-    s = fmaf(e, fmaxf(t, -1000.0f), s);   // e is 0 below that; keeps 0 * -inf out of s
-  };
-  add(xt);
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
     if (r * LT < nvec) {
+      float pm = fmaxf(elem<F32>(x[r], 0), elem<F32>(x[r], 1));
+#pragma unroll
+      for (int e = 2; e < E; e += 2)
+        pm = fmaxf(pm, fmaxf(elem<F32>(x[r], e), elem<F32>(x[r], e + 1)));
+      if (TOP) {
+        best_r = pm > vm ? r : best_r;
+        vm = fmaxf(vm, pm);
+      }
+      a = sums_at(a, fmaxf(a.m, pm));
 #pragma unroll
       for (int e = 0; e < E; ++e) add(elem<F32>(x[r], e));
     }
   }
-  z = block_reduce(z, tf, OpAdd());
-  s = block_reduce(s, tf, OpAdd());
+  xt = tid < rem ? xt : -INFINITY;
+  a = sums_at(a, fmaxf(a.m, xt));
+  add(xt);
+  const Sums t = block_sums(a, ts);
   const bool whole = g.nchunk == 1;
-  const bool empty = z == 0.0f;              // every logit -inf
+  const bool empty = t.z == 0.0f;            // every logit -inf
+  const float m = empty ? -INFINITY : t.m, z = t.z;
   const float l = empty ? 0.0f : logf(z);
   if (tid == 0) {
     if (whole)
-      finish_row<F32>(g, i, row, m, l, z, s, empty);
+      finish_row<F32>(g, i, row, m, l, z, t.s, empty);
     else
-      g.part[i * g.nchunk + c] = make_float4(m, z, s, 0.0f);
+      g.part[i * g.nchunk + c] = make_float4(t.m, z, t.s, 0.0f);
   }
   if (!TOP) return;
 
@@ -227,17 +253,35 @@ __global__ __launch_bounds__(LT) void logprobs_kernel(LpArgs g) {
   const uint32_t jt = (uint32_t)(j0 + nvec * E + tid);
   uint32_t jb = (uint32_t)(j0 + E * tid);   // index of the thread's first logit
   auto index = [&](int r, int e) { return jb + (uint32_t)(E * LT * r + e); };
+  // each pass unpacks the pieces again: kept unpacked, or with every index
+  // formed ahead, they would fill the registers
+  auto repack = [&]() {
+    asm("" : "+v"(jb));
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w = x[r][q];
+        asm("" : "+v"(w));
+        x[r][q] = w;
+      }
+  };
   bool plain = z == z;
   repack();
   if (plain) {   // uniform
-    // first index of the thread's maximum; what is past the end comes last
-    uint32_t at = tid < rem && xt == tm ? jt : 0xffffffffu;
+    // the thread's best: the first place of its maximum in that piece, or the
+    // row's end (whose index is the largest)
+    u32x4 w = x[0];
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r)
+    for (int r = 1; r < R; ++r)
 #pragma unroll
-      for (int e = E - 1; e >= 0; --e)
-        if (elem<F32>(x[r], e) == tm && r * LT + tid < nvec) at = index(r, e);
-    const uint64_t mine = at == 0xffffffffu ? 0 : order_key(tm, at);
+      for (int q = 0; q < 4; ++q) w[q] = best_r == r ? x[r][q] : w[q];
+    int be = 0;
+#pragma unroll
+    for (int e = E - 1; e >= 0; --e) be = elem<F32>(w, e) == vm ? e : be;
+    uint64_t mine = 0;
+    if (tid < nvec) mine = order_key(vm, index(0, 0) + (uint32_t)(E * LT * best_r + be));
+    if (tid < rem) mine = OpMax()(mine, order_key(xt, jt));
     uint64_t gm = mine;
 #pragma unroll
     for (int d = 1; d < LT / LP_GROUPS; d <<= 1) gm = OpMax()(gm, (uint64_t)__shfl_xor(gm, d));
@@ -251,20 +295,25 @@ __global__ __launch_bounds__(LT) void logprobs_kernel(LpArgs g) {
     for (int o = 0; o < LP_GROUPS; ++o) rank += grp[o] > own ? 1 : 0;
     const uint64_t hit = __ballot(rank == top - 1 && own != 0);
     const uint64_t floor_key = hit ? __shfl(own, __builtin_ctzll(hit)) : 1;
+    const float floor_val = hit ? key_value(floor_key) : -INFINITY;
     repack();
-    asm("" : "+v"(jb));   // indices are formed where they are used, too
     if (mine >= floor_key) {
       auto offer = [&](float v, uint32_t j) {
         const uint64_t k = order_key(v, j);
         if (k < floor_key) return;
-        const int at2 = atomicAdd(&count, 1);
-        if (at2 < LP_LIST) list[at2] = k;
+        const int at = atomicAdd(&count, 1);
+        if (at < LP_LIST) list[at] = k;
       };
 #pragma unroll
       for (int r = 0; r < R; ++r)
         if (r * LT + tid < nvec) {
+          float pm = elem<F32>(x[r], 0);
 #pragma unroll
-          for (int e = 0; e < E; ++e) offer(elem<F32>(x[r], e), index(r, e));
+          for (int e = 1; e < E; ++e) pm = fmaxf(pm, elem<F32>(x[r], e));
+          if (pm >= floor_val) {   // few pieces
+#pragma unroll
+            for (int e = 0; e < E; ++e) offer(elem<F32>(x[r], e), index(r, e));
+          }
         }
       if (tid < rem) offer(xt, jt);
     }
@@ -280,7 +329,6 @@ __global__ __launch_bounds__(LT) void logprobs_kernel(LpArgs g) {
     for (int q = 0; q < top; ++q) {
       uint64_t best = 0;
       repack();
-      asm("" : "+v"(jb));
       auto offer = [&](float v, uint32_t j) {
         const uint64_t k = order_key(v, j);
         if (k < last && k > best) best = k;
@@ -303,29 +351,25 @@ __global__ __launch_bounds__(LT) void logprobs_kernel(LpArgs g) {
 // ceil(top / nchunk)-th entry (at least top keys do) are ranked as above.
 template <bool F32>
 __global__ __launch_bounds__(LT) void logprobs_join_kernel(LpArgs g) {
-  __shared__ float tf[LW];
+  __shared__ Sums ts[LW];
   __shared__ uint64_t tk[LW];
   const int tid = threadIdx.x;
   const int64_t i = blockIdx.x;
   const void *row = row_of<F32>(g.x, i, g.ld);
   const float4 *part = g.part + i * g.nchunk;
-  float m = -INFINITY;
-  for (int c = tid; c < g.nchunk; c += LT) m = fmaxf(m, part[c].x);
-  m = block_reduce(m, tf, OpMax());
-  float z = 0.0f, s = 0.0f;
+  Sums a{-FLT_MAX, 0.0f, 0.0f};
   for (int c = tid; c < g.nchunk; c += LT) {
     const float4 p = part[c];
-    if (p.y == 0.0f) continue;                     // nothing but -inf
-    const float t = p.x == -INFINITY ? 0.0f : p.x - m;   // -inf: a chunk of -inf and NaN
-    const float e = expf(t);
-    z += e * p.y;
-    s += e * (p.z + fmaxf(t, -1000.0f) * p.y);
+    const float m = fmaxf(a.m, p.x);
+    a = sums_at(a, m);
+    const Sums b = sums_at(Sums{p.x, p.y, p.z}, m);
+    a.z += b.z;
+    a.s += b.s;
   }
-  z = block_reduce(z, tf, OpAdd());
-  s = block_reduce(s, tf, OpAdd());
-  const bool empty = z == 0.0f;
-  const float l = empty ? 0.0f : logf(z);
-  if (tid == 0) finish_row<F32>(g, i, row, m, l, z, s, empty);
+  const Sums t = block_sums(a, ts);
+  const bool empty = t.z == 0.0f;
+  const float m = empty ? -INFINITY : t.m, l = empty ? 0.0f : logf(t.z);
+  if (tid == 0) finish_row<F32>(g, i, row, m, l, t.z, t.s, empty);
   const int top = g.top;
   if (!top) return;
 

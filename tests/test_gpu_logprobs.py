@@ -5,7 +5,7 @@ Bounds. t = x - m is one float32 subtraction (2^-24 |t|). A term of
 z = sum exp(t) is off by 2^-22 (the exponential) + 2^-23 |t| (its argument's
 rounding and scaling) of itself; weighted by p that is 2^-22 + 2^-23 T with
 T = sum p |t|. A float32 sum in which no addend passes more than V / 64 + 64
-additions adds (V / 64 + 64) 2^-24. So l = log z is off by
+additions (a rescaling, 2^-22, counting as four) adds (V / 64 + 64) 2^-24. So l = log z is off by
 ez = 2^-22 + 2^-23 T + (V / 64 + 64) 2^-24, plus 2^-22 |l|; the entropy, whose
 second sum has the same relative errors on its magnitude T, by
 2 (1 + T) ez + 2^-22 |l|. p = exp(logp) is off by the error of logp plus
@@ -107,7 +107,10 @@ def check(ops, buf, V, targets, top, dent=True, ws=None):
         tol[i] = p * (mag * (dp + 4 * U) + abs(ei) * (dl + ee[i])) + 4 * U * abs(want[i])
         if has[i]:
             tol[i][targets[i]] += 4 * U * abs(gi)
-        tol[i] += 1e-37       # results below the smallest normal number
+        # an exponential below the smallest normal number, 2^-126, may be flushed
+        # to zero: p is then off by up to 2^-126, the gradient by that times mag;
+        # and a product below it by up to 2^-126 itself
+        tol[i] += 2.0 ** -126 * (mag + 1)
     half = 2.0 ** -8 if buf.dtype == torch.bfloat16 else U
     near(dx, want, tol + half * (abs(want) + tol), "gradient")
     return lp, dx
@@ -138,7 +141,7 @@ def test_matches_the_oracle(ops, N, V, ld, dtype, top):
 @pytest.mark.parametrize("V", [100, 40000])
 def test_special_rows(ops, V, dtype):
     print(f"[logprobs special] V={V} {dtype}", flush=True)
-    buf = logits_of(17, V, V, dtype, 3)
+    buf = logits_of(18, V, V, dtype, 3)
     lowest, inf = torch.finfo(dtype).min, float("inf")
     buf[0] = -inf                              # nothing allowed
     buf[1] = lowest                            # a mask of the type's lowest value everywhere
@@ -159,10 +162,12 @@ def test_special_rows(ops, V, dtype):
     buf[14] = torch.arange(V, device="cuda").to(dtype)        # ascending
     buf[15] = -torch.arange(V, device="cuda").float().to(dtype)
     buf[16] = float("nan")
-    t = np.arange(17) % V
+    buf[17] = -inf                             # the lowest value beside banned words
+    buf[17, V // 2:: 3] = lowest
+    t = np.arange(18) % V
     t[3], t[8], t[12] = 0, -100, 1             # row 12's target is banned
     check(ops, buf, V, t, 20)
-    check(ops, buf, V, np.full(17, -100), 3, dent=False)      # nothing to learn: zeros
+    check(ops, buf, V, np.full(18, -100), 3, dent=False)      # nothing to learn: zeros
 
 
 def test_gradient_in_place_strides_and_repeats(ops):
