@@ -125,7 +125,8 @@ BF, F32 = torch.bfloat16, torch.float32
     (2, 4097, 4099, BF, 32), (1, 32000, 32000, BF, 5), (40, 32000, 32000, BF, 0),
     (3, 50257, 50304, BF, 1), (2, 50257, 50257, F32, 20), (1, 131072, 131072, F32, 32),
     (2, 131073, 131080, BF, 20), (1, 300007, 300007, BF, 32), (600, 1000, 1001, BF, 3),
-    (700, 257, 257, F32, 0), (1100, 33000, 33000, BF, 2),
+    (700, 257, 257, F32, 0), (1100, 33000, 33000, BF, 2), (257, 40001, 40001, F32, 4),
+    (256, 131072, 131072, BF, 2), (260, 70000, 70008, F32, 1), (300, 20000, 20000, F32, 32),
 ])
 def test_matches_the_oracle(ops, N, V, ld, dtype, top):
     print(f"[logprobs] N={N} V={V} ld={ld} {dtype} top={top}", flush=True)
