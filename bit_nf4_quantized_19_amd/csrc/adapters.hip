@@ -7,6 +7,9 @@
 // (groups of AD_TOK tokens, splits of an adapter's tokens) are written in the
 // same pass: position p of an adapter whose first position is off opens group
 // (p - off) / AD_TOK when that division is exact, and likewise its splits.
+// Group g of G has record (g % (G / 8)) 8 + g / (G / 8): workgroups go to the
+// eight XCDs in turn, so the groups of one adapter, which are neighbours, meet
+// in one XCD's L2.
 //
 // Each of the 8 waves owns one contiguous eighth of the batch and one row of
 // an LDS histogram (8 x 1025 counters is the most that leaves room for the
@@ -66,6 +69,7 @@ QL_DEV int block_exsum(int v, int *tmp, int tid, int &total) {
 __global__ __launch_bounds__(PT) void adapter_plan_kernel(PlanArgs g) {
   __shared__ int hist[PW][PB];                       // counts, then next positions
   __shared__ int s_off[PB + 1], s_grp[PB], s_split[PB], s_slot[PB];
+  __shared__ int s_per;                              // groups of one eighth of the records
   __shared__ int tmp[PW];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = g.n, nb = n + 1;
@@ -139,8 +143,13 @@ __global__ __launch_bounds__(PT) void adapter_plan_kernel(PlanArgs g) {
     s_off[nb] = g.off[nb] = (int)g.M;
     g.num[0] = tot[2];
     g.num[1] = g.num[2] = g.num[3] = 0;
+    s_per = (int)ql_cdiv(tot[1], 8);
   }
-  for (int64_t i = tot[1] + tid; i < g.max_groups; i += PT) g.grp[AD_GRP * i + 2] = 0;
+  // records without a group (group (i % 8) per + i / 8 would be past the last)
+  const int per8 = (int)ql_cdiv(tot[1], 8);
+  for (int64_t i = tid; i < g.max_groups; i += PT)
+    if (i >= 8 * (int64_t)per8 || (i & 7) * (int64_t)per8 + (i >> 3) >= tot[1])
+      g.grp[AD_GRP * i + 2] = 0;
   __syncthreads();
 
   for (int64_t m0 = lo; m0 < hi; m0 += 64) {
@@ -155,7 +164,8 @@ __global__ __launch_bounds__(PT) void adapter_plan_kernel(PlanArgs g) {
     g.perm[p] = (int)(m0 + lane);
     g.sid[p] = b < n ? b : -1;
     const int q = p - s_off[b], end = s_off[b + 1];
-    int *e = g.grp + AD_GRP * (int64_t)(s_grp[b] + q / AD_TOK);
+    const int gi = s_grp[b] + q / AD_TOK;
+    int *e = g.grp + AD_GRP * ((int64_t)(gi % s_per) * 8 + gi / s_per);
     e[4 + q % AD_TOK] = (int)(m0 + lane);
     if (q % AD_TOK == 0) {
       e[0] = b;
@@ -184,7 +194,7 @@ __global__ __launch_bounds__(PT) void adapter_plan_kernel(PlanArgs g) {
 // never finer than its smallest chunk.
 AdapterPlan::AdapterPlan(void *data, int64_t M_, int n_) : M(M_), n(n_) {
   split_tok = ql_rup(ql_cdiv(M, AD_SPLITS), 128);
-  max_groups = M / AD_TOK + (M < n + 1 ? M : n + 1);
+  max_groups = ql_rup(M / AD_TOK + (M < n + 1 ? M : n + 1), 8);
   max_splits = M / split_tok + n;
   max_slots = 2 * ql_cdiv(M, split_tok);
   int64_t at = 0;

@@ -48,7 +48,7 @@ qlora_status launch_dequantize(const uint8_t *codes, ql::ScaleSrc sc, int64_t n,
 //   off   [n+2]   first position of adapter a; off[n]: of none; off[n+1] = M
 //   num   [4]     splits
 //   grp   [16 g]  (adapter or n for none, first position, tokens, 0, the tokens):
-//                 up to AD_TOK positions; records past the last group have 0 tokens
+//                 up to AD_TOK positions; records of no group have 0 tokens
 //   split [8 s]   (adapter, lo, hi, first slot or -1, index, count, 0, 0): positions
 //                 lo .. hi of one adapter; an adapter with one split has no slot
 // Every adapter has at least one split (an empty one when it has no token).

@@ -161,7 +161,7 @@ __global__ __launch_bounds__(64 * SK_W) void skinny_kernel(SkinnyArgs a) {
     pos0 = gr[1];
     ntok = min(gr[2], SK_TOK);
     none = ad == a.n;
-    if (ntok <= 0) return;   // past the last group
+    if (ntok <= 0) return;   // a record of no group
   }
   const int wi = AD ? 0 : (int)blockIdx.y / a.tbw;   // uniform: fields picked by selects
   const uint16_t *__restrict__ In = a.In;
