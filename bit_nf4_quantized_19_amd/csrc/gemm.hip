@@ -157,6 +157,11 @@ QL_DEV float scale_of(uint32_t qd, float s2, int64_t blk, float mu) {
 // codes (waves 0-3) or scale words (waves 4-7).
 constexpr int kLoadsPerStep = 5;
 
+// First rows of a tile's runs, a bit a row: rows 0-63, 64-127, 128-191, 192-255.
+struct Rows {
+  uint64_t a, b, c, d;
+};
+
 // AD: 0 one adapter; else many, taking 16 |AD| ranks at a time,
 // the matrices' rows (forward) being whole 16-byte pieces (AD > 0) or not
 template <int MODE, bool DQ, int AD>
@@ -596,59 +601,70 @@ struct Tile {
   // the copy where its row (column l % 32 of a block of D) lies in the run.
   // Selecting results, rather than zeroing the other rows' operands, keeps an
   // infinity or NaN in one adapter's matrix out of the others' rows.
-  // Of a split tile, split y takes every S-th run from the y-th on.
+  // Of a split tile, split y takes every S-th run from the y-th on. A wave
+  // finds the runs that meet its rows from the bit masks of their first rows
+  // (walking all the tile's runs cost 0.7 us a run).
   QL_DEV void adapter_terms(int y, int S) {
     // opaque, or the selects among them below become indexed reads of a scratch copy
     int id0 = pre_id[0], id1 = pre_id[1], id2 = pre_id[2], id3 = pre_id[3];
     asm("" : "+v"(id0), "+v"(id1), "+v"(id2), "+v"(id3));
     const int64_t left = g.M - m0;
-    int live = 0;
-    const uint64_t st0 = run_starts(id0, -1, left, live);
-    const uint64_t st1 = run_starts(id1, __builtin_amdgcn_readlane(id0, 63), left - 64, live);
-    const uint64_t st2 = run_starts(id2, __builtin_amdgcn_readlane(id1, 63), left - 128, live);
-    const uint64_t st3 = run_starts(id3, __builtin_amdgcn_readlane(id2, 63), left - 192, live);
-    if (live == 0) return;
-    const auto next = [=](int p) { return next_start(p, st0, st1, st2, st3, live); };
-    const auto mine = [=](int p) {   // the next run of this split
-      for (int n = 0; n < S && p < live; ++n) p = next(p + 1);
-      return p;
-    };
+    int live = 0, runs = 0;
+    Rows own;   // first rows of this split's runs
+    Rows all;   // of all runs
+    all.a = run_starts(id0, -1, left, live, runs, y, S, own.a);
+    all.b = run_starts(id1, __builtin_amdgcn_readlane(id0, 63), left - 64, live, runs, y, S, own.b);
+    all.c = run_starts(id2, __builtin_amdgcn_readlane(id1, 63), left - 128, live, runs, y, S, own.c);
+    all.d = run_starts(id3, __builtin_amdgcn_readlane(id2, 63), left - 192, live, runs, y, S, own.d);
     const int blk = 256 * ((g.r + 3) & ~3);     // bytes of a run's block
     const int per = (BM * 128) / blk;           // blocks of a stage
     const int half = 3 * per / 2;               // runs in flight together
     const uint32_t x0 = lds_addr(s_X0), x1 = lds_addr(s_X1), x2 = lds_addr(s_X2);
-    // runs from row p on, `half` of them at most, into the blocks from slot on
-    const auto fetch = [=](int p, int slot) {
-      for (int n = 0; n < half && p < live; ++n, p = mine(p)) {
+    Rows rem = own;   // not yet fetched
+    // the next runs, `half` of them at most, into the blocks from slot on
+    const auto fetch = [&](int slot) {
+      int n = 0;
+      for (; n < half; ++n) {
+        const int p = take_row(rem);
+        if (p < 0) break;
         const int ad = __builtin_amdgcn_readlane(p < 64 ? id0 : p < 128 ? id1 : p < 192 ? id2 : id3,
                                                  p & 63);
         fetch_run(g.L + (int64_t)ad * g.r * g.Ntot, run_block(slot + n, per, blk, x0, x1, x2));
       }
-      return p;
+      return n;
     };
-    int row = 0, slot = 0;
-    for (int n = 0; n < y && row < live; ++n) row = next(row + 1);
-    int ahead = fetch(row, 0);
+    int slot = 0, done = 0, count = fetch(0);
 #pragma clang loop unroll(disable)
-    while (row < live) {
+    while (count > 0) {
       __builtin_amdgcn_s_waitcnt(0);
       block_sync();   // this batch has landed; the other half's readers are done
-      const int end = ahead;
-      ahead = fetch(end, half - slot);
-      batch_runs<0>(row, end, slot, per, blk, x0, x1, x2, next, mine);
-      batch_runs<1>(row, end, slot, per, blk, x0, x1, x2, next, mine);
-      row = end;
+      const int coming = fetch(half - slot);
+      batch_runs<0>(all, own, live, done, count, slot, per, blk, x0, x1, x2);
+      batch_runs<1>(all, own, live, done, count, slot, per, blk, x0, x1, x2);
+      done += count;
+      count = coming;
       slot = half - slot;
     }
   }
 
-  // The runs of rows row .. end - 1, in the blocks from slot on, for the wave's
-  // row block J.
-  template <int J, class Next, class Mine>
-  QL_DEV void batch_runs(int row, int end, int slot, int per, int blk, uint32_t x0, uint32_t x1,
-                         uint32_t x2, const Next &next, const Mine &mine) {
+  // Runs done .. done + count - 1 of this split, in the blocks from slot on,
+  // for the wave's row block J.
+  template <int J>
+  QL_DEV void batch_runs(const Rows &all, const Rows &own, int live, int done, int count, int slot,
+                         int per, int blk, uint32_t x0, uint32_t x1, uint32_t x2) {
     const int first = 64 * wm + 32 * J;
-    if (row >= first + 32 || end <= first) return;
+    const uint64_t word = wm == 0 ? own.a : wm == 1 ? own.b : wm == 2 ? own.c : own.d;
+    const uint64_t below = J == 0 ? 0 : word & 0xffffffffull;
+    // this split's runs that start before the block, and the last of them
+    int before = __builtin_popcountll(below), prev = -1;
+    if (wm > 0) before += __builtin_popcountll(own.a), prev = last_row(own.a, 0, prev);
+    if (wm > 1) before += __builtin_popcountll(own.b), prev = last_row(own.b, 64, prev);
+    if (wm > 2) before += __builtin_popcountll(own.c), prev = last_row(own.c, 128, prev);
+    prev = last_row(below, 64 * wm, prev);
+    const uint32_t inside = (uint32_t)(word >> (32 * J));
+    const int prev_end = prev < 0 ? 0 : next_start(prev + 1, all, live);
+    const int lo = prev_end > first ? before - 1 : before, hi = before + __builtin_popcount(inside);
+    if (hi <= done || lo >= done + count) return;
     int rr = r32, hh = h;   // opaque: the addresses below are not formed before the last K-steps
     asm volatile("" : "+v"(rr), "+v"(hh));
 #pragma clang loop unroll(disable)
@@ -665,13 +681,21 @@ struct Tile {
           b[c][part] = *(const uint4 *)((part ? g.Slo : g.Shi) +
                                         (m < g.M ? m : g.M - 1) * g.rp + t + 8 * hh);
         }
-      int q0 = row;
+      uint32_t rest = inside;
+      int q0 = prev, q1 = prev_end;
+      if (lo == before && rest) {
+        q0 = first + __builtin_ctz(rest);
+        q1 = next_start(q0 + 1, all, live);
+        rest &= rest - 1;
+      }
 #pragma clang loop unroll(disable)
-      for (int n = 0; q0 < end; ++n) {
-        const int q1 = next(q0 + 1);
-        if (q1 > first && q0 < first + 32)
-          adapter_run<J>(run_block(slot + n, per, blk, x0, x1, x2), t0, b, q0, q1, rr, hh);
-        q0 = mine(q0);
+      for (int n = lo; n < hi; ++n) {
+        if (n >= done && n < done + count)
+          adapter_run<J>(run_block(slot + n - done, per, blk, x0, x1, x2), t0, b, q0, q1, rr, hh);
+        if (!rest) break;
+        q0 = first + __builtin_ctz(rest);
+        q1 = next_start(q0 + 1, all, live);
+        rest &= rest - 1;
       }
     }
   }
@@ -709,13 +733,35 @@ struct Tile {
   }
 
   // Lanes whose row starts a run, given the previous 64 rows' last adapter and
-  // the rows left in the batch; adds the rows with an adapter to live.
-  QL_DEV uint64_t run_starts(int id, int before, int64_t left, int &live) const {
+  // the rows left in the batch; own: those of every S-th run from the y-th on.
+  // live counts the rows with an adapter, runs the runs.
+  QL_DEV uint64_t run_starts(int id, int before, int64_t left, int &live, int &runs, int y, int S,
+                             uint64_t &own) const {
     int prev = __shfl_up(id, 1);
     if (lane == 0) prev = before;
     const bool on = lane < left && id >= 0;
     live += __popcll(__ballot(on));
-    return __ballot(on && id != prev);
+    const uint64_t starts = __ballot(on && id != prev);
+    own = starts;
+    if (S > 1) {
+      const int n = runs + __popcll(starts & ((1ull << lane) - 1));
+      own = __ballot(((starts >> lane) & 1) && n % S == y);
+    }
+    runs += __popcll(starts);
+    return starts;
+  }
+  // Takes the first row out (none: -1).
+  static QL_DEV int take_row(Rows &r) {
+    int p = -1;
+    if (r.a) p = __builtin_ctzll(r.a), r.a &= r.a - 1;
+    else if (r.b) p = 64 + __builtin_ctzll(r.b), r.b &= r.b - 1;
+    else if (r.c) p = 128 + __builtin_ctzll(r.c), r.c &= r.c - 1;
+    else if (r.d) p = 192 + __builtin_ctzll(r.d), r.d &= r.d - 1;
+    return p;
+  }
+  // Last row of the word that starts at row base (none: prev).
+  static QL_DEV int last_row(uint64_t word, int base, int prev) {
+    return word ? base + 63 - __builtin_clzll(word) : prev;
   }
   // LDS address of a run's block: per blocks of blk bytes in each stage.
   static QL_DEV uint32_t run_block(int slot, int per, int blk, uint32_t x0, uint32_t x1,
@@ -724,16 +770,13 @@ struct Tile {
     return x0 + (st > 0) * (x1 - x0) + (st > 1) * (x2 - x1) + (uint32_t)((slot - st * per) * blk);
   }
   // First start at or after row p (live: none).
-  static QL_DEV int next_start(int p, uint64_t a, uint64_t b, uint64_t c, uint64_t d, int live) {
-    const int w = p >> 6, k = p & 63;
-    if (w == 0) a &= ~0ull << k;
-    if (w == 1) b &= ~0ull << k;
-    if (w == 2) c &= ~0ull << k;
-    if (w == 3) d &= ~0ull << k;
-    if (w < 1 && a) return __builtin_ctzll(a);
-    if (w < 2 && b) return 64 + __builtin_ctzll(b);
-    if (w < 3 && c) return 128 + __builtin_ctzll(c);
-    if (w < 4 && d) return 192 + __builtin_ctzll(d);
+  static QL_DEV int next_start(int p, const Rows &r, int live) {
+    const int w = p >> 6;
+    const uint64_t m = ~0ull << (p & 63);
+    if (w == 0 && (r.a & m)) return __builtin_ctzll(r.a & m);
+    if (w <= 1 && (w == 1 ? r.b & m : r.b)) return 64 + __builtin_ctzll(w == 1 ? r.b & m : r.b);
+    if (w <= 2 && (w == 2 ? r.c & m : r.c)) return 128 + __builtin_ctzll(w == 2 ? r.c & m : r.c);
+    if (w <= 3 && (w == 3 ? r.d & m : r.d)) return 192 + __builtin_ctzll(w == 3 ? r.d & m : r.d);
     return live;
   }
 
