@@ -300,6 +300,110 @@ QL_DEV void unit_compute(const GemvArgs &g, const GUnit *const (&us)[NU],
   }
 }
 
+// ---- nine to sixteen tokens, many adapters -----------------------------------
+// The layout above spends an MFMA on four tokens of four blocks (a quarter of
+// its products), so that the lane that owns a block's scale gets the block's
+// sum; with many tokens the MFMAs and the reads of X for them set the time.
+// Here one MFMA takes all sixteen tokens (rows of A) on 32 columns of one
+// block: the four lane groups, which hold whole blocks 4c .. 4c + 3 of a row
+// as loaded (full 128-byte lines), exchange quarters, after which lane (n, q)
+// holds columns 16 q .. + 15 of each of the four. That is a 4 x 4
+// transposition over the groups: eight lane-group swaps a chunk. Two MFMAs
+// then give a block's sums D[4q + i][n], which every lane scales (a lane reads
+// the codes of all its row's scales anyway). X is held in the same upper
+// halves of the table rows, one read's 64 pieces consecutive.
+// Measured with r = 16, the layout above -> this one: sixteen tokens 12.3 ->
+// 11.6 us (4096 x 4096), 17.0 -> 15.0 (11008 x 4096), 23.5 -> 19.9
+// (4096 x 11008); with eight it loses, 10.8 -> 11.3, 13.3 -> 13.7 and
+// 18.7 -> 19.5, so the layout above serves up to eight.
+QL_DEV uint32_t x16_addr(int m, int b, int sc8) {   // X[m][64 b + 8 sc8 ..] of the slice
+  const int piece = m + 16 * (sc8 >> 1);
+  return (uint32_t)(((b * 2 + (sc8 & 1)) * 8 + (piece >> 3)) * 256 + 128 + (piece & 7) * 16);
+}
+
+QL_DEV void swap_groups16(uint32_t &a, uint32_t &b) {   // a: rows a0 b0 a2 b2; b: a1 b1 a3 b3
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+QL_DEV void swap_groups32(uint32_t &a, uint32_t &b) {   // a: rows a0 a1 b0 b1; b: a2 a3 b2 b3
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+template <bool DQ, bool QA>
+QL_DEV void chunk16(GUnit &u, int c, f32x4 &acc, const unsigned char *smem,
+                    const unsigned char *xp, uint32_t lcopy, int n) {
+  // dword s of piece j becomes the codes of block 4c + j, columns 16 q + 8 s ..
+  uint4 lo = u.cw[c][0], hi = u.cw[c][1];
+  swap_groups16(lo.x, lo.z);
+  swap_groups16(lo.y, lo.w);
+  swap_groups16(hi.x, hi.z);
+  swap_groups16(hi.y, hi.w);
+  swap_groups32(lo.x, hi.x);
+  swap_groups32(lo.y, hi.y);
+  swap_groups32(lo.z, hi.z);
+  swap_groups32(lo.w, hi.w);
+  const uint32_t win =
+      !DQ ? 0u
+      : QA ? (uint32_t)__shfl((int)u.qw[0], n + 16 * c)
+           : __builtin_amdgcn_alignbyte(u.qw[c + 1], u.qw[c], (uint32_t)(u.blk0 & 3));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint4 &h = (j >> 1) ? hi : lo;
+      const uint32_t w = (j & 1) ? (s ? h.w : h.z) : (s ? h.y : h.x);
+      uint4 bop;
+      bop.x = *(const uint32_t *)(smem + __builtin_amdgcn_perm(w, lcopy, 0x0C0C0400u));
+      bop.y = *(const uint32_t *)(smem + __builtin_amdgcn_perm(w, lcopy, 0x0C0C0500u));
+      bop.z = *(const uint32_t *)(smem + __builtin_amdgcn_perm(w, lcopy, 0x0C0C0600u));
+      bop.w = *(const uint32_t *)(smem + __builtin_amdgcn_perm(w, lcopy, 0x0C0C0700u));
+      const uint4 aop = *(const uint4 *)(xp + ((4 * c + j) * 2 + s) * 2048);
+      p = ql::mfma16(aop, bop, p);
+    }
+    float ap;   // scale of block 4c + j of row n
+    if (DQ) {
+      const float s2 = ((u.blk0 + 4 * c + j) >> 8) == (u.blk0 >> 8) ? u.s2lo : u.s2hi;
+      ap = (float)(int)(int8_t)(win >> (8 * j)) * s2 + u.mu;
+    } else {
+      ap = __shfl(u.araw[c], n + 16 * j);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = fmaf(ap, p[i], acc[i]);
+  }
+}
+
+// The wave's one or two units, chunk by chunk.
+template <bool DQ, int NU, bool QA, class Issue>
+QL_DEV void unit_compute16(const GemvArgs &g, GUnit *const (&us)[NU], const unsigned char *smem,
+                           uint32_t lcopy, int lane, int64_t slice, Issue issue) {
+  const int n = lane & 15, q = lane >> 4;
+  const unsigned char *xp = smem + (lane >> 3) * 256 + 128 + (lane & 7) * 16;
+  f32x4 acc[NU];
+#pragma unroll
+  for (int v = 0; v < NU; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    issue(c);   // the code loads of a later chunk go out before this chunk's decode
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int v = 0; v < NU; ++v) chunk16<DQ, QA>(*us[v], c, acc[v], smem, xp, lcopy, n);
+  }
+#pragma unroll
+  for (int v = 0; v < NU; ++v) {
+    const int64_t row = us[v]->row0 + n;
+    if (row >= us[v]->dlim) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 4 * q + i;
+      if (t < g.M) g.part[(slice * g.M + t) * g.dtot + us[v]->rbase + row] = acc[v][i];
+    }
+  }
+}
+
 // LoRA down projection H = X A^T (QLoRA glossary, forward paragraph), partial
 // sums over the 128 columns of this slice that wave w covers, on 16x16x32
 // MFMA: A operand = X rows (tokens), B operand = A rows (ranks 16 cb ..
@@ -454,7 +558,8 @@ QL_DEV void adapter_down(const uint16_t *X, const uint16_t *A, const GemvAd &ad,
 // w + GW, both loaded before the table is built, then computed together. The
 // table and the X slice are built once per workgroup.
 // AD: the workgroups past the G of a slice compute the H partials of the
-// tokens' own adapters instead (M rp / 16 of them).
+// tokens' own adapters instead (M rp / 16 of them). TP == 0: the layout of
+// unit_compute16 (with AD, for more than eight tokens).
 template <bool DQ, int TP, bool FULL, bool GRP, bool QA, bool AD>
 __global__ __launch_bounds__(GT) void nf4_gemv_kernel(GemvArgs g) {
   __shared__ __align__(16) unsigned char smem[LDS_BYTES];
@@ -536,7 +641,10 @@ __global__ __launch_bounds__(GT) void nf4_gemv_kernel(GemvArgs g) {
     const int idx = tid + GT * i;
     const int m = idx >> 7, b = (idx >> 3) & 15, sc8 = idx & 7;
     const bool ok = m < g.M && b < nblk;
-    *(uint4 *)(smem + xa_base(m >> 2, b & 3, m & 3) + xa_imm(b >> 2, sc8)) = ok ? xv[i] : ql::zero4();
+    if constexpr (TP == 0)
+      *(uint4 *)(smem + x16_addr(m, b, sc8)) = ok ? xv[i] : ql::zero4();
+    else
+      *(uint4 *)(smem + xa_base(m >> 2, b & 3, m & 3) + xa_imm(b >> 2, sc8)) = ok ? xv[i] : ql::zero4();
   }
   if (tid < (int)(ZBYTES / 16)) *(uint4 *)(smem + ZBASE + 16 * tid) = ql::zero4();
   __syncthreads();
@@ -559,15 +667,26 @@ __global__ __launch_bounds__(GT) void nf4_gemv_kernel(GemvArgs g) {
 
   const uint32_t lcopy = 4u * (uint32_t)(lane & 31);
   const bool a_on = (n >> 2) == q;  // lane group q carries token rows 4q..4q+3
-  uint32_t abase[TP];
+  uint32_t abase[TP > 0 ? TP : 1];
 #pragma unroll
   for (int tp = 0; tp < TP; ++tp) abase[tp] = a_on ? xa_base(tp, q, n & 3) : ZBASE;
   if (has_b) {  // has_b implies has_a
-    const GUnit *const both[2] = {&ua, &ub};
-    unit_compute<DQ, TP, 2, QA>(g, both, smem, abase, lcopy, n, q, slice, issue);
+    if constexpr (TP == 0) {
+      GUnit *const both[2] = {&ua, &ub};
+      unit_compute16<DQ, 2, QA>(g, both, smem, lcopy, lane, slice, issue);
+      return;
+    } else {
+      const GUnit *const both[2] = {&ua, &ub};
+      unit_compute<DQ, TP, 2, QA>(g, both, smem, abase, lcopy, n, q, slice, issue);
+    }
   } else if (has_a) {
-    const GUnit *const one[1] = {&ua};
-    unit_compute<DQ, TP, 1, QA>(g, one, smem, abase, lcopy, n, q, slice, issue);
+    if constexpr (TP == 0) {
+      GUnit *const one[1] = {&ua};
+      unit_compute16<DQ, 1, QA>(g, one, smem, lcopy, lane, slice, issue);
+    } else {
+      const GUnit *const one[1] = {&ua};
+      unit_compute<DQ, TP, 1, QA>(g, one, smem, abase, lcopy, n, q, slice, issue);
+    }
   } else {
 #pragma unroll
     for (int c = 0; c < 4; ++c) issue(c);   // every code register gets its (clamped) load
@@ -1192,7 +1311,8 @@ static qlora_status launch_gemv(int nw, const GemvIn *in, int64_t k, const uint1
     const bool full = (k % (64 * GB)) == 0;
 #define QL_GEMV5(DQV, TPV, FV, QAV)                                            \
   if (ad)                                                                      \
-    nf4_gemv_kernel<DQV, TPV, FV, false, QAV, true><<<grid, GT, 0, st>>>(g);   \
+    nf4_gemv_kernel<DQV, (TPV < 3 ? TPV : 0), FV, false, QAV, true>            \
+        <<<grid, GT, 0, st>>>(g);                                              \
   else if (nw > 1)                                                             \
     nf4_gemv_kernel<DQV, TPV, FV, true, QAV, false><<<grid, GT, 0, st>>>(g);   \
   else                                                                         \
