@@ -87,7 +87,8 @@ qlora_status qlora_adapter_plan_build(const int32_t *ids, const qlora_adapter_pl
 
 size_t qlora_adapters_workspace_bytes(int32_t op, int64_t d, int64_t k, int64_t M, int32_t n,
                                       int32_t r) {
-  if (check_weight_shape(d, k) != QLORA_OK || !plan_shape_ok(M, n) || r < 1 || r > 128)
+  if (check_weight_shape(d, k) != QLORA_OK || !plan_shape_ok(M, n) ||
+      M > QLORA_MAX_ADAPTER_TOKENS || r < 1 || r > 128)
     return (size_t)-1;
   if (op == QLORA_OP_FWD) return (size_t)fwd_layout(nullptr, d, k, M, r).bytes;
   if (op == QLORA_OP_BWD)
@@ -106,6 +107,7 @@ qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight *w, const uint16_t
   if (!X || !Y || !aligned16(X) || !aligned16(Y) || !aligned16(H_save))
     return QLORA_ERR_INVALID_ARG;
   const int64_t d = w->d, k = w->k, M = plan->M;
+  if (M > QLORA_MAX_ADAPTER_TOKENS) return QLORA_ERR_UNSUPPORTED;
   const int r = ad->r, rp = (int)ql_rup(r, 16);
   const FwdWs L = fwd_layout((char *)ws, d, k, M, r);
   if (!ws_ok(ws, ws_bytes, L.bytes)) return QLORA_ERR_WORKSPACE;
@@ -136,6 +138,7 @@ qlora_status qlora_linear_bwd_adapters(const qlora_nf4_weight *w, const uint16_t
       !aligned16(dB) || !aligned16(dX) || !aligned16(H))
     return QLORA_ERR_INVALID_ARG;
   const int64_t d = w->d, k = w->k, M = plan->M;
+  if (M > QLORA_MAX_ADAPTER_TOKENS) return QLORA_ERR_UNSUPPORTED;
   const int r = ad->r, rp = (int)ql_rup(r, 16);
   const AdapterPlan p(plan->data, M, plan->n);
   const BwdWs L = bwd_layout((char *)ws, d, k, p, r);

@@ -500,6 +500,7 @@ __global__ __launch_bounds__(JT) void logprobs_grad_kernel(LpGradArgs g) {
 }
 
 constexpr int64_t kMaxV = (int64_t(1) << 31) - (1 << 16);
+constexpr int64_t kMaxThreads = 0xffffffff;   // of one launch
 
 qlora_status check_logits(const qlora_logits *x) {
   if (!x || x->N < 1 || x->V < 1 || x->ld < x->V || !x->data || !aligned16(x->data))
@@ -583,7 +584,7 @@ size_t qlora_token_logprobs_workspace_bytes(int64_t N, int64_t V, int32_t dtype,
       top > V || (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_F32))
     return (size_t)-1;
   const Split p = split_of(N, V, dtype == QLORA_DTYPE_F32);
-  if (N * p.nchunk > 0x7fffffff) return (size_t)-1;
+  if (N * p.nchunk * p.LT > kMaxThreads) return (size_t)-1;
   return p.nchunk == 1 ? 0 : (size_t)(N * p.nchunk) * (16 + 8 * (size_t)top);
 }
 
@@ -630,7 +631,7 @@ qlora_status qlora_token_logprobs_bwd(const qlora_logits *x, const int64_t *targ
   if (dentropy && !entropy) return QLORA_ERR_INVALID_ARG;
   const bool f32 = x->dtype == QLORA_DTYPE_F32;
   const int64_t nchunk = ql_cdiv(x->V, JT * LG_R * (f32 ? 4 : 8));
-  if (x->N * nchunk > 0x7fffffff) return QLORA_ERR_UNSUPPORTED;
+  if (x->N * nchunk * JT > kMaxThreads) return QLORA_ERR_UNSUPPORTED;
   const LpGradArgs g{x->data, x->N,    x->V,     x->ld,    dx->ld,   targets,
                      stats,   entropy, dlogprob, dentropy, dx->data, (int)nchunk};
   hipStream_t st = (hipStream_t)stream;

@@ -534,13 +534,14 @@ def _device_tensors(*named):
                              f"{tuple(shape)} on the device of {named[0][1]}")
     if dev != torch.cuda.current_device():
         raise ValueError(f"{named[0][1]} is on cuda:{dev}, not on the current device")
+    return dev
 
 
-def _same_device(t, name, named):
-    """``_device_tensors`` of named, and t on the same device."""
-    _device_tensors(*named)
-    if t.get_device() != named[0][0].get_device():
-        raise ValueError(f"{name} and {named[0][1]} must be on one device")
+def _beside(dev, *others):
+    """Every (tensor, name) is on device number dev."""
+    for t, name in others:
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev} like the call's other tensors")
 
 
 def _on(stream):
@@ -587,6 +588,8 @@ def adapter_plan(ids: torch.Tensor, n: int, out: AdapterPlan | None = None,
             out = AdapterPlan(M, n, torch.empty(nbytes, dtype=torch.uint8, device=ids.device))
     elif out.M != M or out.n != n:
         raise ValueError(f"out is a plan of {out.M} tokens and {out.n} adapters, not {M} and {n}")
+    else:
+        _beside(ids.get_device(), (out.data, "out"))
     c = out.c_struct()
     _check(lib().qlora_adapter_plan_build(ids.data_ptr(), ctypes.addressof(c), _stream(stream)),
            "qlora_adapter_plan_build")
@@ -610,15 +613,21 @@ def adapters_workspace(plan: AdapterPlan, d: int, k: int, r: int,
     return _workspace(b, plan.data.device, None)[0]
 
 
-def _adapter_args(w: NF4Weight, X, A, B, scale, plan: AdapterPlan):
+def _adapter_rank(A, plan: AdapterPlan) -> int:
     if A.dim() != 3:
         raise ValueError("A must be n x r x k")
-    n, r = A.shape[0], A.shape[1]
-    if plan.n != n:
-        raise ValueError(f"the plan is for {plan.n} adapters, A holds {n}")
-    _device_tensors((X, "X", torch.bfloat16, (plan.M, w.k)), (A, "A", torch.bfloat16, (n, r, w.k)),
-                    (B, "B", torch.bfloat16, (n, w.d, r)), (scale, "scale", torch.float32, (n,)))
-    return r, AdaptersC(n, r, A.data_ptr(), B.data_ptr(), scale.data_ptr())
+    if plan.n != A.shape[0]:
+        raise ValueError(f"the plan is for {plan.n} adapters, A holds {A.shape[0]}")
+    return A.shape[1]
+
+
+def _adapter_args(w: NF4Weight, X, A, B, scale, plan: AdapterPlan, r: int, ws, *more):
+    """Checks of a call's tensors (``more`` as in ``_device_tensors``); its adapters."""
+    n, k, bf = plan.n, w.k, torch.bfloat16
+    dev = _device_tensors((X, "X", bf, (plan.M, k)), (A, "A", bf, (n, r, k)),
+                          (B, "B", bf, (n, w.d, r)), (scale, "scale", torch.float32, (n,)), *more)
+    _beside(dev, (w.codes, "w"), (plan.data, "plan"), (ws, "ws"))
+    return AdaptersC(n, r, A.data_ptr(), B.data_ptr(), scale.data_ptr())
 
 
 def linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
@@ -628,7 +637,7 @@ def linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch
     """Y[m] = X[m] W'^T + s_a (X[m] A_a^T) B_a^T with a the adapter of token m
     in ``plan``: A (n x r x k), B (n x d x r) bf16, scale (n) float32 holding
     s_a. Returns (Y, H or None); H (M x r float32) is what the backward needs."""
-    r, ad = _adapter_args(w, X, A, B, scale, plan)
+    r = _adapter_rank(A, plan)
     if Y is None or ws is None or (save_h and H is None):
         with _on(stream):
             if Y is None:
@@ -637,12 +646,12 @@ def linear_fwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch
                 H = torch.empty(plan.M, r, dtype=torch.float32, device=X.device)
             if ws is None:
                 ws = adapters_workspace(plan, w.d, w.k, r)
+    y = (Y, "Y", torch.bfloat16, (plan.M, w.d))
     if save_h:
-        _device_tensors((Y, "Y", torch.bfloat16, (plan.M, w.d)),
-                        (H, "H", torch.float32, (plan.M, r)))
+        ad = _adapter_args(w, X, A, B, scale, plan, r, ws, y, (H, "H", torch.float32, (plan.M, r)))
     else:
         H = None
-        _device_tensors((Y, "Y", torch.bfloat16, (plan.M, w.d)))
+        ad = _adapter_args(w, X, A, B, scale, plan, r, ws, y)
     cw, cp = w.c_struct(), plan.c_struct()
     _check(lib().qlora_linear_fwd_adapters(ctypes.byref(cw), X.data_ptr(), ctypes.addressof(ad),
                                            ctypes.addressof(cp), Y.data_ptr(), _ptr(H),
@@ -658,7 +667,7 @@ def linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch
     """Backward of ``linear_fwd_adapters``: (dX or None, dA (n x r x k), dB
     (n x d x r)); adapters without tokens get zero gradients. H as the forward
     returned it, or None to recompute it."""
-    r, ad = _adapter_args(w, X, A, B, scale, plan)
+    r = _adapter_rank(A, plan)
     with _on(stream):
         if need_dx and dX is None:
             dX = torch.empty_like(X)
@@ -668,12 +677,13 @@ def linear_bwd_adapters(w: NF4Weight, X: torch.Tensor, A: torch.Tensor, B: torch
             dB = torch.empty_like(B)
         if ws is None:
             ws = adapters_workspace(plan, w.d, w.k, r, backward=True)
-    _device_tensors((dY, "dY", torch.bfloat16, (plan.M, w.d)), (dA, "dA", torch.bfloat16, A.shape),
-                    (dB, "dB", torch.bfloat16, B.shape))
+    more = [(dY, "dY", torch.bfloat16, (plan.M, w.d)), (dA, "dA", torch.bfloat16, A.shape),
+            (dB, "dB", torch.bfloat16, B.shape)]
     if need_dx:
-        _device_tensors((dX, "dX", torch.bfloat16, X.shape))
+        more.append((dX, "dX", torch.bfloat16, X.shape))
     if H is not None:
-        _device_tensors((H, "H", torch.float32, (plan.M, r)))
+        more.append((H, "H", torch.float32, (plan.M, r)))
+    ad = _adapter_args(w, X, A, B, scale, plan, r, ws, *more)
     cw, cp = w.c_struct(), plan.c_struct()
     _check(lib().qlora_linear_bwd_adapters(ctypes.byref(cw), X.data_ptr(), ctypes.addressof(ad),
                                            ctypes.addressof(cp), dY.data_ptr(), _ptr(H),
@@ -755,9 +765,14 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0,
     checks = ((targets, "targets", torch.int64, (N,)), (out.logprob, "out.logprob", f32, (N,)),
               (out.entropy, "out.entropy", f32, (N,)), (out.stats, "out.stats", f32, (N, 2)))
     if top:
+        if out.top_logprobs is None or out.top_ids is None:
+            raise ValueError(f"out has no top_logprobs and top_ids for top={top}")
         checks += ((out.top_logprobs, "out.top_logprobs", f32, (N, top)),
                    (out.top_ids, "out.top_ids", torch.int64, (N, top)))
-    _same_device(logits, "logits", checks)
+    dev = _device_tensors(*checks)
+    _beside(dev, (logits, "logits"))
+    if ws is not None:
+        _beside(dev, (ws, "ws"))
     _check(lib().qlora_token_logprobs(ctypes.addressof(c), targets.data_ptr(),
                                       out.logprob.data_ptr(), out.stats.data_ptr(),
                                       out.entropy.data_ptr(), top,
@@ -788,9 +803,7 @@ def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lp: TokenLog
               (dlogprob, "dlogprob", torch.float32, (N,)))
     if dentropy is not None:
         checks += ((dentropy, "dentropy", torch.float32, (N,)),)
-    _same_device(logits, "logits", checks)
-    if dlogits.get_device() != logits.get_device():
-        raise ValueError("dlogits must be on the device of logits")
+    _beside(_device_tensors(*checks), (logits, "logits"), (dlogits, "dlogits"))
     _check(lib().qlora_token_logprobs_bwd(ctypes.addressof(c), targets.data_ptr(),
                                           lp.stats.data_ptr(), lp.entropy.data_ptr(),
                                           dlogprob.data_ptr(), _ptr(dentropy),

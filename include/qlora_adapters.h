@@ -27,9 +27,11 @@
 extern "C" {
 #endif
 
-/* Largest adapter count of one call, and most tokens of one plan. */
+/* Largest adapter count of one call, most tokens of one plan, and most tokens
+ * of one linear (a launch of more threads than a grid holds otherwise). */
 #define QLORA_MAX_ADAPTERS 1024
 #define QLORA_MAX_PLAN_TOKENS ((int64_t)1 << 30)
+#define QLORA_MAX_ADAPTER_TOKENS ((int64_t)1 << 24)
 
 /*
  * The adapters of one linear: n adapters of r ranks each.
@@ -69,13 +71,16 @@ QLORA_API size_t qlora_adapter_plan_bytes(int64_t M, int32_t n);
 /*
  * Build the plan of ids [M] (int32, 4-byte aligned). Any id outside [0, n)
  * means no adapter. Tokens are ordered by adapter, tokens of one adapter in
- * batch order. One launch; `bytes` too small returns QLORA_ERR_WORKSPACE.
+ * batch order. One launch. M or n below 1 return QLORA_ERR_INVALID_ARG, above
+ * their limits QLORA_ERR_UNSUPPORTED, and `bytes` too small
+ * QLORA_ERR_WORKSPACE; the calls that take a plan check it the same way.
  */
 QLORA_API qlora_status qlora_adapter_plan_build(const int32_t *ids, const qlora_adapter_plan *plan,
                                                 void *stream);
 
 /* Device workspace of the calls below in bytes for op QLORA_OP_FWD or
- * QLORA_OP_BWD; (size_t)-1 for an unsupported shape. */
+ * QLORA_OP_BWD; (size_t)-1 for an unsupported shape (M above
+ * QLORA_MAX_ADAPTER_TOKENS is one, QLORA_ERR_UNSUPPORTED in the calls). */
 QLORA_API size_t qlora_adapters_workspace_bytes(int32_t op, int64_t d, int64_t k, int64_t M,
                                                 int32_t n, int32_t r);
 
@@ -84,7 +89,8 @@ QLORA_API size_t qlora_adapters_workspace_bytes(int32_t op, int64_t d, int64_t k
  * non-NULL it receives H[m] = X[m] A_a^T (M x r float32; zero rows for
  * tokens without an adapter) for the backward pass. M <= 16 runs the
  * memory-bound decode kernels, larger M the fused dequant-GEMM; both read
- * each touched adapter's matrices in place.
+ * each touched adapter's matrices in place. Adapter-input dropout (the
+ * qlora_dropout of qlora_nf4.h) is not offered here.
  */
 QLORA_API qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight *w, const uint16_t *X,
                                                  const qlora_adapters *adapters,

@@ -1,7 +1,8 @@
 /*
  * qlora_nf4_timing.h -- kernel timing of libqlora_nf4_timing.so, a
  * measurement build of the same sources as libqlora_nf4.so (identical
- * kernels and entry points, declared in qlora_nf4.h). It is not part of the
+ * kernels and entry points, declared in qlora_nf4.h, qlora_adapters.h and
+ * qlora_logprobs.h). It is not part of the
  * method and not in the product library: libqlora_nf4.so exports none of
  * these symbols and keeps no mutable host state.
  *

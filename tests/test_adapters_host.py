@@ -181,3 +181,36 @@ def test_host_tensors_are_refused():
         ops.token_logprobs(x, t)
     with pytest.raises(ValueError):
         ops.token_logprobs_bwd(x, t, ops.TokenLogprobs.empty(4, 0, "cpu"), torch.zeros(4))
+
+
+def test_linear_token_limit():
+    # a plan may hold more tokens than a linear takes
+    L, n = ops.lib(), 4
+    bad = ctypes.c_size_t(-1).value
+    fake = 0x100000   # aligned, never dereferenced: the calls are refused on the host
+    W = ops.NF4WeightC(64, 64, 64, 1, 256, 0, fake, None, fake, fake, fake)
+    a = ops.AdaptersC(n, 8, fake, fake, fake)
+    for op in (ops.OP_FWD, ops.OP_BWD):
+        assert L.qlora_adapters_workspace_bytes(op, 64, 64, 1 << 24, n, 8) != bad
+        assert L.qlora_adapters_workspace_bytes(op, 64, 64, (1 << 24) + 1, n, 8) == bad
+    p = ops.AdapterPlanC((1 << 24) + 1, n, 0, fake, 1 << 40)
+    args = (ctypes.addressof(a), ctypes.addressof(p))
+    assert L.qlora_linear_fwd_adapters(ctypes.byref(W), fake, *args, fake, fake, fake, 1 << 50,
+                                       None) == ops.QLORA_ERR_UNSUPPORTED
+    assert L.qlora_linear_bwd_adapters(ctypes.byref(W), fake, *args, fake, fake, fake, fake, fake,
+                                       fake, 1 << 50, None) == ops.QLORA_ERR_UNSUPPORTED
+
+
+def test_logprobs_thread_limit():
+    # rows whose workgroups would pass 2^32 threads are refused on the host
+    L = ops.lib()
+    bad = ctypes.c_size_t(-1).value
+    fake = 0x100000   # aligned, never dereferenced
+    for dt in (0, 1):
+        assert L.qlora_token_logprobs_workspace_bytes((1 << 24) - 1, 64, dt, 4) == 0
+        assert L.qlora_token_logprobs_workspace_bytes(1 << 24, 64, dt, 4) == bad
+        x = ops.LogitsC(fake, 1 << 24, 64, 64, dt, 0)
+        assert L.qlora_token_logprobs(ctypes.addressof(x), fake, fake, fake, fake, 0, None, None,
+                                      None, 0, None) == ops.QLORA_ERR_UNSUPPORTED
+        assert L.qlora_token_logprobs_bwd(ctypes.addressof(x), fake, fake, fake, fake, None,
+                                          ctypes.addressof(x), None) == ops.QLORA_ERR_UNSUPPORTED
