@@ -49,6 +49,15 @@
 // step, orders everything.
 // Workgroups are mapped XCD-aware: the 32 column tiles of one token block
 // land on the same XCD, whose L2 then holds that In block.
+//
+// Many adapters (the AD forms): the rows of a tile are plan positions, so a
+// tile holds runs of one adapter's tokens in place of a batch's consecutive
+// ones, and In and Out are addressed by token. Main loop and decode are the
+// same; the rank-r term at the end adds, run by run, that adapter's block of
+// B (or A) times the run's rows of S, each result column taken from the one
+// adapter its token has, so that values of other adapters do not reach it.
+// With few tiles S workgroups share a tile's K-steps and a second kernel joins
+// their sums in a fixed order.
 #include <type_traits>
 
 #include "kernels.h"

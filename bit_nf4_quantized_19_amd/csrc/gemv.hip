@@ -41,6 +41,9 @@
 //     while the codes stream in. Partial sums per slice go to a float32
 //     buffer; a second kernel adds the slices in a fixed order, the rank-r
 //     LoRA term in float32, and rounds to bf16.
+// Many adapters (the AD forms): the same partial sums of X W'^T; each token's
+// H is computed against its own adapter's A by workgroups of their own, and
+// an epilogue of its own reads each token's row of its own adapter's B.
 #include <algorithm>
 
 #include "kernels.h"

@@ -25,6 +25,13 @@
 //   * layout: the zero-padded and transposed copies of A and B the other
 //     kernels read (A^T for the dX epilogue, B^T for G), in one launch.
 // r is padded to rp (a multiple of 16) with zero rows/columns.
+//
+// Many adapters (the AD forms of skinny and colacc): a workgroup of skinny
+// takes up to 8 tokens of one adapter (a group of the batch's plan) and reads
+// that adapter's matrix only; a workgroup of colacc takes one split of one
+// adapter's tokens, a split adapter's sums joined as above, and an adapter
+// without tokens gets zeros. A tail of a group or split reads as zero rows, so
+// no other adapter's values enter a sum.
 #include <algorithm>
 
 #include "kernels.h"
