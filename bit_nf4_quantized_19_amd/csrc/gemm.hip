@@ -56,8 +56,9 @@
 // same; the rank-r term at the end adds, run by run, that adapter's block of
 // B (or A) times the run's rows of S, each result column taken from the one
 // adapter its token has, so that values of other adapters do not reach it.
-// With few tiles S workgroups share a tile's K-steps and a second kernel joins
-// their sums in a fixed order.
+// Tiles that do not fill the chip are split: S workgroups share a tile's
+// K-steps and a second kernel joins their sums in a fixed order.
+#include <algorithm>
 #include <type_traits>
 
 #include "kernels.h"
@@ -87,12 +88,14 @@ struct GemmArgs {
   const int *perm, *sid;
 };
 
-// Many adapters with few tiles: S workgroups (grid y) share a tile's K-steps
-// and leave their sums in part for the join kernel. Kept apart so that the
-// one-adapter kernels' arguments stay as they are.
+// Many adapters: the first `whole` tiles (in launch order) take a workgroup
+// each; of the others S workgroups each (split slow, tile fast) share the
+// K-steps and leave their sums in part for the join kernel. Kept apart so that
+// the one-adapter kernels' arguments stay as they are.
 struct GemmArgsAd : GemmArgs {
   int S;
-  float4 *part;   // [tile][S][16][NT]
+  uint32_t whole;
+  float4 *part;   // [tile past the whole ones][S][16][NT]
 };
 
 // LDS, one object per stage. The level table is the most aligned object, so
@@ -206,7 +209,7 @@ struct Tile {
   int64_t k0, nkt;    // AD: first K of this workgroup's steps; all steps (nk: its own)
 
   // tile (tm, tn): token rows tm*BM.., output columns tn*BN..
-  QL_DEV void init(const GemmArgs &ga, int64_t tm, int64_t tn, int S = 1) {
+  QL_DEV void init(const GemmArgs &ga, int64_t tm, int64_t tn, int y = 0, int S = 1) {
     g = ga;
     tid = threadIdx.x;
     lane = tid & 63;
@@ -220,8 +223,8 @@ struct Tile {
     nk = ql_cdiv(g.Ktot, BK);
     if (AD) {
       nkt = nk;
-      const int64_t lo = blockIdx.y * nkt / S;
-      nk = (blockIdx.y + 1) * nkt / S - lo;
+      const int64_t lo = y * nkt / S;
+      nk = (y + 1) * nkt / S - lo;
       k0 = lo * BK;
     }
     mu = DQ ? g.sc.mu[0] : 0.0f;
@@ -977,33 +980,54 @@ QL_DEV void tile_of(int64_t ntn, int64_t ntm, int64_t &tm, int64_t &tn) {
   tn = tile % ntn;
 }
 
+// The same for tile number u of the many-adapter launch. The column tiles'
+// second half takes the token blocks in reverse, so that an XCD with a token
+// block of many runs gets one of few.
+QL_DEV void adapter_tile_of(uint32_t u, uint32_t ntn, uint32_t ntm, int64_t &tm, int64_t &tn) {
+  const uint32_t total = ntn * ntm;
+  const uint32_t tile = (total & 7) == 0 ? (u & 7) * (total >> 3) + (u >> 3) : u;
+  tm = tile / ntn;
+  tn = tile % ntn;
+  if (2 * tn >= ntn) tm = ntm - 1 - tm;
+}
+
 template <int MODE, bool DQ, int AD>
 __global__ __launch_bounds__(NT, 1) void nf4_gemm_kernel(
     std::conditional_t<AD != 0, GemmArgsAd, GemmArgs> g) {
   if (threadIdx.x < 16) s_lv[threadIdx.x] = __uint_as_float(c_levels_g[threadIdx.x]);
   int64_t tm, tn;
-  tile_of(ql_cdiv(g.Ntot, BN), ql_cdiv(g.M, BM), tm, tn);
   Tile<MODE, DQ, AD> t;
-  // many adapters: the column tiles' second half takes the token blocks in
-  // reverse, so that an XCD with a token block of many runs gets one of few
-  if (AD && 2 * tn >= ql_cdiv(g.Ntot, BN)) tm = ql_cdiv(g.M, BM) - 1 - tm;
-  if constexpr (AD != 0)
-    t.init(g, tm, tn, g.S);
-  else
-    t.init(g, tm, tn);
-  __syncthreads();  // level table
-  t.run();
-  if constexpr (AD != 0)
-    if (g.S > 1) {   // the adapters' terms go into the splits' sums
-      t.adapter_terms(blockIdx.y, g.S);
-      t.publish(g.part + ((tm * ql_cdiv(g.Ntot, BN) + tn) * g.S + blockIdx.y) * 16 * NT);
+  if constexpr (AD != 0) {
+    const uint32_t ntn = (uint32_t)ql_cdiv(g.Ntot, BN), ntm = (uint32_t)ql_cdiv(g.M, BM);
+    uint32_t u = blockIdx.x, slot = 0;
+    int y = 0, S = 1;
+    if (u >= g.whole) {
+      const uint32_t rest = ntn * ntm - g.whole;
+      y = (int)((u - g.whole) / rest);
+      slot = (u - g.whole) % rest;
+      u = g.whole + slot;
+      S = g.S;
+    }
+    adapter_tile_of(u, ntn, ntm, tm, tn);
+    t.init(g, tm, tn, y, S);
+    __syncthreads();  // level table
+    t.run();
+    if (S > 1) {   // the adapters' terms go into the splits' sums
+      t.adapter_terms(y, S);
+      t.publish(g.part + ((int64_t)slot * S + y) * 16 * NT);
       return;
     }
+  } else {
+    tile_of(ql_cdiv(g.Ntot, BN), ql_cdiv(g.M, BM), tm, tn);
+    t.init(g, tm, tn);
+    __syncthreads();  // level table
+    t.run();
+  }
   t.epilogue();
 }
 
 // Split K: adds a tile's S partial sums in split order, rounds and stores
-// them; workgroup 4 tile + 2 i + j takes that 32 x 32 block of every wave's
+// them; workgroup 4 (tile - whole) + 2 i + j takes that 32 x 32 block of every wave's
 // eighth, all of a thread's loads in flight at once. The sums are handed over
 // by a kernel boundary because the XCDs' L2s are not coherent: with the tile's
 // last workgroup adding them inside the GEMM (agent-scope 8-byte stores) the
@@ -1014,7 +1038,9 @@ __global__ __launch_bounds__(NT) void nf4_gemm_join_kernel(GemmArgsAd g) {
   const int wn = wave & 1, wm = wave >> 1;
   const int64_t tile = blockIdx.x >> 2;
   const int i = (blockIdx.x >> 1) & 1, j = blockIdx.x & 1;
-  const int64_t tn = tile % ql_cdiv(g.Ntot, BN), tm = tile / ql_cdiv(g.Ntot, BN);
+  int64_t tm, tn;
+  adapter_tile_of(g.whole + (uint32_t)tile, (uint32_t)ql_cdiv(g.Ntot, BN),
+                  (uint32_t)ql_cdiv(g.M, BM), tm, tn);
   const int64_t p = tm * BM + wm * 64 + 32 * j + r32;
   const int64_t n = tn * BN + wn * 64 + 32 * i + 4 * h;
   if (p >= g.M) return;
@@ -1052,7 +1078,14 @@ static void launch_join(const GemmArgsAd &g, unsigned tiles, hipStream_t st) {
   }
 }
 
+struct AdapterSplit {
+  int64_t whole;   // tiles with a workgroup of their own, the first of the launch
+  int S;           // workgroups of each other tile
+};
+
 }  // namespace
+
+static AdapterSplit gemm_adapter_split(int64_t M, int64_t Ntot, int64_t Ktot);
 
 static qlora_status launch_gemm(int mode, const GemmArgs &ga, const GemmAdapters *ad,
                                 hipStream_t st) {
@@ -1078,10 +1111,13 @@ static qlora_status launch_gemm(int mode, const GemmArgs &ga, const GemmAdapters
   (GemmArgs &)g = ga;
   g.perm = ad->perm;
   g.sid = ad->sid;
-  g.S = gemm_adapter_splits(g.M, g.Ntot, g.Ktot);
+  const AdapterSplit sp = gemm_adapter_split(g.M, g.Ntot, g.Ktot);
+  g.S = sp.S;
+  g.whole = (uint32_t)sp.whole;
+  const unsigned split = (unsigned)(tiles - sp.whole);   // tiles that are split
   g.part = (float4 *)ad->part;
 #define QL_GEMM(MODEV, DQV, ADV) \
-  nf4_gemm_kernel<MODEV, DQV, ADV><<<dim3(grid, (unsigned)g.S), NT, 0, st>>>(g);
+  nf4_gemm_kernel<MODEV, DQV, ADV><<<(unsigned)sp.whole + split * sp.S, NT, 0, st>>>(g);
 #define QL_GEMM_AD(MODEV, DQV)                                                  \
   if (MODEV == 1 || g.r % 8 == 0) {                                             \
     if (g.rp == 16) { QL_GEMM(MODEV, DQV, 1) } else { QL_GEMM(MODEV, DQV, 4) }  \
@@ -1095,39 +1131,45 @@ static qlora_status launch_gemm(int mode, const GemmArgs &ga, const GemmAdapters
   }
 #undef QL_GEMM_AD
 #undef QL_GEMM
-  if (g.S > 1) launch_join(g, grid, st);
+  if (split) launch_join(g, split, st);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
 
-// Workgroups per tile: the count with the least time by what was measured, in
-// 10 ns. A workgroup takes its K-steps plus four for its start and end; a step
-// takes 0.92 us while up to 0.6 of the 256 compute units work and 1.25 us when
-// all do; a split adds 5 us for the join and the partial sums' bytes, written
-// and read, at 6 TB/s. Measured forward times (4096 x 4096, r = 16, eight
-// adapters; one workgroup a tile / the chosen split): 64 tokens 66 / 31 us,
-// 512 69 / 41, 1024 69 / 60; 4096 x 11008, 777 tokens 166 / 115; a split of
-// 2048 tokens would take 111 us instead of 90.
-int gemm_adapter_splits(int64_t M, int64_t Ntot, int64_t Ktot) {
+// Which tiles are split over K and into how many workgroups: none, those past
+// the last full round of the 256 compute units, or all, by the least time of
+// what was measured, in 10 ns. A workgroup takes its K-steps plus four for its
+// start and end; a step takes 0.92 us while up to 0.6 of the compute units
+// work and 1.25 us when all do; a split adds 5 us for the join and the partial
+// sums' bytes, written and read, at 6 TB/s. Measured forward times (4096 x
+// 4096, r = 16, eight adapters; one workgroup a tile / the chosen split): 64
+// tokens 66 / 31 us, 512 69 / 41, 1024 69 / 60; 4096 x 11008, 777 tokens 166 /
+// 115; a split of 2048 tokens would take 111 us instead of 90. Tiles past the
+// last full round alone: 4096 x 4096, 2304 tokens 157 / 121 us; 5120 x 5120,
+// 1800 tokens 175 / 150; backward of 4096 x 11008, 777 tokens 185 / 159.
+static AdapterSplit gemm_adapter_split(int64_t M, int64_t Ntot, int64_t Ktot) {
   const int64_t tn = ql_cdiv(Ntot, BN), tiles = tn * ql_cdiv(M, BM), nk = ql_cdiv(Ktot, BK);
-  int best = 1;
+  const int64_t full = tiles / 256 * 256;
+  AdapterSplit best{tiles, 1};
   int64_t least = 0;
-  for (const int S : {1, 2, 3, 4, 6, 8}) {   // those launch_join knows
-    if (S > nk) break;
-    const int64_t steps = ql_cdiv(nk, S) + 4, rounds = tiles * S / 256, rest = tiles * S % 256;
-    int64_t t = rounds * steps * 125;
-    if (rest) t += steps * (rest <= 154 ? 92 : 92 + (rest - 154) * 33 / 102);
-    if (S > 1) t += 500 + S * tn * M / 59;
-    if (S == 1 || t < least) {
-      least = t;
-      best = S;
+  for (const int64_t whole : {full, (int64_t)0})
+    for (const int S : {1, 2, 3, 4, 6, 8}) {   // those launch_join knows
+      const int64_t rest = tiles - whole;
+      if (S > nk || (rest == 0 && S > 1)) break;
+      const int64_t wgs = rest * S, steps = ql_cdiv(nk, S) + 4, last = wgs % 256;
+      int64_t t = whole / 256 * (nk + 4) * 125 + wgs / 256 * steps * 125;
+      if (last) t += steps * (last <= 154 ? 92 : 92 + (last - 154) * 33 / 102);
+      if (S > 1) t += 500 + S * std::min(tn * M, rest * BM) / 59;
+      if (least == 0 || t < least) {
+        least = t;
+        best = S == 1 ? AdapterSplit{tiles, 1} : AdapterSplit{whole, S};
+      }
     }
-  }
   return best;
 }
 size_t gemm_adapter_part_bytes(int64_t M, int64_t Ntot, int64_t Ktot) {
-  const int S = gemm_adapter_splits(M, Ntot, Ktot);
-  return S == 1 ? 0 : (size_t)(ql_cdiv(Ntot, BN) * ql_cdiv(M, BM) * S) * BN * BM * 4;
+  const AdapterSplit sp = gemm_adapter_split(M, Ntot, Ktot);
+  return (size_t)((ql_cdiv(Ntot, BN) * ql_cdiv(M, BM) - sp.whole) * sp.S) * BN * BM * 4;
 }
 
 qlora_status launch_gemm_fwd(const uint8_t *codes, ql::ScaleSrc sc, int64_t d, int64_t k,

@@ -156,7 +156,6 @@ struct GemmAdapters {
   const int *perm, *sid;   // of the plan
   void *part;              // gemm_adapter_part_bytes(M, Ntot, Ktot), 256-byte aligned
 };
-int gemm_adapter_splits(int64_t M, int64_t Ntot, int64_t Ktot);
 size_t gemm_adapter_part_bytes(int64_t M, int64_t Ntot, int64_t Ktot);
 qlora_status launch_gemm_fwd(const uint8_t *codes, ql::ScaleSrc sc, int64_t d,
                              int64_t k, const uint16_t *X, int64_t M,

@@ -1,13 +1,13 @@
 """Many adapters and token log probabilities where calls meet or sizes grow:
-matrices past 2^32 bytes, two streams at once on one plan, outputs that lack
-what was asked. Bounds as in test_gpu_adapters.py: sums of c exact products
+matrices past 2^32 bytes, tiles past the last full round, two streams at once
+on one plan, outputs that lack what was asked. Bounds as in test_gpu_adapters.py: sums of c exact products
 off by at most c 2^-24 of their magnitudes, high and low parts by 2^-16,
 outputs rounded once (2^-8)."""
 
 import numpy as np
 import pytest
 
-from _helpers import bf16_f64, to_host_bits
+from _helpers import (bf16_f64, oracle_quant, oracle_wdeq, rel_frob, to_dev, to_host_bits)
 from bit_nf4_quantized_19_amd import synth
 from oracle import adapters as oad
 
@@ -96,6 +96,38 @@ def test_offsets_past_32_bits(ops):
         p = ops.adapter_plan(ids[rt[-m:]].contiguous(), n)
         Y, _ = ops.linear_fwd_adapters(w, x[-m:].contiguous(), A, B, scale, p)
         within(bits(Y), Yw[-m:], tY[-m:], ("decode", m))
+
+
+@pytest.mark.parametrize("d,k,M,n,r", [(2048, 11008, 777, 5, 12), (11008, 2176, 800, 6, 40)])
+def test_tiles_past_the_last_full_round(ops, d, k, M, n, r):
+    # 344 tiles (of dX; of Y) for 256 compute units: some whole, the rest split
+    print(f"[adapters rounds] d={d} k={k} M={M} n={n} r={r}", flush=True)
+    rng = np.random.default_rng(M)
+    bf = lambda shape, scale, seed: synth.normal_bf16(shape, scale, seed)   # noqa: E731
+    W0, X, dY = bf((d, k), 0.02, 1), bf((M, k), 1.0, 2), bf((M, d), 1.0, 3)
+    A, B = bf((n, r, k), k ** -0.5, 4), bf((n, d, r), 0.1, 5)
+    s, ids = rng.uniform(0.25, 4.0, n).astype(np.float32), rng.integers(-1, n, M)
+    Wd = oracle_wdeq(oracle_quant(W0, True), d, k)
+    f = [bf16_f64(v) for v in (X, A, B, dY)]
+    Yw, _ = oad.forward(Wd, f[0], f[1], f[2], s.astype(np.float64), ids)
+    dXw, dAw, dBw = oad.backward(Wd, f[0], f[1], f[2], s.astype(np.float64), ids, f[3])
+    gX, gA, gB, gY = (to_dev(v) for v in (X, A, B, dY))
+    gs, gi = torch.from_numpy(s).cuda(), torch.from_numpy(ids.astype(np.int32)).cuda()
+    w, plan = ops.quantize(to_dev(W0), True), ops.adapter_plan(gi, n)
+    first = None
+    for _ in range(2):
+        Y, H = ops.linear_fwd_adapters(w, gX, gA, gB, gs, plan)
+        got = (Y,) + ops.linear_bwd_adapters(w, gX, gA, gB, gs, plan, gY, H=H)
+        torch.cuda.synchronize()
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+    for name, g, want in zip(("Y", "dX", "dA", "dB"), got, (Yw, dXw, dAw, dBw)):
+        assert rel_frob(bits(g), want) <= 2e-2, name
+    for g, want in ((bits(got[0]), Yw), (bits(got[1]), dXw)):
+        row = np.sqrt(((g - want) ** 2).sum(1) / (want ** 2).sum(1))
+        assert row.max() <= 2e-2
+        for c in range(0, want.shape[1], 128):   # a tile's columns
+            assert rel_frob(g[:, c:c + 128], want[:, c:c + 128]) <= 2e-2, c
 
 
 @pytest.mark.parametrize("M", [9, 14, 300])
