@@ -315,10 +315,11 @@ QL_DEV void unit_compute(const GemvArgs &g, const GUnit *const (&us)[NU],
 // then give a block's sums D[4q + i][n], which every lane scales (a lane reads
 // the codes of all its row's scales anyway). X is held in the same upper
 // halves of the table rows, one read's 64 pieces consecutive.
-// Measured with r = 16, the layout above -> this one: sixteen tokens 12.3 ->
-// 11.6 us (4096 x 4096), 17.0 -> 15.0 (11008 x 4096), 23.5 -> 19.9
-// (4096 x 11008); with eight it loses, 10.8 -> 11.3, 13.3 -> 13.7 and
-// 18.7 -> 19.5, so the layout above serves up to eight.
+// Measured with r = 16, the layout above -> this one: sixteen tokens 12.1 ->
+// 10.9 us (4096 x 4096), 17.2 -> 14.2 (11008 x 4096), 17.4 -> 14.0
+// (4096 x 11008); with four it loses, 9.7 -> 10.5, 10.8 -> 11.7 and 11.9 ->
+// 12.9, and with eight, 10.1 -> 10.5, 12.9 -> 12.9 and 14.0 -> 13.5, it mostly
+// does not gain, so the layout above serves up to eight.
 QL_DEV uint32_t x16_addr(int m, int b, int sc8) {   // X[m][64 b + 8 sc8 ..] of the slice
   const int piece = m + 16 * (sc8 >> 1);
   return (uint32_t)(((b * 2 + (sc8 & 1)) * 8 + (piece >> 3)) * 256 + 128 + (piece & 7) * 16);
@@ -561,7 +562,7 @@ QL_DEV void adapter_down(const uint16_t *X, const uint16_t *A, const GemvAd &ad,
 // w + GW, both loaded before the table is built, then computed together. The
 // table and the X slice are built once per workgroup.
 // AD: the workgroups past the G of a slice compute the H partials of the
-// tokens' own adapters instead (M rp / 16 of them). TP == 0: the layout of
+// tokens' own adapters instead (M rp / 16 of them, in turn). TP == 0: the layout of
 // unit_compute16 (with AD, for more than eight tokens).
 template <bool DQ, int TP, bool FULL, bool GRP, bool QA, bool AD>
 __global__ __launch_bounds__(GT) void nf4_gemv_kernel(GemvArgs g) {
@@ -571,8 +572,8 @@ __global__ __launch_bounds__(GT) void nf4_gemv_kernel(GemvArgs g) {
   const int64_t nbr = g.k >> 6;
   const int64_t slice = blockIdx.y;
   if (AD && (int)blockIdx.x >= g.G) {
-    adapter_down<GB>(g.X, g.w[0].Ap, g.ad, g.k, g.M, g.rp, g.w[0].hpart, (int)blockIdx.x - g.G,
-                     slice, wave, lane);
+    for (int h = (int)blockIdx.x - g.G; h < (int)g.M * (g.rp / 16); h += (int)gridDim.x - g.G)
+      adapter_down<GB>(g.X, g.w[0].Ap, g.ad, g.k, g.M, g.rp, g.w[0].hpart, h, slice, wave, lane);
     return;
   }
   const int64_t b0 = slice * GB;
@@ -1291,8 +1292,18 @@ static qlora_status launch_gemv(int nw, const GemvIn *in, int64_t k, const uint1
   }
   // about one workgroup per compute unit, each slice served by G of them,
   // and at most two row groups per wave
-  const int64_t G = std::min<int64_t>(
-      ngroups, std::max<int64_t>(std::max<int64_t>(1, ncu / S), ql_cdiv(ngroups, 2 * GW)));
+  const int64_t per = std::max<int64_t>(1, ncu / S), least = ql_cdiv(ngroups, 2 * GW);
+  // Adapters: a slice's H workgroups count among its units, so that no second
+  // round follows; where H's pieces do not fit beside the fewest row workgroups,
+  // an H workgroup takes up to four of them in turn. Against one workgroup a
+  // piece on top of a full round, r = 16, 4 / 8 / 16 tokens: 4096 x 4096 12.5 /
+  // 11.0 / 11.6 -> 9.7 / 10.1 / 10.9 us, 4096 x 11008 14.7 / 18.7 / 19.5 -> 12.0
+  // / 14.0 / 14.0. Where the row workgroups alone need more than a round
+  // (8192 x 22016) every piece keeps its own: 36 us at sixteen tokens, 39 in turn.
+  const int64_t nh = ad ? M * (rp / 16) : 0;
+  const int64_t nhw =
+      per < least ? nh : std::min(nh, std::max(per - least, ql_cdiv(nh, 4)));
+  const int64_t G = std::min(ngroups, std::max<int64_t>(std::max<int64_t>(1, per - nhw), least));
   const int64_t rpw = ql_cdiv(ngroups, G);
   if (S > 65535 || G > (int64_t(1) << 30) || eblocks > 0x7fffffff) return QLORA_ERR_UNSUPPORTED;
   if (ad) g.ad = *ad;
@@ -1306,7 +1317,7 @@ static qlora_status launch_gemv(int nw, const GemvIn *in, int64_t k, const uint1
   g.part = part;
   g.dtot = dtot;
   g.rp = rp;
-  dim3 grid((unsigned)(G + (ad ? M * (rp / 16) : 0)), (unsigned)S);
+  dim3 grid((unsigned)(G + nhw), (unsigned)S);
   {
     QlProf prof(QLORA_K_GEMV, st);
     const int tp = (int)ql_cdiv(M, 4);
