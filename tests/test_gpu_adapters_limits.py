@@ -130,6 +130,33 @@ def test_tiles_past_the_last_full_round(ops, d, k, M, n, r):
             assert rel_frob(g[:, c:c + 128], want[:, c:c + 128]) <= 2e-2, c
 
 
+@pytest.mark.parametrize("d,k,M,n,r", [
+    (1024, 11008, 16, 5, 64),      # H's pieces taken in turn, a last turn not full
+    (1024, 11008, 8, 3, 128),
+    (2912, 22016, 11, 4, 16),      # row workgroups of more than one round
+    (2912, 22016, 5, 4, 40)])
+def test_decode_h_workgroups(ops, d, k, M, n, r):
+    print(f"[adapters decode] d={d} k={k} M={M} n={n} r={r}", flush=True)
+    rng = np.random.default_rng(M)
+    W0, X = synth.normal_bf16((d, k), 0.02, 1), synth.normal_bf16((M, k), 1.0, 2)
+    A, B = synth.normal_bf16((n, r, k), k ** -0.5, 3), synth.normal_bf16((n, d, r), 0.1, 4)
+    s, ids = rng.uniform(0.25, 4.0, n).astype(np.float32), rng.integers(-1, n, M)
+    gi = torch.from_numpy(ids.astype(np.int32)).cuda()
+    w, plan = ops.quantize(to_dev(W0), True), ops.adapter_plan(gi, n)
+    H = torch.full((M, r), float("nan"), device="cuda")
+    Y, H = ops.linear_fwd_adapters(w, to_dev(X), to_dev(A), to_dev(B), torch.from_numpy(s).cuda(),
+                                   plan, H=H)
+    torch.cuda.synchronize()
+    Wd = oracle_wdeq(oracle_quant(W0, True), d, k)
+    x, a, b = bf16_f64(X), bf16_f64(A), bf16_f64(B)
+    Yw, Hw = oad.forward(Wd, x, a, b, s.astype(np.float64), ids)
+    Ha = oad.forward(np.zeros((d, k)), abs(x), abs(a), abs(b), s.astype(np.float64), ids)[1]
+    assert (abs(H.cpu().numpy() - Hw) <= 2 * k * U24 * Ha).all()
+    got = bits(Y)
+    for m in range(M):
+        assert rel_frob(got[m], Yw[m]) <= 2e-2, m
+
+
 @pytest.mark.parametrize("M", [9, 14, 300])
 def test_two_streams_share_a_plan(ops, M):
     # two linears of one batch at once, each with its own workspace, on one plan
