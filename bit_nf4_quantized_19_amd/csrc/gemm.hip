@@ -88,14 +88,14 @@ struct GemmArgs {
   const int *perm, *sid;
 };
 
-// Many adapters: the first `whole` tiles (in launch order) take a workgroup
-// each; of the others S workgroups each (split slow, tile fast) share the
-// K-steps and leave their sums in part for the join kernel. Kept apart so that
-// the one-adapter kernels' arguments stay as they are.
+// Many adapters: the tiles of the first `whole` tile columns take a workgroup
+// each and come first in the launch; of the others S workgroups each (split
+// slow, tile fast) share the K-steps and leave their sums in part for the join
+// kernel. Kept apart so that the one-adapter kernels' arguments stay as they are.
 struct GemmArgsAd : GemmArgs {
   int S;
   uint32_t whole;
-  float4 *part;   // [tile past the whole ones][S][16][NT]
+  float4 *part;   // [tile of the columns past the whole ones][S][16][NT]
 };
 
 // LDS, one object per stage. The level table is the most aligned object, so
@@ -978,15 +978,20 @@ QL_DEV void tile_of(int64_t ntn, int64_t ntm, int64_t &tm, int64_t &tn) {
   tn = tile % ntn;
 }
 
-// The same for tile number u of the many-adapter launch. The column tiles'
-// second half takes the token blocks in reverse, so that an XCD with a token
-// block of many runs gets one of few.
-QL_DEV void adapter_tile_of(uint32_t u, uint32_t ntn, uint32_t ntm, int64_t &tm, int64_t &tn) {
-  const uint32_t total = ntn * ntm;
-  const uint32_t tile = (total & 7) == 0 ? (u & 7) * (total >> 3) + (u >> 3) : u;
-  tm = tile / ntn;
-  tn = tile % ntn;
-  if (2 * tn >= ntn) tm = ntm - 1 - tm;
+// The same for tile number u of the many-adapter launch's whole tile columns,
+// or of those that are split: ncol columns from c0 on, dealt to the XCDs in
+// eight parts as equal as their number allows (in launch order where it is not
+// a multiple of eight: backward of 2500 tokens at 11008 x 4096, 250 whole tiles
+// and 70 split, 327 -> 333 us). The columns' second half takes the token blocks
+// in reverse, so that an XCD with a token block of many runs gets one of few.
+QL_DEV void adapter_tile_of(uint32_t u, uint32_t c0, uint32_t ncol, uint32_t ntm, int64_t &tm,
+                            int64_t &tn) {
+  const uint32_t total = ncol * ntm;
+  const uint32_t x = u & 7, tile = x * (total >> 3) + min(x, total & 7) + (u >> 3);
+  tm = tile / ncol;
+  tn = tile % ncol;
+  if (2 * tn >= ncol) tm = ntm - 1 - tm;
+  tn += c0;
 }
 
 template <int MODE, bool DQ, int AD>
@@ -997,16 +1002,17 @@ __global__ __launch_bounds__(NT, 1) void nf4_gemm_kernel(
   Tile<MODE, DQ, AD> t;
   if constexpr (AD != 0) {
     const uint32_t ntn = (uint32_t)ql_cdiv(g.Ntot, BN), ntm = (uint32_t)ql_cdiv(g.M, BM);
-    uint32_t u = blockIdx.x, slot = 0;
+    const uint32_t nwhole = g.whole * ntm;
+    uint32_t slot = blockIdx.x, c0 = 0, ncol = g.whole;
     int y = 0, S = 1;
-    if (u >= g.whole) {
-      const uint32_t rest = ntn * ntm - g.whole;
-      y = (int)((u - g.whole) / rest);
-      slot = (u - g.whole) % rest;
-      u = g.whole + slot;
+    if (slot >= nwhole) {
+      c0 = g.whole;
+      ncol = ntn - g.whole;
+      y = (int)((slot - nwhole) / (ncol * ntm));
+      slot = (slot - nwhole) % (ncol * ntm);
       S = g.S;
     }
-    adapter_tile_of(u, ntn, ntm, tm, tn);
+    adapter_tile_of(slot, c0, ncol, ntm, tm, tn);
     t.init(g, tm, tn, y, S);
     __syncthreads();  // level table
     t.run();
@@ -1025,8 +1031,7 @@ __global__ __launch_bounds__(NT, 1) void nf4_gemm_kernel(
 }
 
 // Split K: adds a tile's S partial sums in split order, rounds and stores
-// them; workgroup 4 (tile - whole) + 2 i + j takes that 32 x 32 block of every wave's
-// eighth, all of a thread's loads in flight at once. The sums are handed over
+// them; workgroup 4 slot + 2 i + j takes that 32 x 32 block of every wave's eighth, all of a thread's loads in flight at once. The sums are handed over
 // by a kernel boundary because the XCDs' L2s are not coherent: with the tile's
 // last workgroup adding them inside the GEMM (agent-scope 8-byte stores) the
 // hand-over cost 25 to 40 us at 32 to 128 tiles.
@@ -1037,7 +1042,7 @@ __global__ __launch_bounds__(NT) void nf4_gemm_join_kernel(GemmArgsAd g) {
   const int64_t tile = blockIdx.x >> 2;
   const int i = (blockIdx.x >> 1) & 1, j = blockIdx.x & 1;
   int64_t tm, tn;
-  adapter_tile_of(g.whole + (uint32_t)tile, (uint32_t)ql_cdiv(g.Ntot, BN),
+  adapter_tile_of((uint32_t)tile, g.whole, (uint32_t)ql_cdiv(g.Ntot, BN) - g.whole,
                   (uint32_t)ql_cdiv(g.M, BM), tm, tn);
   const int64_t p = tm * BM + wm * 64 + 32 * j + r32;
   const int64_t n = tn * BN + wn * 64 + 32 * i + 4 * h;
@@ -1077,7 +1082,7 @@ static void launch_join(const GemmArgsAd &g, unsigned tiles, hipStream_t st) {
 }
 
 struct AdapterSplit {
-  int64_t whole;   // tiles with a workgroup of their own, the first of the launch
+  int64_t whole;   // tile columns whose tiles have a workgroup of their own
   int S;           // workgroups of each other tile
 };
 
@@ -1112,10 +1117,11 @@ static qlora_status launch_gemm(int mode, const GemmArgs &ga, const GemmAdapters
   const AdapterSplit sp = gemm_adapter_split(g.M, g.Ntot, g.Ktot);
   g.S = sp.S;
   g.whole = (uint32_t)sp.whole;
-  const unsigned split = (unsigned)(tiles - sp.whole);   // tiles that are split
+  const unsigned whole = (unsigned)(sp.whole * ql_cdiv(g.M, BM));   // workgroups of whole tiles
+  const unsigned split = grid - whole;                              // tiles that are split
   g.part = (float4 *)ad->part;
 #define QL_GEMM(MODEV, DQV, ADV) \
-  nf4_gemm_kernel<MODEV, DQV, ADV><<<(unsigned)sp.whole + split * sp.S, NT, 0, st>>>(g);
+  nf4_gemm_kernel<MODEV, DQV, ADV><<<whole + split * sp.S, NT, 0, st>>>(g);
 #define QL_GEMM_AD(MODEV, DQV)                                                  \
   if (MODEV == 1 || g.r % 8 == 0) {                                             \
     if (g.rp == 16) { QL_GEMM(MODEV, DQV, 1) } else { QL_GEMM(MODEV, DQV, 4) }  \
@@ -1136,38 +1142,42 @@ static qlora_status launch_gemm(int mode, const GemmArgs &ga, const GemmAdapters
 
 // Which tiles are split over K and into how many workgroups: none, those past
 // the last full round of the 256 compute units, or all, by the least time of
-// what was measured, in 10 ns. A workgroup takes its K-steps plus four for its
+// what was measured, in 10 ns. Whole or split goes by the tile's columns, not
+// its tokens, so that a token's sums are taken in the same order wherever the
+// batch puts it (a full round can then fall short of 256 tiles: by up to 6%
+// slower than the first 256 tiles whatever their columns, 141 -> 149 us for
+// 10000 tokens at 1000 x 4096). A workgroup takes its K-steps plus four for its
 // start and end; a step takes 0.92 us while up to 0.6 of the compute units
 // work and 1.25 us when all do; a split adds 5 us for the join and the partial
 // sums' bytes, written and read, at 6 TB/s. Measured forward times (4096 x
 // 4096, r = 16, eight adapters; one workgroup a tile / the chosen split): 64
 // tokens 66 / 31 us, 512 69 / 41, 1024 69 / 60; 4096 x 11008, 777 tokens 166 /
-// 115; a split of 2048 tokens would take 111 us instead of 90. Tiles past the
-// last full round alone: 4096 x 4096, 2304 tokens 157 / 121 us; 5120 x 5120,
+// 115; a split of 2048 tokens would take 111 us instead of 90. The columns past
+// the last full round alone: 4096 x 4096, 2304 tokens 157 / 123 us; 5120 x 5120,
 // 1800 tokens 175 / 150; backward of 4096 x 11008, 777 tokens 185 / 159.
 static AdapterSplit gemm_adapter_split(int64_t M, int64_t Ntot, int64_t Ktot) {
-  const int64_t tn = ql_cdiv(Ntot, BN), tiles = tn * ql_cdiv(M, BM), nk = ql_cdiv(Ktot, BK);
-  const int64_t full = tiles / 256 * 256;
-  AdapterSplit best{tiles, 1};
+  const int64_t tn = ql_cdiv(Ntot, BN), tm = ql_cdiv(M, BM), nk = ql_cdiv(Ktot, BK);
+  const int64_t full = tn * tm / 256 * 256 / tm;   // columns of the full rounds
+  AdapterSplit best{tn, 1};
   int64_t least = 0;
-  for (const int64_t whole : {full, (int64_t)0})
+  for (const int64_t cols : {full, (int64_t)0})
     for (const int S : {1, 2, 3, 4, 6, 8}) {   // those launch_join knows
-      const int64_t rest = tiles - whole;
+      const int64_t whole = cols * tm, rest = (tn - cols) * tm;
       if (S > nk || (rest == 0 && S > 1)) break;
       const int64_t wgs = rest * S, steps = ql_cdiv(nk, S) + 4, last = wgs % 256;
-      int64_t t = whole / 256 * (nk + 4) * 125 + wgs / 256 * steps * 125;
+      int64_t t = ql_cdiv(whole, 256) * (nk + 4) * 125 + wgs / 256 * steps * 125;
       if (last) t += steps * (last <= 154 ? 92 : 92 + (last - 154) * 33 / 102);
       if (S > 1) t += 500 + S * std::min(tn * M, rest * BM) / 59;
       if (least == 0 || t < least) {
         least = t;
-        best = S == 1 ? AdapterSplit{tiles, 1} : AdapterSplit{whole, S};
+        best = S == 1 ? AdapterSplit{tn, 1} : AdapterSplit{cols, S};
       }
     }
   return best;
 }
 size_t gemm_adapter_part_bytes(int64_t M, int64_t Ntot, int64_t Ktot) {
   const AdapterSplit sp = gemm_adapter_split(M, Ntot, Ktot);
-  return (size_t)((ql_cdiv(Ntot, BN) * ql_cdiv(M, BM) - sp.whole) * sp.S) * BN * BM * 4;
+  return (size_t)((ql_cdiv(Ntot, BN) - sp.whole) * ql_cdiv(M, BM) * sp.S) * BN * BM * 4;
 }
 
 qlora_status launch_gemm_fwd(const uint8_t *codes, ql::ScaleSrc sc, int64_t d, int64_t k,

@@ -16,7 +16,10 @@
  * outputs do not alias inputs, bit-identical results on every call), and one
  * more: the values of a token depend on its own row and its own adapter
  * only. An infinity or NaN in another token's row or another adapter's
- * matrices does not reach it.
+ * matrices does not reach it, and among batches of the same M a token's H, Y
+ * and dX are a function, bit for bit, of its row, its adapter and the adapter's
+ * number, wherever the token stands and whatever the others use. Batches of
+ * other sizes may add in another order.
  */
 #ifndef QLORA_ADAPTERS_H
 #define QLORA_ADAPTERS_H
