@@ -81,3 +81,79 @@ def test_whole_and_split_columns_against_the_oracle(ops, d, k, M, n, r):
         assert row.max() <= 2e-2, name
         for c in range(0, want.shape[1], 128):
             assert rel_frob(g[:, c:c + 128], want[:, c:c + 128]) <= 2e-2, (name, c)
+
+
+SPLIT = [(1024, 768, 300, 5, 16), (1024, 1024, 700, 6, 40), (6912, 768, 1200, 5, 8)]
+
+
+@pytest.mark.parametrize("d,k,M,n,r", SPLIT)
+def test_infinities_stay_with_their_token_and_adapter(ops, d, k, M, n, r):
+    print(f"[adapters alone] d={d} k={k} M={M} n={n} r={r}", flush=True)
+    t = inputs(d, k, M, n, r, "mixed", 41, False)
+    clean = run(ops, on_device(t))
+    bad = {key: v.copy() for key, v in t.items()}
+    nan, inf = 0x7FC0, 0x7F80
+    bad["A"][1, :, ::7], bad["B"][1, ::5, :] = nan, inf
+    hit = t["ids"] == 1
+    bad["X"][hit], bad["dY"][hit] = inf, nan
+    got = run(ops, on_device(bad))
+    keep = torch.from_numpy(~hit).cuda()
+    for name in ("Y", "H", "dX"):
+        assert torch.equal(clean[name][keep], got[name][keep]), name
+        assert not torch.isfinite(got[name][~keep].float()).all()
+    others = torch.tensor([a for a in range(n) if a != 1], device="cuda")
+    for name in ("dA", "dB"):
+        assert torch.equal(clean[name][others], got[name][others]), name
+
+
+@pytest.mark.parametrize("d,k,M,n,r", SPLIT)
+def test_two_streams_on_one_plan(ops, d, k, M, n, r):
+    # two linears of one batch at once: partial sums, counters and join of each
+    # in its own workspace
+    print(f"[adapters streams] d={d} k={k} M={M} n={n} r={r}", flush=True)
+    lin, plan = [], None
+    for i in range(2):
+        g = on_device(inputs(d, k, M, n, r, "mixed", 43 + i, False))
+        plan = plan or ops.adapter_plan(g["ids"], n)
+        w = ops.quantize(g["W0"], True)
+        a = dict(w=w, X=g["X"], A=g["A"], B=g["B"], scale=g["scale"], plan=plan)
+        Y, H = ops.linear_fwd_adapters(**a)
+        want = (Y, H) + ops.linear_bwd_adapters(**a, dY=g["dY"], H=H)
+        lin.append((a, g["dY"], want, ops.adapters_workspace(plan, d, k, r, backward=True),
+                    torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(6):
+        for a, dY, _, ws, st in lin:
+            Y, H = ops.linear_fwd_adapters(**a, ws=ws, stream=st)
+            got.append((Y, H) + ops.linear_bwd_adapters(**a, dY=dY, H=H, ws=ws, stream=st))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, lin[i % 2][2])), i
+
+
+@pytest.mark.parametrize("d,k,M,n,r", SPLIT)
+def test_graph_replay(ops, d, k, M, n, r):
+    # plan, forward and backward captured, replayed over a workspace and outputs
+    # that hold something else, with the program's own work between
+    print(f"[adapters graph] d={d} k={k} M={M} n={n} r={r}", flush=True)
+    t = on_device(inputs(d, k, M, n, r, "mixed", 47, False))
+    want = run(ops, t)
+    w, plan = ops.quantize(t["W0"], True), ops.adapter_plan(t["ids"], n)
+    b = {name: torch.empty_like(v) for name, v in want.items()}
+    ws = ops.adapters_workspace(plan, d, k, r, backward=True)
+    args = (w, t["X"], t["A"], t["B"], t["scale"], plan)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.adapter_plan(t["ids"], n, out=plan)
+        ops.linear_fwd_adapters(*args, Y=b["Y"], H=b["H"], ws=ws)
+        ops.linear_bwd_adapters(*args, t["dY"], H=b["H"], dX=b["dX"], dA=b["dA"], dB=b["dB"], ws=ws)
+    for i in range(4):
+        for x in b.values():
+            x.fill_(7.0)
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(b[x], want[x]) for x in b), i
+        assert torch.equal(run(ops, t)["dX"], want["dX"])
