@@ -1156,10 +1156,6 @@ size_t gemv_part_bytes(int64_t dtot, int64_t k, int64_t M, int rp, int nw) {
   return (size_t)(gemv_splits(k) * M * dtot * 4 + nw * gemv_splits(k) * GW * M * rp * 4);
 }
 
-// The VALU path for M <= VMAXM without adapter-input dropout: S = k / 2048
-// slices (the last may be ragged), one H partial per slice and weight; its
-// partial sums fit in the workspace sized for the MFMA path (fewer slices,
-// fewer H partials).
 static qlora_status launch_epilogue_adapters(const GemvIn &in, int64_t M, int64_t S, int rp,
                                              const GemvAd &ad, const float *scale,
                                              const float *part, const float *hpart,
@@ -1172,6 +1168,11 @@ static qlora_status launch_epilogue_adapters(const GemvIn &in, int64_t M, int64_
   return QLORA_OK;
 }
 
+// The VALU path for M <= VMAXM without adapter-input dropout: S = k / 2048
+// slices (the last may be ragged), one H partial per slice and weight (with
+// adapters: per slice and token); its
+// partial sums fit in the workspace sized for the MFMA path (fewer slices,
+// fewer H partials).
 static qlora_status launch_gemv_valu(int nw, const GemvIn *in, int64_t k, const uint16_t *X,
                                      int64_t M, int r, int rp, float s, float *part,
                                      hipStream_t st, const GemvAd *ad, const float *scale) {

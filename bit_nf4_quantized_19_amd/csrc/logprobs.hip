@@ -376,7 +376,7 @@ __global__ __launch_bounds__(JT) void logprobs_join_kernel(LpArgs g) {
 
   __shared__ uint64_t list[LP_LIST];
   __shared__ int count;
-  const int total = g.nchunk * top;                // at most 2^16 chunks of 32
+  const int total = g.nchunk * top;                // at most 2^17 chunks of 32
   const uint64_t *keys = g.keys + i * total;
   const int depth = (top + g.nchunk - 1) / g.nchunk;
   uint64_t low = ~0ull;
@@ -518,11 +518,12 @@ struct Split {
   int64_t chunk, nchunk;
 };
 
-// With rows for every compute unit, a row of up to 8192 pieces stays with one
-// workgroup of 256 or 512 threads (no join; 333 x 50257 bf16 in one of 512:
-// 16.6 us, in two of 256 18.8; 1024 threads measured no faster than the join).
-// Otherwise a row is cut into the largest chunks of 256 threads that still
-// give two workgroups per unit.
+// A row of 4097 to 8192 pieces stays with one workgroup of 512 threads where
+// there are 256 rows or more (no join; 333 x 50257 bf16 16.6 us, in two of 256
+// threads 18.8; 1024 threads measured no faster than the join). Any other row
+// goes to workgroups of 256 threads, 4096 pieces or less each, in the largest
+// chunks that give 512 workgroups in all, two a compute unit, or the smallest (256
+// pieces): rows of up to 4096 pieces stay whole from 512 rows on.
 Split split_of(int64_t N, int64_t V, bool f32) {
   const int64_t e = f32 ? 4 : 8;
   static const int kR[] = {1, 2, 4, 6, 8, 12, 16};

@@ -379,8 +379,6 @@ struct CmRegs {
   float4 q[RPM * KS / 32 > 0 ? RPM * KS / 32 : 1];
 };
 
-// Rows at or past M (here: the end of this workgroup's token range) read as 0.
-// AD: rows are plan positions of tokens perm[m].
 // A thread's tokens of a chunk (AD), read one chunk ahead of the rows they name.
 template <int RPM, int KS>
 struct CmTok {
@@ -396,6 +394,8 @@ QL_DEV void cm_tokens(CmTok<RPM, KS> &T, const int *perm, int64_t M, int rp, int
     T.q[u] = perm[min(m0 + (tid + 256 * u) / (rp / 4), M - 1)];
 }
 
+// Rows at or past M (here: the end of this workgroup's token range) read as 0.
+// AD: rows are plan positions of tokens perm[m].
 template <bool MK, int RPM, int KS, bool AD>
 QL_DEV void cm_load(CmRegs<RPM, KS> &R, const ColaccProb &P, int64_t M, int rp, int64_t m0, int64_t c0,
                     int tid, const ColaccAd &ad, const CmTok<RPM, KS> &T) {

@@ -748,7 +748,8 @@ def logprobs_workspace(logits: torch.Tensor, top: int = 0) -> torch.Tensor | Non
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0,
                    out: TokenLogprobs | None = None, ws: torch.Tensor | None = None,
                    stream=None) -> TokenLogprobs:
-    """Per row of logits (N x V bf16 or float32, rows at any stride): the log
+    """Per row of logits (N x V bf16 or float32, rows at any stride, the first of
+    them 16-byte aligned; a view that starts elsewhere is refused): the log
     probability of its target (int64; outside [0, V): ignored, 0), the
     entropy, and the ``top`` (0..32) best alternatives by value, then index."""
     c = _logits(logits, "logits")

@@ -92,7 +92,10 @@ QLORA_API size_t qlora_adapters_workspace_bytes(int32_t op, int64_t d, int64_t k
  * non-NULL it receives H[m] = X[m] A_a^T (M x r float32; zero rows for
  * tokens without an adapter) for the backward pass. M <= 16 runs the
  * memory-bound decode kernels, larger M the fused dequant-GEMM; both read
- * each touched adapter's matrices in place. Adapter-input dropout (the
+ * each touched adapter's matrices in place. As in qlora_linear_fwd, W'
+ * enters the matrix units as bf16: the GEMM (and every backward) as w' =
+ * bf16(level a'), the decode kernels as bf16(level), times a' in float32
+ * after each block's sum; the two differ by the rounding of a weight. Adapter-input dropout (the
  * qlora_dropout of qlora_nf4.h) is not offered here.
  */
 QLORA_API qlora_status qlora_linear_fwd_adapters(const qlora_nf4_weight *w, const uint16_t *X,

@@ -38,7 +38,8 @@ enum { QLORA_DTYPE_BF16 = 0, QLORA_DTYPE_F32 = 1 };
 
 /*
  * Logits: N rows of V values, row i at data + i * ld elements (ld >= V).
- * `data` is 16-byte aligned; ld is any number of elements.
+ * `data` is 16-byte aligned (else QLORA_ERR_INVALID_ARG); ld is any number of
+ * elements, so that the other rows start at any element.
  */
 typedef struct qlora_logits {
   void *data;
@@ -55,10 +56,11 @@ QLORA_API size_t qlora_token_logprobs_workspace_bytes(int64_t N, int64_t V, int3
  * targets [N] int64; logprob [N]; stats [N][2] = (m, l), which the gradient
  * needs; entropy [N] or NULL; top_logprobs [N][top] float32 and top_ids
  * [N][top] int64 for 0 <= top <= min(V, QLORA_MAX_TOP) (NULL when top is 0).
- * 1 <= N, 1 <= V < 2^31 - 2^16; else QLORA_ERR_INVALID_ARG. top > QLORA_MAX_TOP, or a
- * shape too large for one launch (2^32 threads: more than about 16 million short rows),
- * returns QLORA_ERR_UNSUPPORTED. targets and top_ids are 8-byte, the float outputs
- * 4-byte aligned.
+ * N < 1, V < 1, ld < V, top < 0 or top > V: QLORA_ERR_INVALID_ARG. V >= 2^31 - 2^16,
+ * N >= 2^31, ld > 2^40, top > QLORA_MAX_TOP (and <= V), or a shape too large for one
+ * launch (2^32 threads: more than about 16 million short rows): QLORA_ERR_UNSUPPORTED.
+ * The gradient's shapes have the same limits. targets and top_ids are 8-byte, the
+ * float outputs 4-byte aligned.
  */
 QLORA_API qlora_status qlora_token_logprobs(const qlora_logits *logits, const int64_t *targets,
                                             float *logprob, float *stats, float *entropy,
