@@ -410,28 +410,6 @@ qlora_status qlora_merge(const qlora_nf4_weight *w, const uint16_t *A, const uin
                       (hipStream_t)stream);
 }
 
-// Device address of a buffer the AdamW step may touch: device memory as is,
-// page-locked host memory through its device mapping. Anything else
-// (pageable host memory, unknown pointers) is refused, so the kernel never
-// dereferences an address the device cannot reach.
-static bool device_view(const void *p, void **dp) {
-  hipPointerAttribute_t a;
-  if (hipPointerGetAttributes(&a, p) != hipSuccess) {
-    (void)hipGetLastError();
-    return false;
-  }
-  if (a.type == hipMemoryTypeDevice) {
-    *dp = const_cast<void *>(p);
-    return true;
-  }
-  if (a.type == hipMemoryTypeHost && a.devicePointer) {
-    // the offset of p inside its allocation carries over to the mapping
-    *dp = (char *)a.devicePointer + ((const char *)p - (const char *)a.hostPointer);
-    return true;
-  }
-  return false;
-}
-
 qlora_status qlora_adamw_step(float *param, float *exp_avg, float *exp_avg_sq,
                               const uint16_t *grad, uint16_t *param_bf16, int64_t n,
                               const qlora_adamw_hparams *hp, int64_t step, void *stream) {

@@ -64,4 +64,26 @@ bool ws_ok(const void *ws, size_t ws_bytes, int64_t need) {
   return ws && (((uintptr_t)ws & (kAlign - 1)) == 0) && (int64_t)ws_bytes >= need;
 }
 
+// Device address of a buffer an optimiser step may touch: device memory as is,
+// page-locked host memory through its device mapping. Anything else
+// (pageable host memory, unknown pointers) is refused, so the kernel never
+// dereferences an address the device cannot reach.
+bool device_view(const void *p, void **dp) {
+  hipPointerAttribute_t a;
+  if (hipPointerGetAttributes(&a, p) != hipSuccess) {
+    (void)hipGetLastError();
+    return false;
+  }
+  if (a.type == hipMemoryTypeDevice) {
+    *dp = const_cast<void *>(p);
+    return true;
+  }
+  if (a.type == hipMemoryTypeHost && a.devicePointer) {
+    // the offset of p inside its allocation carries over to the mapping
+    *dp = (char *)a.devicePointer + ((const char *)p - (const char *)a.hostPointer);
+    return true;
+  }
+  return false;
+}
+
 }  // namespace

@@ -207,6 +207,37 @@ struct AdamScalars {
 qlora_status launch_adamw(float *p, float *m, float *v, const uint16_t *g, uint16_t *out,
                           int64_t n, const AdamScalars &s, hipStream_t st);
 
+// int8_rows.hip : records of an 8-bit base. Codes (rows x ldq, zero past cols)
+// and scale of each row of X (rows x cols bf16), times mul[cols] when given.
+qlora_status launch_int8_rows(const uint16_t *X, int64_t rows, int64_t cols, const float *mul,
+                              int8_t *q, int64_t ldq, float *scale, hipStream_t st);
+
+// int8_gemm.hip : the product with a d x k record, forward (mode 0) or dX
+// (mode 1). In: M x ldi codes, ldi a multiple of 128, zero past the
+// contraction; sx [M]. L, hi, lo (M x rp), r, rp: the rank-r term as in
+// launch_gemm_fwd / _dx (rp == 0: none).
+qlora_status launch_int8_gemm(int mode, const int8_t *W, const float *sw, int64_t d, int64_t k,
+                              const int8_t *In, int64_t ldi, const float *sx, int64_t M,
+                              const uint16_t *L, const uint16_t *hi, const uint16_t *lo, int r,
+                              int rp, uint16_t *Out, hipStream_t st);
+// The forward of up to INT8_GEMV_TOKENS tokens; H (M x rp float32), s on its product.
+constexpr int64_t INT8_GEMV_TOKENS = 64;
+qlora_status launch_int8_gemv(const int8_t *W, const float *sw, int64_t d, int64_t k,
+                              const int8_t *In, int64_t ldi, const float *sx, int64_t M,
+                              const uint16_t *B, const float *H, int r, int rp, float s,
+                              uint16_t *Y, hipStream_t st);
+
+// muon.hip : one orthogonalised momentum step of n matrices
+struct MuonScalars {
+  float beta, c1, lr, scale, wd;
+  double eps, a, b, c;
+  int steps, nesterov;
+};
+size_t muon_ws_bytes(int64_t n, int64_t rows, int64_t cols);
+qlora_status launch_muon(float *p, float *m, const uint16_t *g, uint16_t *out, int64_t n,
+                         int64_t rows, int64_t cols, const MuonScalars &s, void *ws,
+                         hipStream_t st);
+
 // compute units of the current device (capi.hip; queried on every call, 256
 // if the query fails)
 int ql_num_cus();

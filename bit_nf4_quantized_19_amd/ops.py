@@ -94,6 +94,16 @@ SIGNATURES = {
     "qlora_token_logprobs": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _sz,
                                             _vp]),
     "qlora_token_logprobs_bwd": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    # include/qlora_int8.h
+    "qlora_int8_quantize": (ctypes.c_int, [_vp, _vp, _vp]),
+    "qlora_int8_workspace_bytes": (_sz, [_i32, _i64, _i64, _i64, _i32]),
+    "qlora_linear_fwd_int8": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _i32, _f32, _vp, _vp, _vp,
+                                             _sz, _vp]),
+    "qlora_linear_bwd_int8": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _i32, _f32, _vp, _vp, _vp,
+                                             _vp, _vp, _vp, _sz, _vp]),
+    # include/qlora_muon.h
+    "qlora_muon_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "qlora_muon_step": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
 }
 
 #: the timing build's extra symbols; mirrors include/qlora_nf4_timing.h
@@ -110,7 +120,8 @@ TIMING_SIGNATURES = {
 KERNELS = ["quantize", "double_quant", "dequantize", "gemm_fwd", "gemm_dx", "gemv",
            "gemv_epilogue", "lora_down", "lora_reduce", "lora_colacc", "lora_colacc_reduce",
            "merge", "layout", "adamw", "loftq_product", "loftq_small", "residual", "adapter_plan",
-           "logprobs", "logprobs_grad"]
+           "logprobs", "logprobs_grad", "int8_rows", "int8_gemm_fwd", "int8_gemm_dx", "int8_gemv",
+           "muon"]
 
 
 def _load(path: str, signatures: dict) -> ctypes.CDLL:
@@ -813,6 +824,222 @@ def token_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, lp: TokenLog
     return dlogits
 
 
+# ---------------------------------------------------------------------------
+# an 8-bit integer base (include/qlora_int8.h)
+class Int8WeightC(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int64), ("k", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
+@dataclass
+class Int8Weight:
+    """8-bit base weight: int8 codes and one float32 scale per output channel."""
+    d: int
+    k: int
+    codes: torch.Tensor     # int8 [d, k]
+    scale: torch.Tensor     # float32 [d]
+
+    def c_struct(self) -> Int8WeightC:
+        return Int8WeightC(self.d, self.k, self.codes.data_ptr(), self.scale.data_ptr())
+
+    @staticmethod
+    def empty(d: int, k: int, device="cuda") -> "Int8Weight":
+        return Int8Weight(d, k, torch.empty(d, k, dtype=torch.int8, device=device),
+                          torch.empty(d, dtype=torch.float32, device=device))
+
+    def _named(self):
+        return ((self.codes, "codes", torch.int8, (self.d, self.k)),
+                (self.scale, "scale", torch.float32, (self.d,)))
+
+
+def quantize_int8(W: torch.Tensor, out: Int8Weight | None = None, stream=None) -> Int8Weight:
+    """Record of W (d x k bf16): per row scale = max|w| / 127 and the codes
+    w / scale rounded to nearest, ties to even."""
+    if W.dim() != 2:
+        raise ValueError("W must be d x k")
+    d, k = W.shape
+    if out is None:
+        with _on(stream):
+            out = Int8Weight.empty(d, k, W.device)
+    _device_tensors((W, "W", torch.bfloat16, (d, k)), *out._named())
+    if (out.d, out.k) != (d, k):
+        raise ValueError(f"out is a record of {out.d} x {out.k}, not {d} x {k}")
+    c = out.c_struct()
+    _check(lib().qlora_int8_quantize(W.data_ptr(), ctypes.addressof(c), _stream(stream)),
+           "qlora_int8_quantize")
+    return out
+
+
+def int8_workspace_bytes(op: int, d: int, k: int, M: int, r: int) -> int:
+    b = lib().qlora_int8_workspace_bytes(op, d, k, M, r)
+    if b == ctypes.c_size_t(-1).value:
+        raise QLoRAError(QLORA_ERR_UNSUPPORTED, "int8_workspace_bytes")
+    return int(b)
+
+
+def int8_workspace(w: Int8Weight, M: int, r: int = 0, backward: bool = False) -> torch.Tensor:
+    """Workspace of the forward of M tokens (and of the backward too, when
+    asked); calls on one stream can share it."""
+    b = int8_workspace_bytes(OP_FWD, w.d, w.k, M, r)
+    if backward:
+        b = max(b, int8_workspace_bytes(OP_BWD, w.d, w.k, M, r))
+    return _workspace(b, w.codes.device, None)[0]
+
+
+def _int8_rank(A, B) -> int:
+    if (A is None) != (B is None):
+        raise ValueError("A and B come together")
+    if A is None:
+        return 0
+    if A.dim() != 2 or A.shape[0] < 1:
+        raise ValueError("A must be r x k")
+    return A.shape[0]
+
+
+def _int8_args(w: Int8Weight, named, A, B, r: int, ws):
+    """Checks of a call's tensors, ``named`` as in ``_device_tensors``."""
+    named = list(named) + list(w._named())
+    if r:
+        named += [(A, "A", torch.bfloat16, (r, w.k)), (B, "B", torch.bfloat16, (w.d, r))]
+    _beside(_device_tensors(*named), (ws, "ws"))
+
+
+def linear_fwd_int8(w: Int8Weight, X: torch.Tensor, A: torch.Tensor | None = None,
+                    B: torch.Tensor | None = None, lora_alpha: float = 0.0, save_h: bool = True,
+                    Y: torch.Tensor | None = None, H: torch.Tensor | None = None,
+                    ws: torch.Tensor | None = None, stream=None):
+    """Y = sx sw (Xq Wq^T) + (alpha/r) (X A^T) B^T on an 8-bit base, the tokens
+    quantised by row; without A and B the product alone. Returns (Y, H or None)."""
+    r = _int8_rank(A, B)
+    M = X.shape[0]
+    save_h = save_h and r > 0
+    if Y is None or ws is None or (save_h and H is None):
+        with _on(stream):
+            if Y is None:
+                Y = torch.empty(M, w.d, dtype=torch.bfloat16, device=X.device)
+            if save_h and H is None:
+                H = torch.empty(M, r, dtype=torch.float32, device=X.device)
+            if ws is None:
+                ws = int8_workspace(w, M, r)
+    named = [(X, "X", torch.bfloat16, (M, w.k)), (Y, "Y", torch.bfloat16, (M, w.d))]
+    if save_h:
+        named.append((H, "H", torch.float32, (M, r)))
+    else:
+        H = None
+    _int8_args(w, named, A, B, r, ws)
+    c = w.c_struct()
+    _check(lib().qlora_linear_fwd_int8(ctypes.addressof(c), X.data_ptr(), M, _ptr(A), _ptr(B), r,
+                                       float(lora_alpha), Y.data_ptr(), _ptr(H), ws.data_ptr(),
+                                       ws.nbytes, _stream(stream)), "qlora_linear_fwd_int8")
+    return Y, H
+
+
+def linear_bwd_int8(w: Int8Weight, X: torch.Tensor | None, A: torch.Tensor | None,
+                    B: torch.Tensor | None, lora_alpha: float, dY: torch.Tensor,
+                    H: torch.Tensor | None = None, need_dx: bool = True, dX=None, dA=None, dB=None,
+                    ws: torch.Tensor | None = None, stream=None):
+    """Backward of ``linear_fwd_int8``: (dX or None, dA, dB); H as the forward
+    returned it, or None to recompute it. Without A and B (X may be None) only
+    dX is computed and dA and dB are None."""
+    r = _int8_rank(A, B)
+    M, dev = dY.shape[0], dY.device
+    with _on(stream):
+        if need_dx and dX is None:
+            dX = torch.empty(M, w.k, dtype=torch.bfloat16, device=dev)
+        if r and dA is None:
+            dA = torch.empty_like(A)
+        if r and dB is None:
+            dB = torch.empty_like(B)
+        if ws is None:
+            ws = int8_workspace(w, M, r, backward=True)
+    if not need_dx:
+        dX = None
+    if not r and (dA is not None or dB is not None or H is not None):
+        raise ValueError("H, dA and dB belong to A and B")
+    bf = torch.bfloat16
+    named = [(dY, "dY", bf, (M, w.d))]
+    if r:
+        if X is None:
+            raise ValueError("X is needed for dA")
+        named += [(X, "X", bf, (M, w.k)), (dA, "dA", bf, (r, w.k)), (dB, "dB", bf, (w.d, r))]
+    if dX is not None:
+        named.append((dX, "dX", bf, (M, w.k)))
+    if H is not None:
+        named.append((H, "H", torch.float32, (M, r)))
+    _int8_args(w, named, A, B, r, ws)
+    c = w.c_struct()
+    _check(lib().qlora_linear_bwd_int8(ctypes.addressof(c), _ptr(X) if r else None, M, _ptr(A),
+                                       _ptr(B), r, float(lora_alpha), dY.data_ptr(), _ptr(H),
+                                       _ptr(dX), _ptr(dA), _ptr(dB), ws.data_ptr(), ws.nbytes,
+                                       _stream(stream)), "qlora_linear_bwd_int8")
+    return dX, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# orthogonalised momentum step (include/qlora_muon.h)
+#: coefficients of the quintic Newton-Schulz iteration x -> a x + b x^3 + c x^5
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+class MuonHParamsC(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("eps", ctypes.c_double),
+                ("scale", ctypes.c_double), ("a", ctypes.c_double), ("b", ctypes.c_double),
+                ("c", ctypes.c_double), ("steps", ctypes.c_int32), ("nesterov", ctypes.c_int32)]
+
+
+def _matrices(t: torch.Tensor):
+    if t.dim() not in (2, 3):
+        raise ValueError("param must be rows x cols or n x rows x cols")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def muon_workspace(param: torch.Tensor, device=None) -> torch.Tensor:
+    """Workspace of ``muon_step`` for parameters of this shape, on ``device``
+    (default: the parameters' own, the current one where they are paged out)."""
+    b = lib().qlora_muon_workspace_bytes(*_matrices(param))
+    if b == ctypes.c_size_t(-1).value:
+        raise QLoRAError(QLORA_ERR_UNSUPPORTED, "muon_workspace")
+    if device is None:
+        device = param.device if param.is_cuda else "cuda"
+    return _workspace(int(b), device, None)[0]
+
+
+def muon_step(param: torch.Tensor, momentum: torch.Tensor, grad: torch.Tensor,
+              param_bf16: torch.Tensor, lr: float = 0.02, beta: float = 0.95,
+              weight_decay: float = 0.0, nesterov: bool = True, steps: int = 5, eps: float = 1e-7,
+              scale: float | None = None, coefficients=MUON_COEFFICIENTS,
+              ws: torch.Tensor | None = None, stream=None):
+    """One orthogonalised momentum step in place on (param, momentum) (float32,
+    rows x cols or n x rows x cols, each matrix on its own, the smaller side at
+    most 128) with the bf16 gradient, writing the bf16 copy of the updated
+    parameter. ``scale`` of the update: sqrt(max(1, rows / cols)) by default.
+
+    param and momentum may be CUDA tensors or page-locked host tensors, as in
+    ``adamw_step``."""
+    n, rows, cols = _matrices(param)
+    for t, name in ((param, "param"), (momentum, "momentum")):
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.shape != param.shape:
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape "
+                             f"{tuple(param.shape)}")
+        if not (t.is_cuda or t.is_pinned()):
+            raise ValueError(f"{name} must be a CUDA tensor or page-locked host memory")
+    dev = _device_tensors((grad, "grad", torch.bfloat16, param.shape),
+                          (param_bf16, "param_bf16", torch.bfloat16, param.shape))
+    if ws is None:
+        with _on(stream):
+            ws = muon_workspace(param, grad.device)
+    _beside(dev, (ws, "ws"), *((t, nm) for t, nm in ((param, "param"), (momentum, "momentum"))
+                               if t.is_cuda))
+    if scale is None:
+        scale = max(1.0, rows / cols) ** 0.5
+    hp = MuonHParamsC(lr, beta, weight_decay, eps, scale, *coefficients, int(steps),
+                      int(bool(nesterov)))
+    _check(lib().qlora_muon_step(param.data_ptr(), momentum.data_ptr(), grad.data_ptr(),
+                                 param_bf16.data_ptr(), n, rows, cols, ctypes.addressof(hp),
+                                 ws.data_ptr(), ws.nbytes, _stream(stream)), "qlora_muon_step")
+
+
 def profile_begin(cap: int = 4096, kernels=None):
     """Start bracketing kernel launches of the timing build with HIP events
     (include/qlora_nf4_timing.h); only calls made inside ``timing_build()``
@@ -843,4 +1070,7 @@ __all__ = ["NF4Weight", "QLoRAError", "quantize", "dequantize", "linear_fwd", "l
            "profile_begin", "profile_end", "profile_query", "timing_build", "timing_lib",
            "TIMING_LIB_PATH", "AdapterPlan", "adapter_plan", "adapters_workspace",
            "adapters_workspace_bytes", "linear_fwd_adapters", "linear_bwd_adapters",
-           "TokenLogprobs", "token_logprobs", "token_logprobs_bwd", "logprobs_workspace"]
+           "TokenLogprobs", "token_logprobs", "token_logprobs_bwd", "logprobs_workspace",
+           "Int8Weight", "quantize_int8", "int8_workspace", "int8_workspace_bytes",
+           "linear_fwd_int8", "linear_bwd_int8", "MUON_COEFFICIENTS", "muon_workspace",
+           "muon_step"]

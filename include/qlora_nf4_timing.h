@@ -1,8 +1,8 @@
 /*
  * qlora_nf4_timing.h -- kernel timing of libqlora_nf4_timing.so, a
  * measurement build of the same sources as libqlora_nf4.so (identical
- * kernels and entry points, declared in qlora_nf4.h, qlora_adapters.h and
- * qlora_logprobs.h). It is not part of the
+ * kernels and entry points, declared in qlora_nf4.h, qlora_adapters.h,
+ * qlora_logprobs.h, qlora_int8.h and qlora_muon.h). It is not part of the
  * method and not in the product library: libqlora_nf4.so exports none of
  * these symbols and keeps no mutable host state.
  *
@@ -37,7 +37,8 @@ enum {
   QLORA_K_LORA_COLACC_REDUCE = 10, QLORA_K_MERGE = 11, QLORA_K_LAYOUT = 12,
   QLORA_K_ADAMW = 13, QLORA_K_LOFTQ_PRODUCT = 14, QLORA_K_LOFTQ_SMALL = 15,
   QLORA_K_RESIDUAL = 16, QLORA_K_ADAPTER_PLAN = 17, QLORA_K_LOGPROBS = 18,
-  QLORA_K_LOGPROBS_GRAD = 19, QLORA_K_COUNT = 20
+  QLORA_K_LOGPROBS_GRAD = 19, QLORA_K_INT8_ROWS = 20, QLORA_K_INT8_GEMM_FWD = 21,
+  QLORA_K_INT8_GEMM_DX = 22, QLORA_K_INT8_GEMV = 23, QLORA_K_MUON = 24, QLORA_K_COUNT = 25
 };
 QLORA_API qlora_status qlora_profile_begin(int32_t cap, uint32_t mask);
 QLORA_API qlora_status qlora_profile_end(void);

@@ -26,6 +26,10 @@ Modules
                  one base): ``oracle.lora`` on each adapter's tokens.
 ``oracle.logprobs`` Log probabilities of given tokens, entropy, the best
                  alternatives and the gradient of the logits, in float64.
+``oracle.int8``  8-bit records by row (float32 roundings as defined), the layer
+                 on them forward and backward, in float64.
+``oracle.muon``  Orthogonalised momentum step: float32 momentum, the iteration
+                 on the matrix itself in float64.
 
 Every function cites the page passage it follows. A page is cited by its
 title and section, e.g. "QLoRA glossary (Ultralytics), 'QLoRA 的工作原理'".
