@@ -33,9 +33,10 @@ struct FwdWs {
   float *sx;
   float *H;            // M x rp
   uint16_t *hi, *lo;   // s H
+  void *part;
   int64_t ldq, bytes;
 };
-FwdWs fwd_layout(char *base, int64_t k, int64_t M, int r) {
+FwdWs fwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
   const int64_t rp = ql_rup(r, 16);
   Carve c{base};
   FwdWs L{};
@@ -45,13 +46,15 @@ FwdWs fwd_layout(char *base, int64_t k, int64_t M, int r) {
   L.H = c.take<float>(M * rp * 4);
   L.hi = c.take<uint16_t>(M * rp * 2);
   L.lo = c.take<uint16_t>(M * rp * 2);
+  L.part = c.take<void>(M > INT8_GEMV_TOKENS ? (int64_t)int8_gemm_part_bytes(M, d, k) : 0);
   L.bytes = c.off;
   return L;
 }
 
 struct BwdWs {
   int8_t *q;           // M x ldq codes of dY sw
-  float *se, *H, *G, *part;
+  float *se, *H, *G, *cpart;
+  void *part;
   uint16_t *Bt, *hi, *lo;
   int64_t ldq, bytes;
 };
@@ -69,8 +72,9 @@ BwdWs bwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
     L.hi = c.take<uint16_t>(M * rp * 2);
     L.lo = c.take<uint16_t>(M * rp * 2);
     L.Bt = (r % 16) ? c.take<uint16_t>((int64_t)rp * d * 2) : nullptr;
-    L.part = c.take<float>((int64_t)colacc_part_bytes(M, d, k, rp));
+    L.cpart = c.take<float>((int64_t)colacc_part_bytes(M, d, k, rp));
   }
+  L.part = c.take<void>((int64_t)int8_gemm_part_bytes(M, k, d));
   L.bytes = c.off;
   return L;
 }
@@ -90,7 +94,7 @@ qlora_status qlora_int8_quantize(const uint16_t *W, const qlora_int8_weight *out
 size_t qlora_int8_workspace_bytes(int32_t op, int64_t d, int64_t k, int64_t M, int32_t r) {
   if (check_shape(d, k) != QLORA_OK || M < 1 || M > QLORA_INT8_MAX_TOKENS || r < 0 || r > 128)
     return (size_t)-1;
-  if (op == QLORA_OP_FWD) return (size_t)fwd_layout(nullptr, k, M, r).bytes;
+  if (op == QLORA_OP_FWD) return (size_t)fwd_layout(nullptr, d, k, M, r).bytes;
   if (op == QLORA_OP_BWD) return (size_t)bwd_layout(nullptr, d, k, M, r).bytes;
   return (size_t)-1;
 }
@@ -108,21 +112,20 @@ qlora_status qlora_linear_fwd_int8(const qlora_int8_weight *w, const uint16_t *X
     return QLORA_ERR_INVALID_ARG;
   if (M > QLORA_INT8_MAX_TOKENS) return QLORA_ERR_UNSUPPORTED;
   const int64_t d = w->d, k = w->k;
-  const FwdWs L = fwd_layout((char *)ws, k, M, r);
+  const FwdWs L = fwd_layout((char *)ws, d, k, M, r);
   if (!ws_ok(ws, ws_bytes, L.bytes)) return QLORA_ERR_WORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   const int rp = (int)ql_rup(r, 16);
   const float sc = r ? lora_alpha / (float)r : 0.0f;
   if ((s = launch_int8_rows(X, M, k, nullptr, L.q, L.ldq, L.sx, st)) != QLORA_OK) return s;
-  const bool decode = M <= INT8_GEMV_TOKENS;
-  if (r && (s = launch_skinny(X, M, k, A, false, r, rp, L.H, H_save, r, sc,
-                              decode ? nullptr : L.hi, decode ? nullptr : L.lo, st)) != QLORA_OK)
+  if (r && (s = launch_skinny(X, M, k, A, false, r, rp, L.H, H_save, r, sc, L.hi, L.lo, st)) !=
+               QLORA_OK)
     return s;
-  if (decode)
-    return launch_int8_gemv(w->codes, w->scale, d, k, L.q, L.ldq, L.sx, M, B, L.H, r, rp, sc, Y,
+  if (M <= INT8_GEMV_TOKENS)
+    return launch_int8_gemv(w->codes, w->scale, d, k, L.q, L.ldq, L.sx, M, B, L.hi, L.lo, r, rp, Y,
                             st);
   return launch_int8_gemm(0, w->codes, w->scale, d, k, L.q, L.ldq, L.sx, M, B, L.hi, L.lo, r, rp,
-                          Y, st);
+                          Y, L.part, st);
 }
 
 qlora_status qlora_linear_bwd_int8(const qlora_int8_weight *w, const uint16_t *X, int64_t M,
@@ -155,7 +158,7 @@ qlora_status qlora_linear_bwd_int8(const qlora_int8_weight *w, const uint16_t *X
     }
     // G = dY B and s G as bf16 hi/lo; the launch also clears the counters of
     // the gradients' launch. B is read in place, or from a padded B^T
-    int *cnt = colacc_counters(L.part, M, d, k, rp);
+    int *cnt = colacc_counters(L.cpart, M, d, k, rp);
     const int64_t ncnt = colacc_counter_count(d, k);
     const uint16_t *P = B;
     if (r % 16) {
@@ -168,14 +171,14 @@ qlora_status qlora_linear_bwd_int8(const qlora_int8_weight *w, const uint16_t *X
       return s;
     const DropParams none{0u, 0u, 0u, 1.0f, 0};
     if ((s = launch_colacc2(ColaccReq{dY, d, H, dB, 0, none, nullptr},
-                            ColaccReq{X, k, L.G, dA, 1, none, nullptr}, M, rp, r, sc, L.part,
+                            ColaccReq{X, k, L.G, dA, 1, none, nullptr}, M, rp, r, sc, L.cpart,
                             st)) != QLORA_OK)
       return s;
   }
   if (!dX) return QLORA_OK;
   if ((s = launch_int8_rows(dY, M, d, w->scale, L.q, L.ldq, L.se, st)) != QLORA_OK) return s;
   return launch_int8_gemm(1, w->codes, w->scale, d, k, L.q, L.ldq, L.se, M, A, L.hi, L.lo, r, rp,
-                          dX, st);
+                          dX, L.part, st);
 }
 
 }  // extern "C"

@@ -14,7 +14,6 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 struct I8Args {
   const int8_t *W;       // d x k codes
@@ -28,6 +27,8 @@ struct I8Args {
   const uint16_t *Shi, *Slo;   // M x rp
   int r, rp;
   uint16_t *Out;         // M x Ntot
+  int S;                 // workgroups that share a tile's K-steps
+  i32x4 *part;           // S > 1: their sums, [split][tile][block][thread]
 };
 
 QL_DEV uint32_t lds_addr(const void *p) {
@@ -55,165 +56,82 @@ QL_DEV void block_sync() {
   asm volatile("" ::: "memory");
 }
 
-QL_DEV i32x16 mfma_i8(const i32x4 &a, const i32x4 &b, const i32x16 &c) {
-  return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+// 16x16x64: lane l supplies row l % 16, codes 16 (l / 16) .. +15 of both
+// operands and holds rows 4 (l / 16) .. +3 of column l % 16. The 32x32x32 form
+// has the same rate but draws more power, and the chip is power-limited here:
+// 4.0 against 3.4 POP/s sustained on random codes.
+QL_DEV i32x4 mfma_i8(const i32x4 &a, const i32x4 &b, const i32x4 &c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-constexpr int BK = 128;   // K-step: 128 codes, rows of 128 bytes in LDS
+constexpr int BK = 128;   // K-step: 128 codes
+constexpr int SL = BK / 64;   // K-slices of a step
 
-// Chunk (16 bytes) c of K-contiguous tile row `row`: its place in the row,
-// permuted so that neighbouring rows' equal chunks lie in different banks.
-QL_DEV int swz(int row, int c) { return c ^ ((row ^ (row >> 2)) & 7); }
+// Where chunk (16 bytes) c of a tile row is kept in its row, so that what one
+// operand read takes lies in different banks (64 of 4 bytes). K-contiguous
+// tiles have rows of 128 bytes and are read 16 rows x 16 bytes at a time;
+// the weight tile of dX has rows of BN bytes and is read 8 rows x 16 columns
+// at a time, from two groups of 8 rows 16 apart.
+QL_DEV int swz(int row, int c) { return c ^ ((row >> 1) & 7); }
+QL_DEV int swz_dx(int row, int c) { return c ^ (row & 7) ^ ((row >> 4) & 1); }
 
-// MODE 0 forward, 1 dX. BN x BM tile by WN x WM waves, NST LDS stages.
-template <int MODE, int BN, int BM, int WN, int WM, int NST>
-__global__ __launch_bounds__(64 * WN * WM) void int8_gemm_kernel(I8Args g) {
-  constexpr int NW = WN * WM, TI = BN / WN / 32, TJ = BM / WM / 32;
-  constexpr int WDMA = BN * BK / 1024 / NW, XDMA = BM * BK / 1024 / NW;
-  __shared__ __align__(1024) uint4 s_t[NST * (BN + BM) * BK / 16];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wave % WN, wm = wave / WN, r32 = lane & 31, h = lane >> 5;
+// First column and token of tile id. XCD-aware order: workgroups of one XCD
+// (id % 8) take a contiguous range, in groups of 4 token blocks with the column
+// tile slow, so that an XCD's L2 serves its 32 tiles' shared rows.
+template <int BN, int BM>
+QL_DEV void tile_of(const I8Args &g, uint32_t bid, int64_t &n0, int64_t &m0) {
+  const uint32_t tn = (uint32_t)((g.Ntot + BN - 1) / BN), tm = (uint32_t)((g.M + BM - 1) / BM);
+  const uint32_t nt = tn * tm, q = nt / 8, rest = nt % 8, x = bid % 8;
+  const uint32_t id = x * q + (x < rest ? x : rest) + bid / 8;
+  const uint32_t g0 = id / (4 * tn) * 4, gm = tm - g0 < 4 ? tm - g0 : 4, in = id - g0 * tn;
+  n0 = (int64_t)(in / gm) * BN;
+  m0 = (int64_t)(g0 + in % gm) * BM;
+}
 
-  // XCD-aware order of the tiles: workgroups of one XCD (id % 8) take a
-  // contiguous range, in groups of 4 token blocks with the column tile slow
-  const int64_t tn = ql_cdiv(g.Ntot, BN), tm = ql_cdiv(g.M, BM), nt = tn * tm;
-  int64_t id = blockIdx.x;
-  {
-    const int64_t q = nt / 8, rest = nt % 8, x = id % 8, y = id / 8;
-    id = x * q + (x < rest ? x : rest) + y;
-  }
-  const int64_t g0 = id / (4 * tn) * 4, gm = tm - g0 < 4 ? tm - g0 : 4, in = id - g0 * tn;
-  const int64_t n0 = in / gm * BN, m0 = (g0 + in % gm) * BM;
-
-  // this lane's DMA sources (rows and columns past the matrix fetch the last
-  // valid ones: their sums are not stored, or meet the zeros of In past Ktot)
-  int64_t xoff[XDMA], woff[WDMA];
-  int wrow[WDMA];
-#pragma unroll
-  for (int i = 0; i < XDMA; ++i) {
-    const int row = 8 * (XDMA * wave + i) + (lane >> 3);
-    const int64_t m = m0 + row < g.M ? m0 + row : g.M - 1;
-    xoff[i] = m * g.ldi + 16 * swz(row, lane & 7);
-  }
-#pragma unroll
-  for (int i = 0; i < WDMA; ++i) {
-    if (MODE == 0) {
-      const int row = 8 * (WDMA * wave + i) + (lane >> 3);
-      const int64_t n = n0 + row < g.d ? n0 + row : g.d - 1;
-      wrow[i] = 16 * swz(row, lane & 7);
-      woff[i] = n * g.k;
-    } else {
-      constexpr int CPR = BN / 16;   // chunks of a tile row
-      const int p = 64 * (WDMA * wave + i) + lane;
-      wrow[i] = p / CPR;
-      const int c = (p % CPR) ^ (wrow[i] & 7);
-      const int64_t n = n0 + 16 * c;
-      woff[i] = n < g.k ? n : g.k - 16;
-    }
-  }
-  const int nk = (int)ql_cdiv(g.Ktot, BK);
-  auto issue = [&](int step) {
-    const int64_t kk = (int64_t)step * BK;
-    const uint32_t base = lds_addr(s_t) + (uint32_t)(step % NST) * (BN + BM) * BK;
-#pragma unroll
-    for (int i = 0; i < WDMA; ++i) {
-      const int8_t *src;
-      if (MODE == 0) {
-        const int64_t c = kk + wrow[i];
-        src = g.W + woff[i] + (c < g.k ? c : g.k - 16);
-      } else {
-        const int64_t j = kk + wrow[i];
-        src = g.W + (j < g.d ? j : g.d - 1) * g.k + woff[i];
-      }
-      dma16(src, base + 1024 * (WDMA * wave + i));
-    }
-#pragma unroll
-    for (int i = 0; i < XDMA; ++i)
-      dma16(g.In + xoff[i] + kk, base + BN * BK + 1024 * (XDMA * wave + i));
-  };
-
-  i32x16 acc[TI][TJ];
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
-
-  for (int s = 0; s < NST - 1 && s < nk; ++s) issue(s);
-  for (int step = 0; step < nk; ++step) {
-    // this step's DMAs have landed; those of NST - 2 later steps may be in flight
-    if (step + NST - 2 < nk) wait_vm_le<(NST - 2) * (WDMA + XDMA)>();
-    else wait_vm_le<0>();
-    block_sync();
-    // refill the stage of the step before, which every wave has read
-    if (step + NST - 1 < nk) issue(step + NST - 1);
-    const char *ws = (const char *)s_t + (step % NST) * (BN + BM) * BK;
-    const char *xs = ws + BN * BK;
-#pragma unroll
-    for (int c = 0; c < BK / 32; ++c) {
-      i32x4 a[TI], b[TJ];
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const int nl = (wn * TI + i) * 32;
-        if (MODE == 0) {
-          const int row = nl + r32;
-          a[i] = *(const i32x4 *)(ws + row * BK + 16 * swz(row, 2 * c + h));
-        } else {
-          // two transposing reads of 8 rows x 16 columns per 16 lanes
-          const int t = (lane & 15) >> 1, ch = nl / 16 + ((lane >> 4) & 1);
-          const int row = 32 * c + 16 * h + t;
-          typedef __attribute__((address_space(3))) i32x2 lds2;
-          const char *p = ws + row * BN + 16 * (ch ^ (row & 7)) + 8 * (lane & 1);
-          const i32x2 lo = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2 *)p);
-          const i32x2 hi = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2 *)(p + 8 * BN));
-          a[i] = i32x4{lo[0], lo[1], hi[0], hi[1]};
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const int row = (wm * TJ + j) * 32 + r32;
-        b[j] = *(const i32x4 *)(xs + row * BK + 16 * swz(row, 2 * c + h));
-      }
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma_i8(a[i], b[j], acc[i][j]);
-    }
-  }
-
-  // scales, then the rank-r term on the float32 values, rounded once to bf16
+// A wave's 16 TI x 16 TJ block at column n0, token m0: scales, then the rank-r
+// term on the float32 values, rounded once to bf16. The block goes through the
+// wave's TI * TJ * 512 bytes of LDS, so that whole lines of 128 bytes are
+// stored: 8-byte stores of the lanes' four columns took 7 us more for 2048 x
+// 4096 outputs.
+template <int MODE, int TI, int TJ>
+QL_DEV void epilogue(const I8Args &g, const i32x4 (&acc)[TI][TJ], char *blk, int64_t n0,
+                     int64_t m0) {
+  const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4;
   float sx[TJ];
   int64_t mrow[TJ];
 #pragma unroll
   for (int j = 0; j < TJ; ++j) {
-    mrow[j] = m0 + (wm * TJ + j) * 32 + r32;
-    sx[j] = g.sx[mrow[j] < g.M ? mrow[j] : g.M - 1];
+    const int64_t m = m0 + j * 16 + c16;
+    mrow[j] = m < g.M ? m : g.M - 1;
+    sx[j] = g.sx[mrow[j]];
   }
+  constexpr int WB = TI * 32, CPW = WB / 16;   // bytes and chunks of a block's row
+  static_assert((CPW & (CPW - 1)) == 0, "a power of two");
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
-    const int64_t nb = n0 + (wn * TI + i) * 32;
-    f32x16 v[TJ];
-    float4 sw[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t n = nb + 8 * q + 4 * h;
-      sw[q] = MODE == 0 ? *(const float4 *)(g.sw + (n < g.d ? n : g.d - 4))
-                        : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    const int64_t nb = n0 + i * 16;
+    f32x4 v[TJ];
+    float4 sw = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (MODE == 0) {
+      const int64_t n = nb + 4 * grp;
+      sw = *(const float4 *)(g.sw + (n < g.d ? n : g.d - 4));
     }
 #pragma unroll
-    for (int j = 0; j < TJ; ++j)
+    for (int j = 0; j < TJ; ++j) {
+      const float w[4] = {sw.x, sw.y, sw.z, sw.w};
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
+      for (int q = 0; q < 4; ++q) {
         const float f = (float)acc[i][j][q] * sx[j];
-        const float w[4] = {sw[q >> 2].x, sw[q >> 2].y, sw[q >> 2].z, sw[q >> 2].w};
-        v[j][q] = MODE == 0 ? f * w[q & 3] : f;
+        v[j][q] = MODE == 0 ? f * w[q] : f;
       }
+    }
+    // 16 ranks at a time: lanes 0-31 take s H's high parts, lanes 32-63 its low
+    // parts, against the same rows of L
+    const uint16_t *S = grp < 2 ? g.Shi : g.Slo;
+    int64_t n = nb + c16;
+    n = n < g.Ntot ? n : g.Ntot - 1;
     for (int t0 = 0; t0 < g.rp; t0 += 16) {
-      const int t = t0 + 8 * h;
-      int64_t n = nb + r32;
-      n = n < g.Ntot ? n : g.Ntot - 1;
+      const int t = t0 + 8 * (grp & 1);
       uint4 l;
       if (MODE == 0 && g.r % 8 == 0) {
         l = t < g.r ? *(const uint4 *)(g.L + n * g.r + t) : ql::zero4();
@@ -229,36 +147,209 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_gemm_kernel(I8Args g) {
                        e[6] | (e[7] << 16));
       }
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const int64_t m = mrow[j] < g.M ? mrow[j] : g.M - 1;
-        const uint4 hi = *(const uint4 *)(g.Shi + m * g.rp + t);
-        const uint4 lo = *(const uint4 *)(g.Slo + m * g.rp + t);
-        v[j] = ql::mfma32(l, hi, v[j]);
-        v[j] = ql::mfma32(l, lo, v[j]);
-      }
+      for (int j = 0; j < TJ; ++j)
+        v[j] = ql::mfma16(l, *(const uint4 *)(S + mrow[j] * g.rp + t), v[j]);
     }
+    // row j * 16 + c16 of the block, columns 16 i + 4 grp .. +3, the row's
+    // 16-byte chunks permuted by the row
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      if (mrow[j] >= g.M) continue;
-      uint16_t *out = g.Out + mrow[j] * g.Ntot;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t n = nb + 8 * q + 4 * h;
-        if (n < g.Ntot)
-          *(uint2 *)(out + n) = make_uint2(ql::pack_bf16x2(v[j][4 * q], v[j][4 * q + 1]),
-                                           ql::pack_bf16x2(v[j][4 * q + 2], v[j][4 * q + 3]));
-      }
+      const int row = 16 * j + c16, c = (2 * i + (grp >> 1)) ^ (c16 & (CPW - 1));
+      *(uint2 *)(blk + row * WB + 16 * c + 8 * (grp & 1)) =
+          make_uint2(ql::pack_bf16x2(v[j][0], v[j][1]), ql::pack_bf16x2(v[j][2], v[j][3]));
     }
+  }
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int x = 0; x < TJ * 16 * CPW / 64; ++x) {
+    const int row = x * (64 / CPW) + lane / CPW, c = lane % CPW;
+    const uint4 v = *(const uint4 *)(blk + row * WB + 16 * (c ^ (row & 15 & (CPW - 1))));
+    const int64_t m = m0 + row, n = n0 + 8 * c;
+    if (m < g.M && n < g.Ntot) *(uint4 *)(g.Out + m * g.Ntot + n) = v;
   }
 }
 
-// ---- decode: up to 64 tokens ------------------------------------------------
-// A workgroup of eight waves owns 16 rows of the weight and all tokens, its
-// waves take 64-code chunks of the rows in turn (v_mfma_i32_16x16x64_i8: lane l
-// supplies row l % 16, codes 16 (l / 16) .. +15 of both operands and holds
-// rows 4 (l / 16) .. +3 of token l % 16); the waves' int32 sums meet in LDS.
-// Bound by the weight's bytes: each is read once, in pieces of 512 consecutive
-// bytes a row and round of waves.
+// MODE 0 forward, 1 dX. BN x BM tile by WN x WM waves, NST LDS stages; SPLIT:
+// g.S workgroups share the tile's K-steps and leave their sums in g.part.
+template <int MODE, int BN, int BM, int WN, int WM, int NST, bool SPLIT>
+__global__ __launch_bounds__(64 * WN * WM) void int8_gemm_kernel(I8Args g) {
+  constexpr int NW = WN * WM, TI = BN / WN / 16, TJ = BM / WM / 16;
+  constexpr int WDMA = BN * BK / 1024 / NW, XDMA = BM * BK / 1024 / NW;
+  constexpr uint32_t STAGE = (BN + BM) * BK;
+  __shared__ __align__(1024) uint4 s_t[NST * STAGE / 16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave % WN, wm = wave / WN, c16 = lane & 15, grp = lane >> 4;
+  uint32_t tile = blockIdx.x;
+  int first = 0, nk = (int)ql_cdiv(g.Ktot, BK);   // this workgroup's K-steps
+  if (SPLIT) {
+    // tile fast: an XCD's workgroups share tokens of one range of K
+    const uint32_t nt = gridDim.x / (uint32_t)g.S, y = tile / nt;
+    tile -= y * nt;
+    first = (int)(y * (uint32_t)nk / (uint32_t)g.S);
+    nk = (int)((y + 1) * (uint32_t)nk / (uint32_t)g.S) - first;
+  }
+  int64_t n0, m0;
+  tile_of<BN, BM>(g, tile, n0, m0);
+
+  // this lane's DMA sources (rows and columns past the matrix fetch the last
+  // valid ones: their sums are not stored, or meet the zeros of In past Ktot)
+  const int8_t *xsrc[XDMA], *wsrc[WDMA];
+  uint32_t wrow[WDMA];   // forward: offset in the row's step; dX: row of the step
+#pragma unroll
+  for (int i = 0; i < XDMA; ++i) {
+    const int row = 8 * (XDMA * wave + i) + (lane >> 3);
+    const int64_t m = m0 + row < g.M ? m0 + row : g.M - 1;
+    xsrc[i] = g.In + m * g.ldi + 16 * swz(row, lane & 7);
+  }
+#pragma unroll
+  for (int i = 0; i < WDMA; ++i) {
+    if (MODE == 0) {
+      const int row = 8 * (WDMA * wave + i) + (lane >> 3);
+      const int64_t n = n0 + row < g.d ? n0 + row : g.d - 1;
+      wrow[i] = 16 * swz(row, lane & 7);
+      wsrc[i] = g.W + n * g.k;
+    } else {
+      constexpr int CPR = BN / 16;   // chunks of a tile row
+      const int p = 64 * (WDMA * wave + i) + lane;
+      wrow[i] = p / CPR;
+      const int64_t n = n0 + 16 * swz_dx(wrow[i], p % CPR);
+      wsrc[i] = g.W + (n < g.k ? n : g.k - 16);
+    }
+  }
+  const uint32_t k = (uint32_t)g.k, wend = MODE == 0 ? k - 16 : (uint32_t)g.d - 1;
+  auto issue = [&](int step, uint32_t stage) {   // stage: its byte offset
+    const uint32_t kk = (uint32_t)(first + step) * BK, base = lds_addr(s_t) + stage;
+#pragma unroll
+    for (int i = 0; i < WDMA; ++i) {
+      const uint32_t e = kk + wrow[i] < wend ? kk + wrow[i] : wend;
+      dma16(wsrc[i] + (MODE == 0 ? (uint64_t)e : (uint64_t)e * k), base + 1024 * (WDMA * wave + i));
+    }
+#pragma unroll
+    for (int i = 0; i < XDMA; ++i)
+      dma16(xsrc[i] + kk, base + BN * BK + 1024 * (XDMA * wave + i));
+  };
+
+  // LDS offsets of this lane's operands: the K-contiguous ones by K-slice
+  // (rows 16 apart are permuted alike), those of a dX weight tile by block
+  uint32_t koff[SL], noff[TI];
+#pragma unroll
+  for (int c = 0; c < SL; ++c) koff[c] = c16 * BK + 16 * swz(c16, 4 * c + grp);
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int row = 16 * grp + (c16 >> 1);
+    noff[i] = row * BN + 16 * swz_dx(row, wn * TI + i) + 8 * (lane & 1);
+  }
+
+  i32x4 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+  // operands of a K-slice and of the slice after it, read under its products
+  i32x4 fa[2][TI], fb[2][TJ];
+  auto read = [&](uint32_t stage, int c) {
+    const char *ws = (const char *)s_t + stage, *xs = ws + BN * BK;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      if (MODE == 0) {
+        fa[c][i] = *(const i32x4 *)(ws + koff[c] + (wn * TI + i) * 16 * BK);
+      } else {
+        // two transposing reads, each 8 rows x 16 columns per 16 lanes: lane
+        // 2 t + e addresses columns 8 e .. +7 of row t and gets the 8 rows of
+        // column lane % 16 (rows 8 on are permuted like rows 0 on)
+        typedef __attribute__((address_space(3))) i32x2 lds2;
+        const char *q = ws + noff[i] + 64 * c * BN;
+        const i32x2 lo = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2 *)q);
+        const i32x2 hi = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2 *)(q + 8 * BN));
+        fa[c][i] = i32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+      fb[c][j] = *(const i32x4 *)(xs + koff[c] + (wm * TJ + j) * 16 * BK);
+  };
+  auto products = [&](int c, int i0, int i1) {
+#pragma unroll
+    for (int i = i0; i < i1; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] = mfma_i8(fa[c][i], fb[c][j], acc[i][j]);
+  };
+  static_assert(SL == 2, "two slices a step, one operand set each");
+
+  for (int s = 0; s < NST && s < nk; ++s) issue(s, s * STAGE);
+  // step 0's DMAs have landed; those of NST - 1 later steps may be in flight
+  if (NST <= nk) wait_vm_le<(NST - 1) * (WDMA + XDMA)>();
+  else wait_vm_le<0>();
+  block_sync();
+  read(0, 0);
+  uint32_t stage = 0;
+  for (int step = 0; step + 1 < nk; ++step) {
+    read(stage, 1);
+    products(0, 0, TI);
+    // this wave has read its stage whole, and so has every wave past the
+    // barrier: the stage is refilled. The next one is ready once its DMAs have
+    // landed (those of NST - 2 later steps may be in flight)
+    if (step + NST - 1 < nk) wait_vm_le<(NST - 2) * (WDMA + XDMA)>();
+    else wait_vm_le<0>();
+    block_sync();
+    const uint32_t next = stage + STAGE == NST * STAGE ? 0 : stage + STAGE;
+    read(next, 0);
+    products(1, 0, 1);
+    if (step + NST < nk) issue(step + NST, stage);
+    products(1, 1, TI);
+    stage = next;
+  }
+  read(stage, 1);
+  products(0, 0, TI);
+  products(1, 0, TI);
+
+  if (SPLIT) {
+    i32x4 *to = g.part + (int64_t)blockIdx.x * (TI * TJ * 64 * NW) + tid;   // [split][tile]
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) to[(i * TJ + j) * 64 * NW] = acc[i][j];
+    return;
+  }
+  block_sync();   // the last operands have been read
+  epilogue<MODE, TI, TJ>(g, acc, (char *)s_t + wave * (TI * TJ * 512), n0 + wn * TI * 16,
+                         m0 + wm * TJ * 16);
+}
+
+// The tiles' sums from their splits, exact in any order, and the epilogue.
+template <int MODE, int BN, int BM, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM) void int8_join_kernel(I8Args g) {
+  constexpr int NW = WN * WM, TI = BN / WN / 16, TJ = BM / WM / 16;
+  __shared__ __align__(1024) uint4 s_t[NW * TI * TJ * 32];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t n0, m0;
+  tile_of<BN, BM>(g, blockIdx.x, n0, m0);
+  i32x4 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  const i32x4 *from = g.part + (int64_t)blockIdx.x * (TI * TJ * 64 * NW) + threadIdx.x;
+#pragma unroll 2
+  for (int y = 0; y < g.S; ++y, from += (int64_t)gridDim.x * (TI * TJ * 64 * NW))
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] += from[(i * TJ + j) * 64 * NW];
+  epilogue<MODE, TI, TJ>(g, acc, (char *)s_t + wave * (TI * TJ * 512), n0 + (wave % WN) * TI * 16,
+                         m0 + (wave / WN) * TJ * 16);
+}
+
+// ---- decode: up to 16 tokens ------------------------------------------------
+// A workgroup of eight waves owns 16 NR rows of the weight and all tokens; a
+// wave takes UN consecutive 64-code chunks of every row at a time and the
+// waves' int32 sums meet in LDS. Bound by the weight's bytes, each read once.
+// The tokens' codes come from L2 as often as there are workgroups, for which
+// two row blocks share them where there are rows enough. Wave w also takes
+// ranks 16 w .. +15 of the rank-r term, whose operands it loads up front.
 struct I8Gemv {
   const int8_t *W;
   const float *sw;
@@ -268,100 +359,174 @@ struct I8Gemv {
   const float *sx;
   int M;
   const uint16_t *B;     // d x r
-  const float *H;        // M x rp
+  const uint16_t *hi, *lo;   // M x rp: s H
   int r, rp;
-  float s;
   uint16_t *Y;           // M x d
 };
 
 constexpr int GV_W = 8;
 
-template <int TB, int UN>
+template <int NR, int UN>
 __global__ __launch_bounds__(64 * GV_W) void int8_gemv_kernel(I8Gemv g) {
-  __shared__ int s_red[GV_W][TB][4][64];
+  __shared__ int s_red[GV_W][NR][4][64];
+  __shared__ float s_lr[GV_W][NR][4][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, grp = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int64_t row = n0 + c16 < g.d ? n0 + c16 : g.d - 1;
-  const int8_t *w = g.W + row * g.k + 16 * grp;
-  const int8_t *x[TB];
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * NR;
+  const int m = c16 < g.M ? c16 : g.M - 1;
+  const int8_t *w[NR], *const x = g.In + m * g.ldi + 16 * grp;
+  int64_t row[NR];
 #pragma unroll
-  for (int b = 0; b < TB; ++b) {
-    const int m = 16 * b + c16 < g.M ? 16 * b + c16 : g.M - 1;
-    x[b] = g.In + m * g.ldi + 16 * grp;
+  for (int b = 0; b < NR; ++b) {
+    row[b] = n0 + 16 * b + c16 < g.d ? n0 + 16 * b + c16 : g.d - 1;
+    w[b] = g.W + row[b] * g.k + 16 * grp;
   }
-  i32x4 acc[TB];
+  // ranks 16 wave .. +15: lanes 0-31 against the high parts, 32-63 the low
+  const bool lr = 16 * wave < g.rp;
+  uint4 lv[NR], sv = ql::zero4();
+  if (lr) {
+    const int t = 16 * wave + 8 * (grp & 1);
+    sv = *(const uint4 *)((grp < 2 ? g.hi : g.lo) + (int64_t)m * g.rp + t);
 #pragma unroll
-  for (int b = 0; b < TB; ++b) acc[b] = i32x4{0, 0, 0, 0};
+    for (int b = 0; b < NR; ++b) {
+      if (g.r % 8 == 0) {
+        lv[b] = t < g.r ? *(const uint4 *)(g.B + row[b] * g.r + t) : ql::zero4();
+      } else {
+        uint32_t e[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const int tc = t + y < g.r ? t + y : g.r - 1;
+          e[y] = g.B[row[b] * g.r + tc];
+          e[y] = t + y < g.r ? e[y] : 0u;
+        }
+        lv[b] = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
+                           e[6] | (e[7] << 16));
+      }
+    }
+  }
+  i32x4 acc[NR];
+#pragma unroll
+  for (int b = 0; b < NR; ++b) acc[b] = i32x4{0, 0, 0, 0};
   const int nc = (int)(g.k >> 6);
-  for (int c = wave; c < nc; c += GV_W * UN) {
-    i32x4 a[UN], v[UN][TB];
+  for (int c = wave * UN; c < nc; c += GV_W * UN) {
+    i32x4 a[UN][NR], v[UN];
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       // chunks past the end: the last one against zeros
-      const int cc = c + u * GV_W, at = 64 * (cc < nc ? cc : nc - 1);
-      a[u] = *(const i32x4 *)(w + at);
+      const int at = 64 * (c + u < nc ? c + u : nc - 1);
 #pragma unroll
-      for (int b = 0; b < TB; ++b) v[u][b] = *(const i32x4 *)(x[b] + at);
+      for (int b = 0; b < NR; ++b) a[u][b] = *(const i32x4 *)(w[b] + at);
+      v[u] = *(const i32x4 *)(x + at);
     }
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      if (c + u * GV_W >= nc) a[u] = i32x4{0, 0, 0, 0};
+      if (c + u >= nc) v[u] = i32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int b = 0; b < TB; ++b)
-        acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], v[u][b], acc[b], 0, 0, 0);
+      for (int b = 0; b < NR; ++b) acc[b] = mfma_i8(a[u][b], v[u], acc[b]);
     }
   }
 #pragma unroll
-  for (int b = 0; b < TB; ++b)
+  for (int b = 0; b < NR; ++b) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) s_red[wave][b][q][lane] = acc[b][q];
+    if (lr) {
+      const f32x4 t = ql::mfma16(lv[b], sv, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s_lr[wave][b][q][lane] = t[q];
+    }
+  }
   __syncthreads();
-  for (int o = threadIdx.x; o < 256 * TB; o += 64 * GV_W) {
-    const int n = o & 15, m = o >> 4, b = m >> 4;
-    if (m >= g.M || n0 + n >= g.d) continue;
+  for (int o = threadIdx.x; o < 256 * NR; o += 64 * GV_W) {
+    const int n = o % (16 * NR), t = o / (16 * NR), b = n >> 4;
+    if (t >= g.M || n0 + n >= g.d) continue;
+    const int q = n & 3, l = 16 * ((n & 15) >> 2) + t;
     int sum = 0;
 #pragma unroll
-    for (int v = 0; v < GV_W; ++v) sum += s_red[v][b][n & 3][16 * (n >> 2) + (m & 15)];
-    float y = (float)sum * g.sx[m] * g.sw[n0 + n];
-    if (g.r) {
-      const uint16_t *bw = g.B + (n0 + n) * g.r;
-      const float *hm = g.H + (int64_t)m * g.rp;
-      float dot = 0.0f;
-      for (int t = 0; t < g.r; ++t) dot = fmaf(hm[t], ql::bf16_to_f(bw[t]), dot);
-      y += g.s * dot;
-    }
-    g.Y[(int64_t)m * g.d + n0 + n] = ql::f_to_bf16(y);
+    for (int v = 0; v < GV_W; ++v) sum += s_red[v][b][q][l];
+    float y = (float)sum * g.sx[t] * g.sw[n0 + n];
+    for (int v = 0; 16 * v < g.rp; ++v) y += s_lr[v][b][q][l];
+    g.Y[(int64_t)t * g.d + n0 + n] = ql::f_to_bf16(y);
   }
+}
+
+// ---- host -----------------------------------------------------------------------
+// Tile and splits of a product of M tokens, N columns, K codes.
+struct I8Plan {
+  int cfg;        // 0: 128 x 256, 1: 128 x 128, 2: 128 x 64 (columns x tokens)
+  int S;
+  int64_t tiles, part;   // part: bytes of partial sums
+};
+I8Plan i8_plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t tn = ql_cdiv(N, 128), nk = ql_cdiv(K, BK);
+  I8Plan best{0, 1, tn * ql_cdiv(M, 256), 0};
+  double least = -1.0;
+  for (int cfg = 0; cfg < 3; ++cfg) {
+    const int64_t bm = cfg == 0 ? 256 : cfg == 1 ? 128 : 64, tiles = tn * ql_cdiv(M, bm);
+    if (cfg == 2 && M > 64) continue;
+    const double step = cfg == 0 ? 0.95 : cfg == 1 ? 0.5 : 0.3;   // us
+    for (int S : {1, 2, 3, 4, 6, 8}) {
+      if (S > 1 && (cfg == 0 || S * 2 > nk)) break;
+      double t = (double)ql_cdiv(tiles * S, 256) * (step * (double)ql_cdiv(nk, S) + 6.0);
+      if (S > 1) t += 3.0 + (double)(S * tiles * bm * 128 * 4) * 2.0 / 5e6;
+      if (least < 0.0 || t < least) {
+        least = t;
+        best = I8Plan{cfg, S, tiles, S > 1 ? S * tiles * bm * 128 * 4 : 0};
+      }
+    }
+  }
+  return best;
+}
+
+template <int MODE, int BM, int WN, int WM, int NST>
+void launch_cfg(const I8Args &g, const I8Plan &p, hipStream_t st) {
+  constexpr int NTH = 64 * WN * WM;
+  if (p.S == 1) {
+    int8_gemm_kernel<MODE, 128, BM, WN, WM, NST, false><<<(unsigned)p.tiles, NTH, 0, st>>>(g);
+  } else {
+    int8_gemm_kernel<MODE, 128, BM, WN, WM, NST, true>
+        <<<(unsigned)(p.tiles * p.S), NTH, 0, st>>>(g);
+    int8_join_kernel<MODE, 128, BM, WN, WM><<<(unsigned)p.tiles, NTH, 0, st>>>(g);
+  }
+}
+
+template <int MODE>
+void launch_mode(const I8Args &g, const I8Plan &p, hipStream_t st) {
+  if (p.cfg == 0)
+    int8_gemm_kernel<MODE, 128, 256, 4, 2, 3, false><<<(unsigned)p.tiles, 512, 0, st>>>(g);
+  else if (p.cfg == 1) launch_cfg<MODE, 128, 4, 2, 4>(g, p, st);
+  else launch_cfg<MODE, 64, 4, 2, 6>(g, p, st);
 }
 
 }  // namespace
 
+size_t int8_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {
+  return (size_t)i8_plan(M, N, K).part;
+}
+
 qlora_status launch_int8_gemm(int mode, const int8_t *W, const float *sw, int64_t d, int64_t k,
                               const int8_t *In, int64_t ldi, const float *sx, int64_t M,
                               const uint16_t *L, const uint16_t *hi, const uint16_t *lo, int r,
-                              int rp, uint16_t *Out, hipStream_t st) {
-  const I8Args g{W, sw, d, k, In, ldi, sx, M, mode == 0 ? d : k, mode == 0 ? k : d,
-                 L, hi, lo, r, rp, Out};
-  const unsigned grid = (unsigned)(ql_cdiv(g.Ntot, 128) * ql_cdiv(M, 256));
+                              int rp, uint16_t *Out, void *part, hipStream_t st) {
+  const int64_t N = mode == 0 ? d : k, K = mode == 0 ? k : d;
+  const I8Plan p = i8_plan(M, N, K);
+  const I8Args g{W, sw, d, k, In, ldi, sx, M, N, K, L, hi, lo, r, rp, Out, p.S, (i32x4 *)part};
   QlProf prof(mode == 0 ? QLORA_K_INT8_GEMM_FWD : QLORA_K_INT8_GEMM_DX, st);
-  if (mode == 0) int8_gemm_kernel<0, 128, 256, 2, 4, 3><<<grid, 512, 0, st>>>(g);
-  else int8_gemm_kernel<1, 128, 256, 2, 4, 3><<<grid, 512, 0, st>>>(g);
+  if (mode == 0) launch_mode<0>(g, p, st);
+  else launch_mode<1>(g, p, st);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
 
 qlora_status launch_int8_gemv(const int8_t *W, const float *sw, int64_t d, int64_t k,
                               const int8_t *In, int64_t ldi, const float *sx, int64_t M,
-                              const uint16_t *B, const float *H, int r, int rp, float s,
-                              uint16_t *Y, hipStream_t st) {
-  const I8Gemv g{W, sw, d, k, In, ldi, sx, (int)M, B, H, r, rp, s, Y};
-  const unsigned grid = (unsigned)ql_cdiv(d, 16);
+                              const uint16_t *B, const uint16_t *hi, const uint16_t *lo, int r,
+                              int rp, uint16_t *Y, hipStream_t st) {
+  const I8Gemv g{W, sw, d, k, In, ldi, sx, (int)M, B, hi, lo, r, rp, Y};
   QlProf prof(QLORA_K_INT8_GEMV, st);
-  if (M <= 16) int8_gemv_kernel<1, 8><<<grid, 64 * GV_W, 0, st>>>(g);
-  else if (M <= 32) int8_gemv_kernel<2, 4><<<grid, 64 * GV_W, 0, st>>>(g);
-  else int8_gemv_kernel<4, 4><<<grid, 64 * GV_W, 0, st>>>(g);
+  // two row blocks a workgroup once one fills the chip twice
+  if (d >= 8192) int8_gemv_kernel<2, 4><<<(unsigned)ql_cdiv(d, 32), 64 * GV_W, 0, st>>>(g);
+  else int8_gemv_kernel<1, 8><<<(unsigned)ql_cdiv(d, 16), 64 * GV_W, 0, st>>>(g);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }

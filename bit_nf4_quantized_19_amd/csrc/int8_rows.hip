@@ -138,7 +138,7 @@ void launch(const RowsArgs &a, hipStream_t st) {
   const int n = a.ldq;
   const unsigned four = (unsigned)ql_cdiv(a.rows, 4), one = (unsigned)a.rows;
   if (n <= 1024) int8_rows_kernel<1, 2, MUL, true><<<four, 256, 0, st>>>(a);
-  else if (n <= 4096) int8_rows_kernel<1, 8, MUL, true><<<four, 256, 0, st>>>(a);
+  else if (n <= 4096) int8_rows_kernel<4, 2, MUL, true><<<one, 256, 0, st>>>(a);
   else if (n <= 8192) int8_rows_kernel<4, 4, MUL, true><<<one, 256, 0, st>>>(a);
   else if (n <= 16384) int8_rows_kernel<4, 8, MUL, true><<<one, 256, 0, st>>>(a);
   else int8_rows_kernel<4, 4, MUL, false><<<one, 256, 0, st>>>(a);

@@ -215,17 +215,19 @@ qlora_status launch_int8_rows(const uint16_t *X, int64_t rows, int64_t cols, con
 // int8_gemm.hip : the product with a d x k record, forward (mode 0) or dX
 // (mode 1). In: M x ldi codes, ldi a multiple of 128, zero past the
 // contraction; sx [M]. L, hi, lo (M x rp), r, rp: the rank-r term as in
-// launch_gemm_fwd / _dx (rp == 0: none).
+// launch_gemm_fwd / _dx (rp == 0: none). part: int8_gemm_part_bytes(M, columns,
+// contraction) bytes of workspace.
+size_t int8_gemm_part_bytes(int64_t M, int64_t N, int64_t K);
 qlora_status launch_int8_gemm(int mode, const int8_t *W, const float *sw, int64_t d, int64_t k,
                               const int8_t *In, int64_t ldi, const float *sx, int64_t M,
                               const uint16_t *L, const uint16_t *hi, const uint16_t *lo, int r,
-                              int rp, uint16_t *Out, hipStream_t st);
-// The forward of up to INT8_GEMV_TOKENS tokens; H (M x rp float32), s on its product.
-constexpr int64_t INT8_GEMV_TOKENS = 64;
+                              int rp, uint16_t *Out, void *part, hipStream_t st);
+// The forward of up to INT8_GEMV_TOKENS tokens.
+constexpr int64_t INT8_GEMV_TOKENS = 16;
 qlora_status launch_int8_gemv(const int8_t *W, const float *sw, int64_t d, int64_t k,
                               const int8_t *In, int64_t ldi, const float *sx, int64_t M,
-                              const uint16_t *B, const float *H, int r, int rp, float s,
-                              uint16_t *Y, hipStream_t st);
+                              const uint16_t *B, const uint16_t *hi, const uint16_t *lo, int r,
+                              int rp, uint16_t *Y, hipStream_t st);
 
 // muon.hip : one orthogonalised momentum step of n matrices
 struct MuonScalars {

@@ -34,6 +34,7 @@ struct MuonArgs {
   uint16_t *out;
   int64_t rows, cols, len;   // len: the longer side
   int R, tall;               // tall: element (i, c) of the short and long side at c R + i
+  int vec;                   // every group of four elements is aligned and whole or absent
   uint32_t magic;            // ceil(2^20 / R): x / R for x < 64 * 128
   int split;                 // workgroups per matrix
   int64_t chunks;            // of CK along the long side
@@ -43,9 +44,19 @@ struct MuonArgs {
 };
 
 constexpr int CK = 64;        // long-side elements of a chunk
-constexpr int US = CK + 4;    // row stride of a chunk in LDS (64 banks: 4 i + k distinct)
 
 template <int NB> constexpr int tiles() { return NB * (NB + 1) / 2; }
+// Row strides of a chunk in LDS, stored as it lies in memory: wide [i][c], tall
+// [c][i]. The matrix cores' operand reads take 16 x 4 elements; the strides put
+// them on 64 different banks: gram reads 16 i by 4 c, apply 4 i by 16 c.
+template <int NB, bool TALL> constexpr int gram_stride() {
+  return !TALL ? CK + 4 : NB == 1 ? 16 : NB <= 5 ? 80 : 144;
+}
+template <int NB, bool TALL> constexpr int apply_stride() { return TALL ? 16 * NB + 4 : CK + 16; }
+template <int NB, bool TALL, int ST> constexpr int chunk_floats() {
+  return TALL ? CK * ST : 16 * NB * ST;
+}
+template <bool TALL, int ST> QL_DEV int place(int i, int c) { return TALL ? c * ST + i : i * ST + c; }
 
 QL_DEV float muon_m(float m, float g, const MuonScalars &s) {
   return __fadd_rn(__fmul_rn(s.beta, m), __fmul_rn(s.c1, g));
@@ -54,54 +65,152 @@ QL_DEV float muon_u(float m, float g, const MuonScalars &s) {   // m: the update
   return s.nesterov ? __fadd_rn(__fmul_rn(s.c1, g), __fmul_rn(s.beta, m)) : m;
 }
 
-// Calls f(offset in the matrix, place in the LDS chunk) for every element of
-// chunk c0 that exists, each by one thread.
-template <class F>
-QL_DEV void for_chunk(const MuonArgs &a, int64_t c0, F f) {
+// A thread's share of a chunk: NB groups of four elements consecutive in
+// memory, group 256 j + thread. Groups run along the rows of a wide matrix
+// (16 a row) and through the chunk of a tall one.
+struct Group {
+  int64_t off;   // of the first element in the matrix
+  int n;         // elements that exist: 0 .. 4
+};
+template <bool TALL>
+QL_DEV Group group_of(const MuonArgs &a, int64_t c0, int j) {
+  const int e = 256 * j + threadIdx.x;
   const int w = (int)(a.len - c0 < CK ? a.len - c0 : CK);
-  if (!a.tall) {
-    for (int e = threadIdx.x; e < a.R * CK; e += blockDim.x) {
-      const int i = e / CK, c = e % CK;
-      if (c < w) f(i * a.cols + c0 + c, i * US + c);
-    }
+  Group q;
+  if (TALL) {
+    q.off = c0 * a.R + 4 * e;
+    q.n = w * a.R - 4 * e;
   } else {
-    for (int e = threadIdx.x; e < a.R * w; e += blockDim.x) {
-      const int c = (int)((uint32_t)e * a.magic >> 20), i = e - c * a.R;
-      f(c0 * a.R + e, i * US + c);
+    const int c = 4 * (e & 15);
+    q.off = (e >> 4) * a.cols + c0 + c;
+    q.n = (e >> 4) < a.R ? w - c : 0;
+  }
+  q.n = q.n < 0 ? 0 : q.n > 4 ? 4 : q.n;
+  return q;
+}
+QL_DEV void load4(const float *p, const Group &q, int vec, float (&v)[4]) {
+  if (vec) {
+    const float4 x = q.n ? *(const float4 *)(p + q.off) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = x < q.n ? p[q.off + x] : 0.0f;
+  }
+}
+QL_DEV void load4(const uint16_t *p, const Group &q, int vec, float (&v)[4]) {
+  if (vec) {
+    const uint2 x = q.n ? *(const uint2 *)(p + q.off) : make_uint2(0u, 0u);
+    v[0] = ql::bf16lo(x.x), v[1] = ql::bf16hi(x.x), v[2] = ql::bf16lo(x.y), v[3] = ql::bf16hi(x.y);
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = x < q.n ? ql::bf16_to_f(p[q.off + x]) : 0.0f;
+  }
+}
+QL_DEV void store4(float *p, const Group &q, int vec, const float (&v)[4]) {
+  if (vec) {
+    if (q.n) *(float4 *)(p + q.off) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (x < q.n) p[q.off + x] = v[x];
+  }
+}
+QL_DEV void store4(uint16_t *p, const Group &q, int vec, const float (&v)[4]) {
+  if (vec) {
+    if (q.n)
+      *(uint2 *)(p + q.off) =
+          make_uint2(ql::pack_bf16x2(v[0], v[1]), ql::pack_bf16x2(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (x < q.n) p[q.off + x] = ql::f_to_bf16(v[x]);
+  }
+}
+// The group's places in the LDS chunk (absent elements of the chunk too: they
+// hold zeros), as one 16-byte access where they are consecutive.
+template <bool TALL, int ST, class F4, class F1>
+QL_DEV void in_lds(const MuonArgs &a, int j, F4 four, F1 one) {
+  const int e = 256 * j + threadIdx.x;
+  if (e >= 16 * a.R) return;
+  if (!TALL) {
+    four(place<TALL, ST>(e >> 4, 4 * (e & 15)));
+  } else {
+    const uint32_t f = 4 * e;
+    const int c = (int)(f * a.magic >> 20), i = (int)f - c * a.R;
+    if ((a.R & 3) == 0) {
+      four(place<TALL, ST>(i, c));
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t fx = f + x;
+        const int cx = (int)(fx * a.magic >> 20);
+        one(place<TALL, ST>((int)fx - cx * a.R, cx), x);
+      }
     }
   }
 }
+template <bool TALL, int ST>
+QL_DEV void put4(const MuonArgs &a, int j, float *s, const float (&v)[4]) {
+  in_lds<TALL, ST>(a, j, [&](int at) { *(float4 *)(s + at) = make_float4(v[0], v[1], v[2], v[3]); },
+                   [&](int at, int x) { s[at] = v[x]; });
+}
+template <bool TALL, int ST>
+QL_DEV void get4(const MuonArgs &a, int j, const float *s, float (&v)[4]) {
+  in_lds<TALL, ST>(a, j, [&](int at) {
+    const float4 x = *(const float4 *)(s + at);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+  }, [&](int at, int x) { v[x] = s[at]; });
+}
 
-template <int NB>
+template <int NB, bool TALL>
 __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs a) {
-  __shared__ float s_u[16 * NB * US];
-  const int lane = threadIdx.x & 63;
+  constexpr int ST = gram_stride<NB, TALL>(), LN = chunk_floats<NB, TALL, ST>();
+  __shared__ __align__(16) float s_u[LN];
+  const int lane = threadIdx.x & 63, c16 = lane & 15, k4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t mat = blockIdx.y, base = mat * a.rows * a.cols;
   const int64_t lo = blockIdx.x * a.chunks / a.split, hi = (blockIdx.x + 1) * a.chunks / a.split;
+  float *const m = a.m + base;
+  const uint16_t *const g = a.g + base;
   // few tiles: the waves share the chunk's columns; many: the tiles
   constexpr bool BYK = NB < 4;
   constexpr int NT = tiles<NB>(), MY = BYK ? NT : (NT + 3) / 4;
   f64x4 acc[MY];
 #pragma unroll
   for (int t = 0; t < MY; ++t) acc[t] = f64x4{0.0, 0.0, 0.0, 0.0};
+  // the padding of the smaller side stays zero
+  for (int e = threadIdx.x; e < LN; e += 256) s_u[e] = 0.0f;
+  float mv[NB][4], gv[NB][4];
+  auto fetch = [&](int64_t ch) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const Group q = group_of<TALL>(a, ch * CK, j);
+      load4(m, q, a.vec, mv[j]);
+      load4(g, q, a.vec, gv[j]);
+    }
+  };
+  fetch(lo);
   for (int64_t ch = lo; ch < hi; ++ch) {
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * NB * US; e += 256) s_u[e] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      float u[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        mv[j][x] = muon_m(mv[j][x], gv[j][x], a.s);
+        u[x] = muon_u(mv[j][x], gv[j][x], a.s);
+      }
+      put4<TALL, ST>(a, j, s_u, u);
+      store4(m, group_of<TALL>(a, ch * CK, j), a.vec, mv[j]);
+    }
     __syncthreads();
-    for_chunk(a, ch * CK, [&](int64_t off, int at) {
-      const float g = ql::bf16_to_f(a.g[base + off]);
-      const float m = muon_m(a.m[base + off], g, a.s);
-      a.m[base + off] = m;
-      s_u[at] = muon_u(m, g, a.s);
-    });
-    __syncthreads();
+    if (ch + 1 < hi) fetch(ch + 1);   // under this chunk's products
 #pragma unroll
     for (int s = 0; s < (BYK ? 4 : 16); ++s) {
-      const int k = 4 * (BYK ? 4 * wave + s : s) + (lane >> 4);
+      const int k = 4 * (BYK ? 4 * wave + s : s) + k4;
       double u[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) u[b] = (double)s_u[(16 * b + (lane & 15)) * US + k];
+      for (int b = 0; b < NB; ++b) u[b] = (double)s_u[place<TALL, ST>(16 * b + c16, k)];
       int t = 0;
 #pragma unroll
       for (int i = 0; i < NB; ++i)
@@ -112,34 +221,80 @@ __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs a) {
         }
     }
   }
-  double *part = a.part + ((mat * a.split + blockIdx.x) * (BYK ? 4 : 1)) * NT * 256;
+  double *part = a.part + (mat * a.split + blockIdx.x) * NT * 256;
+  if (BYK) {   // the waves' sums, in their order
+    double *red = (double *)s_u;
+    static_assert(!BYK || NT * 256 * 8 <= LN * 4, "the chunk's LDS holds the tiles");
+    for (int w = 0; w < 4; ++w) {
+      __syncthreads();
+      if (wave != w) continue;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    if (!BYK && t % 4 != wave) continue;
-    double *to = part + ((BYK ? wave * NT : 0) + t) * 256;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) to[q * 64 + lane] = acc[BYK ? t : t / 4][q];
+        for (int q = 0; q < 4; ++q) {
+          const int at = t * 256 + q * 64 + lane;
+          const double v = w ? red[at] + acc[t][q] : acc[t][q];
+          if (w < 3) red[at] = v;
+          else part[at] = v;
+        }
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (t % 4 == wave)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) part[t * 256 + q * 64 + lane] = acc[t / 4][q];
   }
 }
 
+// Threads of the iterate kernel: a wave per 16 columns, and more to join the
+// partial sums (the others wait).
+template <int NB> constexpr int iterate_threads() { return NB == 1 ? 1024 : 512; }
+
 template <int NB>
-__global__ __launch_bounds__(64 * NB) void muon_iterate_kernel(MuonArgs a) {
-  constexpr int RP = 16 * NB, LS = RP + 2, NT = tiles<NB>();
+__global__ __launch_bounds__(iterate_threads<NB>()) void muon_iterate_kernel(MuonArgs a) {
+  constexpr int RP = 16 * NB, LS = RP + 2, NT = tiles<NB>(), NTH = iterate_threads<NB>();
   __shared__ double s_a[RP * LS];
+  __shared__ double s_j[NB == 1 ? 4 * 256 : 1];
   __shared__ double s_tr;
   const int lane = threadIdx.x & 63, c16 = lane & 15, k4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t mat = blockIdx.x;
-  const int np = a.split * (NB < 4 ? 4 : 1);
-  const double *part = a.part + mat * np * NT * 256;
-  for (int e = threadIdx.x; e < NT * 256; e += 64 * NB) {
+  const double *part = a.part + mat * a.split * NT * 256;
+  auto join = [&](int e, int x0, int x1) {   // partial sums x0 .. x1 - 1 of element e
     double v = 0.0;
-    for (int x = 0; x < np; ++x) v += part[(int64_t)x * NT * 256 + e];
+    int x = x0;
+    for (; x + 16 <= x1; x += 16) {
+      double y[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = part[(int64_t)(x + i) * NT * 256 + e];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v += y[i];
+    }
+    double y[15];
+#pragma unroll
+    for (int i = 0; i < 15; ++i) y[i] = x + i < x1 ? part[(int64_t)(x + i) * NT * 256 + e] : 0.0;
+#pragma unroll
+    for (int i = 0; i < 15; ++i) v += y[i];
+    return v;
+  };
+  auto place_sum = [&](int e, double v) {
     int t = e >> 8, i = 0;
     while (t >= NB - i) t -= NB - i, ++i;
     const int row = 16 * i + 4 * ((e >> 6) & 3) + ((e & 63) >> 4), col = 16 * (i + t) + (e & 15);
     s_a[row * LS + col] = v;
     if (t) s_a[col * LS + row] = v;
+  };
+  if (NB == 1) {   // four quarters of the partial sums at once
+    const int y = threadIdx.x >> 8;
+    s_j[threadIdx.x] = join(threadIdx.x & 255, y * a.split / 4, (y + 1) * a.split / 4);
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      const int e = threadIdx.x;
+      place_sum(e, s_j[e] + s_j[256 + e] + s_j[512 + e] + s_j[768 + e]);
+    }
+  } else {
+    for (int e = threadIdx.x; e < NT * 256; e += NTH) place_sum(e, join(e, 0, a.split));
   }
   __syncthreads();
   if (wave == 0) {
@@ -150,15 +305,16 @@ __global__ __launch_bounds__(64 * NB) void muon_iterate_kernel(MuonArgs a) {
   }
   __syncthreads();
   const double inv = 1.0 / (sqrt(s_tr) + a.s.eps);
-  for (int e = threadIdx.x; e < RP * LS; e += 64 * NB) s_a[e] *= inv * inv;
+  for (int e = threadIdx.x; e < RP * LS; e += NTH) s_a[e] *= inv * inv;
   __syncthreads();
 
-  // wave w holds columns 16 w .. +15 of S and Q as B operands
+  // wave w < NB holds columns 16 w .. +15 of S and Q as B operands
+  const bool on = wave < NB;
   double sp[NB * 4], qp[NB * 4];
 #pragma unroll
   for (int x = 0; x < NB * 4; ++x) {
     const int row = 4 * x + k4, col = 16 * wave + c16;
-    sp[x] = s_a[row * LS + col];
+    sp[x] = on ? s_a[row * LS + col] : 0.0;
     qp[x] = row == col ? 1.0 : 0.0;
   }
   auto times = [&](const double (&in)[NB * 4], double (&out)[NB * 4]) {   // (LDS matrix) * in
@@ -166,10 +322,13 @@ __global__ __launch_bounds__(64 * NB) void muon_iterate_kernel(MuonArgs a) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) d[b] = f64x4{0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-    for (int x = 0; x < NB * 4; ++x)
+    for (int x = 0; x < NB * 4; ++x) {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         d[b] = mfma_f64(s_a[(16 * b + c16) * LS + 4 * x + k4], in[x], d[b]);
+      // keeps the operands of later steps out of registers that three panels fill
+      if (NB > 4) __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -177,71 +336,130 @@ __global__ __launch_bounds__(64 * NB) void muon_iterate_kernel(MuonArgs a) {
   };
   auto store = [&](const double (&v)[NB * 4]) {
     __syncthreads();
+    if (on)
 #pragma unroll
-    for (int x = 0; x < NB * 4; ++x) s_a[(4 * x + k4) * LS + 16 * wave + c16] = v[x];
+      for (int x = 0; x < NB * 4; ++x) s_a[(4 * x + k4) * LS + 16 * wave + c16] = v[x];
     __syncthreads();
   };
 #pragma clang loop unroll(disable)
   for (int step = 0; step < a.s.steps; ++step) {
     double t[NB * 4];
-    times(sp, t);
-#pragma unroll
-    for (int x = 0; x < NB * 4; ++x)
-      t[x] = (4 * x + k4 == 16 * wave + c16 ? a.s.a : 0.0) + a.s.b * sp[x] + a.s.c * t[x];
-    store(t);
-    times(qp, qp);
-    if (step + 1 < a.s.steps) {
+    if (on) {
       times(sp, t);
-      times(t, sp);
-      store(sp);
+#pragma unroll
+      for (int x = 0; x < NB * 4; ++x)
+        t[x] = (4 * x + k4 == 16 * wave + c16 ? a.s.a : 0.0) + a.s.b * sp[x] + a.s.c * t[x];
     }
+    store(t);
+    const bool more = step + 1 < a.s.steps;
+    if (on) {
+      if (step == 0) {
+#pragma unroll
+        for (int x = 0; x < NB * 4; ++x) qp[x] = t[x];
+      } else {
+        times(qp, qp);
+      }
+      if (more) {
+        times(sp, t);
+        times(t, sp);
+      }
+    }
+    if (more) store(sp);
   }
   double *Q = a.Q + mat * RP * RP;
+  if (on)
 #pragma unroll
-  for (int x = 0; x < NB * 4; ++x) Q[(4 * x + k4) * RP + 16 * wave + c16] = qp[x] * inv;
+    for (int x = 0; x < NB * 4; ++x) Q[(4 * x + k4) * RP + 16 * wave + c16] = qp[x] * inv;
 }
 
-template <int NB>
+template <int NB, bool TALL>
 __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
-  constexpr int RP = 16 * NB;
-  __shared__ float s_u[RP * US];
+  constexpr int RP = 16 * NB, ST = apply_stride<NB, TALL>(), LN = chunk_floats<NB, TALL, ST>();
+  __shared__ __align__(16) float s_u[LN];
   const int lane = threadIdx.x & 63, c16 = lane & 15, k4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t mat = blockIdx.y, base = mat * a.rows * a.cols;
-  const double *Q = a.Q + mat * RP * RP;
   const int64_t lo = blockIdx.x * a.chunks / a.split, hi = (blockIdx.x + 1) * a.chunks / a.split;
+  float *const p = a.p + base;
+  const float *const m = a.m + base;
+  const uint16_t *const g = a.g + base;
+  uint16_t *const out = a.out + base;
+  // The wave's rows of Q stay in registers. Up to three row blocks: all of
+  // them, times 16 of the chunk's columns; more: every fourth row block, times
+  // all columns.
+  constexpr bool BYC = NB < 4;
+  constexpr int RB = BYC ? NB : (NB + 3) / 4, CB = BYC ? 1 : CK / 16;
+  double q[RB][NB * 4];
+  {
+    const double *Q = a.Q + mat * RP * RP;
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const int b = BYC ? r : wave + 4 * r < NB ? wave + 4 * r : wave;   // Q is symmetric up to
+#pragma unroll
+      for (int x = 0; x < NB * 4; ++x) q[r][x] = Q[(4 * x + k4) * RP + 16 * b + c16];   // rounding
+    }
+  }
+  for (int e = threadIdx.x; e < LN; e += 256) s_u[e] = 0.0f;
+  float mv[NB][4], gv[NB][4], pv[NB][4];
+  auto fetch = [&](int64_t ch) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const Group x = group_of<TALL>(a, ch * CK, j);
+      load4(m, x, a.vec, mv[j]);
+      load4(g, x, a.vec, gv[j]);
+    }
+  };
+  fetch(lo);
   for (int64_t ch = lo; ch < hi; ++ch) {
     __syncthreads();
-    for (int e = threadIdx.x; e < RP * US; e += 256) s_u[e] = 0.0f;
-    __syncthreads();
-    for_chunk(a, ch * CK, [&](int64_t off, int at) {
-      s_u[at] = muon_u(a.m[base + off], ql::bf16_to_f(a.g[base + off]), a.s);
-    });
-    __syncthreads();
-    // wave w: columns 16 w .. +15 of the chunk, all rows
-    f64x4 d[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) d[b] = f64x4{0.0, 0.0, 0.0, 0.0};
-    for (int x = 0; x < NB * 4; ++x) {
-      const double u = (double)s_u[(4 * x + k4) * US + 16 * wave + c16];
+    for (int j = 0; j < NB; ++j) {
+      float u[4];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)   // Q is symmetric up to rounding: read by columns
-        d[b] = mfma_f64(Q[(int64_t)(4 * x + k4) * RP + 16 * b + c16], u, d[b]);
+      for (int x = 0; x < 4; ++x) u[x] = muon_u(mv[j][x], gv[j][x], a.s);
+      put4<TALL, ST>(a, j, s_u, u);
+      load4((const float *)p, group_of<TALL>(a, ch * CK, j), a.vec, pv[j]);
     }
     __syncthreads();
+    if (ch + 1 < hi) fetch(ch + 1);   // under this chunk's products
+    f64x4 d[CB][RB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int c = 0; c < CB; ++c)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        s_u[(16 * b + 4 * q + k4) * US + 16 * wave + c16] = (float)d[b][q];
+      for (int r = 0; r < RB; ++r) d[c][r] = f64x4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+    for (int x = 0; x < NB * 4; ++x)
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        const double u = (double)s_u[place<TALL, ST>(4 * x + k4, 16 * (BYC ? wave : c) + c16)];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) d[c][r] = mfma_f64(q[r][x], u, d[c][r]);
+      }
     __syncthreads();
-    for_chunk(a, ch * CK, [&](int64_t off, int at) {
-      const float p = a.p[base + off];
-      const float dir = __fadd_rn(__fmul_rn(a.s.scale, s_u[at]), __fmul_rn(a.s.wd, p));
-      const float q = __fsub_rn(p, __fmul_rn(a.s.lr, dir));
-      a.p[base + off] = q;
-      a.out[base + off] = ql::f_to_bf16(q);
-    });
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        const int b = BYC ? r : wave + 4 * r;
+        if (b >= NB) continue;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          s_u[place<TALL, ST>(16 * b + 4 * x + k4, 16 * (BYC ? wave : c) + c16)] = (float)d[c][r][x];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const Group x = group_of<TALL>(a, ch * CK, j);
+      float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      get4<TALL, ST>(a, j, s_u, o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float dir = __fadd_rn(__fmul_rn(a.s.scale, o[i]), __fmul_rn(a.s.wd, pv[j][i]));
+        o[i] = __fsub_rn(pv[j][i], __fmul_rn(a.s.lr, dir));
+      }
+      store4(p, x, a.vec, o);
+      store4(out, x, a.vec, o);
+    }
   }
 }
 
@@ -255,11 +473,10 @@ MuonPlan muon_plan(int64_t n, int64_t rows, int64_t cols) {
   p.len = rows < cols ? cols : rows;
   p.NB = (int)ql_cdiv(p.R, 16);
   p.chunks = ql_cdiv(p.len, CK);
-  int64_t s = ql_cdiv(1024, n);
+  int64_t s = n < 1024 ? 1024 / n : 1;   // about four workgroups a compute unit
   s = s < p.chunks ? s : p.chunks;
   p.split = (int)s;
-  const int64_t np = s * (p.NB < 4 ? 4 : 1);
-  p.part = ql_rup(n * np * (p.NB * (p.NB + 1) / 2) * 2048, 256);
+  p.part = ql_rup(n * s * (p.NB * (p.NB + 1) / 2) * 2048, 256);
   p.q = ql_rup(n * p.NB * p.NB * 2048, 256);
   return p;
 }
@@ -267,9 +484,11 @@ MuonPlan muon_plan(int64_t n, int64_t rows, int64_t cols) {
 template <int NB>
 void launch_nb(const MuonArgs &a, unsigned n, hipStream_t st) {
   const dim3 grid((unsigned)a.split, n);
-  muon_gram_kernel<NB><<<grid, 256, 0, st>>>(a);
-  muon_iterate_kernel<NB><<<n, 64 * NB, 0, st>>>(a);
-  muon_apply_kernel<NB><<<grid, 256, 0, st>>>(a);
+  if (a.tall) muon_gram_kernel<NB, true><<<grid, 256, 0, st>>>(a);
+  else muon_gram_kernel<NB, false><<<grid, 256, 0, st>>>(a);
+  muon_iterate_kernel<NB><<<n, iterate_threads<NB>(), 0, st>>>(a);
+  if (a.tall) muon_apply_kernel<NB, true><<<grid, 256, 0, st>>>(a);
+  else muon_apply_kernel<NB, false><<<grid, 256, 0, st>>>(a);
 }
 
 }  // namespace
@@ -284,7 +503,7 @@ qlora_status launch_muon(float *p, float *m, const uint16_t *g, uint16_t *out, i
                          hipStream_t st) {
   const MuonPlan pl = muon_plan(n, rows, cols);
   const MuonArgs a{p, m, g, out, rows, cols, pl.len, pl.R, rows > cols,
-                   (uint32_t)((1u << 20) + pl.R - 1) / (uint32_t)pl.R, pl.split, pl.chunks,
+                   (rows > cols ? rows * cols : cols) % 4 == 0, (uint32_t)((1u << 20) + pl.R - 1) / (uint32_t)pl.R, pl.split, pl.chunks,
                    (double *)ws, (double *)((char *)ws + pl.part), s};
   QlProf prof(QLORA_K_MUON, st);
   switch (pl.NB) {

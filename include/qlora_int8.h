@@ -71,8 +71,8 @@ QLORA_API size_t qlora_int8_workspace_bytes(int32_t op, int64_t d, int64_t k, in
 /*
  * Forward: Y (M x d, bf16) of X (M x k, bf16). 1 <= r <= 128, or r == 0 with A,
  * B and H_save NULL for the product alone (a merged weight). If H_save is
- * non-NULL it receives H (M x r float32) for the backward. Up to 64 tokens
- * run the memory-bound decode kernels, more the integer GEMM.
+ * non-NULL it receives H (M x r float32) for the backward. Up to 16 tokens
+ * run the memory-bound decode kernel, more the integer GEMM.
  */
 QLORA_API qlora_status qlora_linear_fwd_int8(const qlora_int8_weight *w, const uint16_t *X,
                                              int64_t M, const uint16_t *A, const uint16_t *B,
