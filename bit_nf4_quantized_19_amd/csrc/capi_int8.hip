@@ -55,7 +55,7 @@ struct BwdWs {
   int8_t *q;           // M x ldq codes of dY sw
   float *se, *H, *G, *cpart;
   void *part;
-  uint16_t *Bt, *hi, *lo;
+  uint16_t *At, *Bt, *hi, *lo;
   int64_t ldq, bytes;
 };
 // sized for the largest case (H recomputed, dX requested)
@@ -71,7 +71,8 @@ BwdWs bwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
     L.G = c.take<float>(M * rp * 4);
     L.hi = c.take<uint16_t>(M * rp * 2);
     L.lo = c.take<uint16_t>(M * rp * 2);
-    L.Bt = (r % 16) ? c.take<uint16_t>((int64_t)rp * d * 2) : nullptr;
+    L.At = c.take<uint16_t>((int64_t)rp * k * 2);
+    L.Bt = c.take<uint16_t>((int64_t)rp * d * 2);
     L.cpart = c.take<float>((int64_t)colacc_part_bytes(M, d, k, rp));
   }
   L.part = c.take<void>((int64_t)int8_gemm_part_bytes(M, k, d));
@@ -117,14 +118,14 @@ qlora_status qlora_linear_fwd_int8(const qlora_int8_weight *w, const uint16_t *X
   hipStream_t st = (hipStream_t)stream;
   const int rp = (int)ql_rup(r, 16);
   const float sc = r ? lora_alpha / (float)r : 0.0f;
-  if ((s = launch_int8_rows(X, M, k, nullptr, L.q, L.ldq, L.sx, st)) != QLORA_OK) return s;
-  if (r && (s = launch_skinny(X, M, k, A, false, r, rp, L.H, H_save, r, sc, L.hi, L.lo, st)) !=
-               QLORA_OK)
-    return s;
+  const Int8Rank rank{A, r, r, rp, L.H, H_save, L.hi, L.lo, sc, nullptr, 0};
+  s = r ? launch_int8_prep(X, M, k, nullptr, L.q, L.ldq, L.sx, rank, st)
+        : launch_int8_rows(X, M, k, nullptr, L.q, L.ldq, L.sx, st);
+  if (s != QLORA_OK) return s;
   if (M <= INT8_GEMV_TOKENS)
     return launch_int8_gemv(w->codes, w->scale, d, k, L.q, L.ldq, L.sx, M, B, L.hi, L.lo, r, rp, Y,
                             st);
-  return launch_int8_gemm(0, w->codes, w->scale, d, k, L.q, L.ldq, L.sx, M, B, L.hi, L.lo, r, rp,
+  return launch_int8_gemm(0, w->codes, w->scale, d, k, L.q, L.ldq, L.sx, M, B, r, L.hi, L.lo, rp,
                           Y, L.part, st);
 }
 
@@ -150,24 +151,24 @@ qlora_status qlora_linear_bwd_int8(const qlora_int8_weight *w, const uint16_t *X
   const int rp = (int)ql_rup(r, 16);
   const float sc = r ? lora_alpha / (float)r : 0.0f;
   if (r) {
-    if (!H || r % 16) {   // H as M x rp
-      if ((s = launch_skinny(X, M, k, A, false, r, rp, L.H, nullptr, 0, sc, nullptr, nullptr,
-                             st)) != QLORA_OK)
+    // B^T for G and A^T for dX, which are read by rows, and H as M x rp
+    const float *pad = r % 16 ? H : nullptr;
+    if ((s = launch_int8_layout(A, B, d, k, r, rp, L.At, L.Bt, pad, M, L.H, st)) != QLORA_OK)
+      return s;
+    if (pad) {
+      H = L.H;
+    } else if (!H) {
+      const Int8Rank rank{A, r, r, rp, L.H, nullptr, nullptr, nullptr, sc, nullptr, 0};
+      if ((s = launch_int8_prep(X, M, k, nullptr, nullptr, 0, nullptr, rank, st)) != QLORA_OK)
         return s;
       H = L.H;
     }
-    // G = dY B and s G as bf16 hi/lo; the launch also clears the counters of
-    // the gradients' launch. B is read in place, or from a padded B^T
-    int *cnt = colacc_counters(L.cpart, M, d, k, rp);
-    const int64_t ncnt = colacc_counter_count(d, k);
-    const uint16_t *P = B;
-    if (r % 16) {
-      const LayoutReq req[1] = {{B, d, r, L.Bt, rp, d, 1}};
-      if ((s = launch_layout(req, 1, st)) != QLORA_OK) return s;
-      P = L.Bt;
-    }
-    if ((s = launch_skinny(dY, M, d, P, r % 16 == 0, rp, rp, L.G, nullptr, 0, sc, L.hi, L.lo, st,
-                           cnt, ncnt)) != QLORA_OK)
+    // G = dY B, s G as bf16 hi/lo and the record of dY sw; the launch also
+    // clears the counters of the gradients' launch
+    const Int8Rank rank{L.Bt, rp, r, rp, L.G, nullptr, L.hi, L.lo, sc,
+                        colacc_counters(L.cpart, M, d, k, rp), colacc_counter_count(d, k)};
+    if ((s = launch_int8_prep(dY, M, d, w->scale, dX ? L.q : nullptr, L.ldq, L.se, rank, st)) !=
+        QLORA_OK)
       return s;
     const DropParams none{0u, 0u, 0u, 1.0f, 0};
     if ((s = launch_colacc2(ColaccReq{dY, d, H, dB, 0, none, nullptr},
@@ -176,9 +177,9 @@ qlora_status qlora_linear_bwd_int8(const qlora_int8_weight *w, const uint16_t *X
       return s;
   }
   if (!dX) return QLORA_OK;
-  if ((s = launch_int8_rows(dY, M, d, w->scale, L.q, L.ldq, L.se, st)) != QLORA_OK) return s;
-  return launch_int8_gemm(1, w->codes, w->scale, d, k, L.q, L.ldq, L.se, M, A, L.hi, L.lo, r, rp,
-                          dX, L.part, st);
+  if (!r && (s = launch_int8_rows(dY, M, d, w->scale, L.q, L.ldq, L.se, st)) != QLORA_OK) return s;
+  return launch_int8_gemm(1, w->codes, w->scale, d, k, L.q, L.ldq, L.se, M, L.At, rp, L.hi, L.lo,
+                          rp, dX, L.part, st);
 }
 
 }  // extern "C"

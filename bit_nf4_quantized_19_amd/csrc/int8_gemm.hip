@@ -23,9 +23,10 @@ struct I8Args {
   int64_t ldi;           // a multiple of 128
   const float *sx;       // [M]
   int64_t M, Ntot, Ktot;
-  const uint16_t *L;     // rank-r term: B (d x r) or A (r x k)
+  const uint16_t *L;     // rank-r term: Ntot x ldl, zero past r where ldl > r
+  int ldl;
   const uint16_t *Shi, *Slo;   // M x rp
-  int r, rp;
+  int rp;
   uint16_t *Out;         // M x Ntot
   int S;                 // workgroups that share a tile's K-steps
   i32x4 *part;           // S > 1: their sums, [split][tile][block][thread]
@@ -88,85 +89,113 @@ QL_DEV void tile_of(const I8Args &g, uint32_t bid, int64_t &n0, int64_t &m0) {
   m0 = (int64_t)(g0 + in % gm) * BM;
 }
 
-// A wave's 16 TI x 16 TJ block at column n0, token m0: scales, then the rank-r
-// term on the float32 values, rounded once to bf16. The block goes through the
-// wave's TI * TJ * 512 bytes of LDS, so that whole lines of 128 bytes are
-// stored: 8-byte stores of the lanes' four columns took 7 us more for 2048 x
-// 4096 outputs.
+// What the epilogue of a wave's 16 TI x 16 TJ block at column n0, token m0 reads:
+// scales and the operands of 16 ranks, loaded under the last products. Lanes
+// 0-31 take s H's high parts, lanes 32-63 its low parts, against the same rows
+// of L.
 template <int MODE, int TI, int TJ>
-QL_DEV void epilogue(const I8Args &g, const i32x4 (&acc)[TI][TJ], char *blk, int64_t n0,
-                     int64_t m0) {
-  const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4;
+struct EpilogueIn {
   float sx[TJ];
-  int64_t mrow[TJ];
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    const int64_t m = m0 + j * 16 + c16;
-    mrow[j] = m < g.M ? m : g.M - 1;
-    sx[j] = g.sx[mrow[j]];
-  }
-  constexpr int WB = TI * 32, CPW = WB / 16;   // bytes and chunks of a block's row
-  static_assert((CPW & (CPW - 1)) == 0, "a power of two");
-#pragma unroll
-  for (int i = 0; i < TI; ++i) {
-    const int64_t nb = n0 + i * 16;
-    f32x4 v[TJ];
-    float4 sw = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-    if (MODE == 0) {
-      const int64_t n = nb + 4 * grp;
-      sw = *(const float4 *)(g.sw + (n < g.d ? n : g.d - 4));
-    }
+  float4 sw[TI];
+  uint4 l[TI], s[TJ];
+
+  QL_DEV void ranks(const I8Args &g, int64_t n0, int64_t m0, int t0) {
+    const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4, t = t0 + 8 * (grp & 1);
+    const uint16_t *S = grp < 2 ? g.Shi : g.Slo;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      const float w[4] = {sw.x, sw.y, sw.z, sw.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float f = (float)acc[i][j][q] * sx[j];
-        v[j][q] = MODE == 0 ? f * w[q] : f;
-      }
+      const int64_t m = m0 + 16 * j + c16;
+      s[j] = *(const uint4 *)(S + (m < g.M ? m : g.M - 1) * g.rp + t);
     }
-    // 16 ranks at a time: lanes 0-31 take s H's high parts, lanes 32-63 its low
-    // parts, against the same rows of L
-    const uint16_t *S = grp < 2 ? g.Shi : g.Slo;
-    int64_t n = nb + c16;
-    n = n < g.Ntot ? n : g.Ntot - 1;
-    for (int t0 = 0; t0 < g.rp; t0 += 16) {
-      const int t = t0 + 8 * (grp & 1);
-      uint4 l;
-      if (MODE == 0 && g.r % 8 == 0) {
-        l = t < g.r ? *(const uint4 *)(g.L + n * g.r + t) : ql::zero4();
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      int64_t n = n0 + 16 * i + c16;
+      n = n < g.Ntot ? n : g.Ntot - 1;
+      if (g.ldl % 8 == 0) {
+        l[i] = t < g.ldl ? *(const uint4 *)(g.L + n * g.ldl + t) : ql::zero4();
       } else {
         uint32_t e[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const int tc = t + x < g.r ? t + x : g.r - 1;
-          e[x] = g.L[MODE == 0 ? n * g.r + tc : tc * g.Ntot + n];
-          e[x] = t + x < g.r ? e[x] : 0u;
+          const int tc = t + x < g.ldl ? t + x : g.ldl - 1;
+          e[x] = g.L[n * g.ldl + tc];
+          e[x] = t + x < g.ldl ? e[x] : 0u;
         }
-        l = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
-                       e[6] | (e[7] << 16));
+        l[i] = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
+                          e[6] | (e[7] << 16));
       }
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        v[j] = ql::mfma16(l, *(const uint4 *)(S + mrow[j] * g.rp + t), v[j]);
     }
-    // row j * 16 + c16 of the block, columns 16 i + 4 grp .. +3, the row's
-    // 16-byte chunks permuted by the row
+  }
+  QL_DEV void load(const I8Args &g, int64_t n0, int64_t m0) {
+    const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int64_t m = m0 + 16 * j + c16;
+      sx[j] = g.sx[m < g.M ? m : g.M - 1];
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int64_t n = n0 + 16 * i + 4 * grp;
+      sw[i] = MODE == 0 ? *(const float4 *)(g.sw + (n < g.d ? n : g.d - 4))
+                        : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    }
+    if (g.rp) ranks(g, n0, m0, 0);
+  }
+};
+
+// The block's scales, then the rank-r term on the float32 values, rounded once
+// to bf16. The block goes through the wave's TI * TJ * 512 bytes of LDS, so
+// that whole lines of 128 bytes are stored: 8-byte stores of the lanes' four
+// columns took 7 us more for 2048 x 4096 outputs.
+template <int MODE, int TI, int TJ>
+QL_DEV void epilogue(const I8Args &g, const i32x4 (&acc)[TI][TJ], EpilogueIn<MODE, TI, TJ> &in,
+                     char *blk, int64_t n0, int64_t m0) {
+  const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4;
+  constexpr int WB = TI * 32, CPW = WB / 16;   // bytes and chunks of a block's row
+  static_assert((CPW & (CPW - 1)) == 0, "a power of two");
+  f32x4 v[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const float w[4] = {in.sw[i].x, in.sw[i].y, in.sw[i].z, in.sw[i].w};
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float f = (float)acc[i][j][q] * in.sx[j];
+        v[i][j][q] = MODE == 0 ? f * w[q] : f;
+      }
+  }
+  for (int t0 = 0; t0 < g.rp; t0 += 16) {
+    uint4 l[TI], sv[TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i) l[i] = in.l[i];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) sv[j] = in.s[j];
+    if (t0 + 16 < g.rp) in.ranks(g, n0, m0, t0 + 16);
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) v[i][j] = ql::mfma16(l[i], sv[j], v[i][j]);
+  }
+  // row j * 16 + c16 of the block, columns 16 i + 4 grp .. +3, the row's 16-byte
+  // chunks permuted by the row
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int row = 16 * j + c16, c = (2 * i + (grp >> 1)) ^ (c16 & (CPW - 1));
       *(uint2 *)(blk + row * WB + 16 * c + 8 * (grp & 1)) =
-          make_uint2(ql::pack_bf16x2(v[j][0], v[j][1]), ql::pack_bf16x2(v[j][2], v[j][3]));
+          make_uint2(ql::pack_bf16x2(v[i][j][0], v[i][j][1]),
+                     ql::pack_bf16x2(v[i][j][2], v[i][j][3]));
     }
-  }
   __builtin_amdgcn_s_waitcnt(0xC07F);
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int x = 0; x < TJ * 16 * CPW / 64; ++x) {
     const int row = x * (64 / CPW) + lane / CPW, c = lane % CPW;
-    const uint4 v = *(const uint4 *)(blk + row * WB + 16 * (c ^ (row & 15 & (CPW - 1))));
+    const uint4 o = *(const uint4 *)(blk + row * WB + 16 * (c ^ (row & 15 & (CPW - 1))));
     const int64_t m = m0 + row, n = n0 + 8 * c;
-    if (m < g.M && n < g.Ntot) *(uint4 *)(g.Out + m * g.Ntot + n) = v;
+    if (m < g.M && n < g.Ntot) *(uint4 *)(g.Out + m * g.Ntot + n) = o;
   }
 }
 
@@ -303,6 +332,8 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_gemm_kernel(I8Args g) {
     stage = next;
   }
   read(stage, 1);
+  EpilogueIn<MODE, TI, TJ> in;
+  if (!SPLIT) in.load(g, n0 + wn * TI * 16, m0 + wm * TJ * 16);
   products(0, 0, TI);
   products(1, 0, TI);
 
@@ -315,7 +346,7 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_gemm_kernel(I8Args g) {
     return;
   }
   block_sync();   // the last operands have been read
-  epilogue<MODE, TI, TJ>(g, acc, (char *)s_t + wave * (TI * TJ * 512), n0 + wn * TI * 16,
+  epilogue<MODE, TI, TJ>(g, acc, in, (char *)s_t + wave * (TI * TJ * 512), n0 + wn * TI * 16,
                          m0 + wm * TJ * 16);
 }
 
@@ -327,6 +358,10 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_join_kernel(I8Args g) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t n0, m0;
   tile_of<BN, BM>(g, blockIdx.x, n0, m0);
+  n0 += (wave % WN) * TI * 16;
+  m0 += (wave / WN) * TJ * 16;
+  EpilogueIn<MODE, TI, TJ> in;
+  in.load(g, n0, m0);
   i32x4 acc[TI][TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i)
@@ -339,8 +374,7 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_join_kernel(I8Args g) {
     for (int i = 0; i < TI; ++i)
 #pragma unroll
       for (int j = 0; j < TJ; ++j) acc[i][j] += from[(i * TJ + j) * 64 * NW];
-  epilogue<MODE, TI, TJ>(g, acc, (char *)s_t + wave * (TI * TJ * 512), n0 + (wave % WN) * TI * 16,
-                         m0 + (wave / WN) * TJ * 16);
+  epilogue<MODE, TI, TJ>(g, acc, in, (char *)s_t + wave * (TI * TJ * 512), n0, m0);
 }
 
 // ---- decode: up to 16 tokens ------------------------------------------------
@@ -506,11 +540,11 @@ size_t int8_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {
 
 qlora_status launch_int8_gemm(int mode, const int8_t *W, const float *sw, int64_t d, int64_t k,
                               const int8_t *In, int64_t ldi, const float *sx, int64_t M,
-                              const uint16_t *L, const uint16_t *hi, const uint16_t *lo, int r,
+                              const uint16_t *L, int ldl, const uint16_t *hi, const uint16_t *lo,
                               int rp, uint16_t *Out, void *part, hipStream_t st) {
   const int64_t N = mode == 0 ? d : k, K = mode == 0 ? k : d;
   const I8Plan p = i8_plan(M, N, K);
-  const I8Args g{W, sw, d, k, In, ldi, sx, M, N, K, L, hi, lo, r, rp, Out, p.S, (i32x4 *)part};
+  const I8Args g{W, sw, d, k, In, ldi, sx, M, N, K, L, ldl, hi, lo, rp, Out, p.S, (i32x4 *)part};
   QlProf prof(mode == 0 ? QLORA_K_INT8_GEMM_FWD : QLORA_K_INT8_GEMM_DX, st);
   if (mode == 0) launch_mode<0>(g, p, st);
   else launch_mode<1>(g, p, st);

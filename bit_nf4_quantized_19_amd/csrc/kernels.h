@@ -212,15 +212,37 @@ qlora_status launch_adamw(float *p, float *m, float *v, const uint16_t *g, uint1
 qlora_status launch_int8_rows(const uint16_t *X, int64_t rows, int64_t cols, const float *mul,
                               int8_t *q, int64_t ldq, float *scale, hipStream_t st);
 
+// A backward's copies, one launch: At[c][t] (k x rp) and Bt[t][c] (rp x d), zero
+// for t >= r, and Hp (M x rp, zero for t >= r) of H (M x r) when H != NULL.
+qlora_status launch_int8_layout(const uint16_t *A, const uint16_t *B, int64_t d, int64_t k, int r,
+                                int rp, uint16_t *At, uint16_t *Bt, const float *H, int64_t M,
+                                float *Hp, hipStream_t st);
+// The same as launch_int8_rows (q NULL: none) together with out[m][t] = sum_c X[m][c] P[t][c], P pr x
+// cols, t < rp (zero from pr on): a linear's first launch. out is M x rp; out2
+// (M x r), hi and lo (s out in bf16 parts, M x rp) may be NULL; zero: nzero ints
+// cleared by the launch.
+struct Int8Rank {
+  const uint16_t *P;
+  int pr, r, rp;
+  float *out, *out2;
+  uint16_t *hi, *lo;
+  float s;
+  int *zero;
+  int64_t nzero;
+};
+qlora_status launch_int8_prep(const uint16_t *X, int64_t rows, int64_t cols, const float *mul,
+                              int8_t *q, int64_t ldq, float *scale, const Int8Rank &k,
+                              hipStream_t st);
+
 // int8_gemm.hip : the product with a d x k record, forward (mode 0) or dX
 // (mode 1). In: M x ldi codes, ldi a multiple of 128, zero past the
-// contraction; sx [M]. L, hi, lo (M x rp), r, rp: the rank-r term as in
-// launch_gemm_fwd / _dx (rp == 0: none). part: int8_gemm_part_bytes(M, columns,
+// contraction; sx [M]. The rank-r term is (hi + lo) L^T: hi, lo M x rp, L columns x
+// ldl with ldl = rp (zero past the rank) or the rank itself; rp == 0: none. part: int8_gemm_part_bytes(M, columns,
 // contraction) bytes of workspace.
 size_t int8_gemm_part_bytes(int64_t M, int64_t N, int64_t K);
 qlora_status launch_int8_gemm(int mode, const int8_t *W, const float *sw, int64_t d, int64_t k,
                               const int8_t *In, int64_t ldi, const float *sx, int64_t M,
-                              const uint16_t *L, const uint16_t *hi, const uint16_t *lo, int r,
+                              const uint16_t *L, int ldl, const uint16_t *hi, const uint16_t *lo,
                               int rp, uint16_t *Out, void *part, hipStream_t st);
 // The forward of up to INT8_GEMV_TOKENS tokens.
 constexpr int64_t INT8_GEMV_TOKENS = 16;

@@ -16,6 +16,8 @@
 // Three launches: gram (updates the momentum; partial Gram sums of a range of
 // the long side), iterate (one workgroup per matrix: joins the partial sums in
 // a fixed order, then the steps), apply (Q times u, and the parameters).
+#include <type_traits>
+
 #include "kernels.h"
 
 namespace {
@@ -44,6 +46,16 @@ struct MuonArgs {
 };
 
 constexpr int CK = 64;        // long-side elements of a chunk
+
+// Barrier between the accesses to LDS of a workgroup's waves; loads and stores
+// of global memory, which no other thread of the launch reads, stay in flight
+// across it.
+QL_DEV void lds_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 template <int NB> constexpr int tiles() { return NB * (NB + 1) / 2; }
 // Row strides of a chunk in LDS, stored as it lies in memory: wide [i][c], tall
@@ -189,9 +201,29 @@ __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs a) {
       load4(g, q, a.vec, gv[j]);
     }
   };
+  // the chunk's products; W: the wave, whose tiles are known at compile time
+  auto sums = [&](auto w) {
+    constexpr int W = decltype(w)::value;
+#pragma unroll
+    for (int s = 0; s < (BYK ? 4 : 16); ++s) {
+      const int k = 4 * (BYK ? 4 * wave + s : s) + k4;
+      double u[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) u[b] = (double)s_u[place<TALL, ST>(16 * b + c16, k)];
+      int t = 0;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = i; j < NB; ++j, ++t)
+          if (BYK || t % 4 == W) {
+            f64x4 &c = acc[BYK ? t : t / 4];
+            c = mfma_f64(u[i], u[j], c);
+          }
+    }
+  };
   fetch(lo);
   for (int64_t ch = lo; ch < hi; ++ch) {
-    __syncthreads();
+    lds_sync();
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       float u[4];
@@ -203,30 +235,19 @@ __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs a) {
       put4<TALL, ST>(a, j, s_u, u);
       store4(m, group_of<TALL>(a, ch * CK, j), a.vec, mv[j]);
     }
-    __syncthreads();
+    lds_sync();
     if (ch + 1 < hi) fetch(ch + 1);   // under this chunk's products
-#pragma unroll
-    for (int s = 0; s < (BYK ? 4 : 16); ++s) {
-      const int k = 4 * (BYK ? 4 * wave + s : s) + k4;
-      double u[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) u[b] = (double)s_u[place<TALL, ST>(16 * b + c16, k)];
-      int t = 0;
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = i; j < NB; ++j, ++t) {
-          if (BYK) acc[t] = mfma_f64(u[i], u[j], acc[t]);
-          else if (t % 4 == wave) acc[t / 4] = mfma_f64(u[i], u[j], acc[t / 4]);
-        }
-    }
+    if (BYK || wave == 0) sums(std::integral_constant<int, 0>());
+    else if (wave == 1) sums(std::integral_constant<int, 1>());
+    else if (wave == 2) sums(std::integral_constant<int, 2>());
+    else sums(std::integral_constant<int, 3>());
   }
   double *part = a.part + (mat * a.split + blockIdx.x) * NT * 256;
   if (BYK) {   // the waves' sums, in their order
     double *red = (double *)s_u;
     static_assert(!BYK || NT * 256 * 8 <= LN * 4, "the chunk's LDS holds the tiles");
     for (int w = 0; w < 4; ++w) {
-      __syncthreads();
+      lds_sync();
       if (wave != w) continue;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -411,7 +432,7 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
   };
   fetch(lo);
   for (int64_t ch = lo; ch < hi; ++ch) {
-    __syncthreads();
+    lds_sync();
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       float u[4];
@@ -420,7 +441,7 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
       put4<TALL, ST>(a, j, s_u, u);
       load4((const float *)p, group_of<TALL>(a, ch * CK, j), a.vec, pv[j]);
     }
-    __syncthreads();
+    lds_sync();
     if (ch + 1 < hi) fetch(ch + 1);   // under this chunk's products
     f64x4 d[CB][RB];
 #pragma unroll
@@ -435,7 +456,7 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
 #pragma unroll
         for (int r = 0; r < RB; ++r) d[c][r] = mfma_f64(q[r][x], u, d[c][r]);
       }
-    __syncthreads();
+    lds_sync();
 #pragma unroll
     for (int c = 0; c < CB; ++c)
 #pragma unroll
@@ -446,7 +467,7 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
         for (int x = 0; x < 4; ++x)
           s_u[place<TALL, ST>(16 * b + 4 * x + k4, 16 * (BYC ? wave : c) + c16)] = (float)d[c][r][x];
       }
-    __syncthreads();
+    lds_sync();
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const Group x = group_of<TALL>(a, ch * CK, j);

@@ -129,6 +129,9 @@ SHAPES = [
     (1000, 704, 64, 33), (128, 128, 65, 16), (256, 256, 256, 16), (520, 448, 257, 12),
     (4096, 4096, 1, 16), (4096, 4096, 4, 16), (11008, 4096, 16, 16), (4096, 11008, 50, 24),
     (4096, 4096, 300, 64), (2048, 11008, 129, 128), (8, 4096, 700, 20), (11008, 64, 513, 40),
+    # rows past a workgroup's registers on either side of the layer
+    (136, 8256, 300, 12), (264, 8320, 1030, 16), (136, 16448, 20, 16), (16448, 128, 20, 24),
+    (8264, 192, 300, 20), (136, 8192, 1027, 16), (4160, 6080, 1030, 33), (520, 5056, 280, 48),
 ]
 
 
