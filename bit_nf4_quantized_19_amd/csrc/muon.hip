@@ -15,7 +15,8 @@
 //
 // Three launches: gram (updates the momentum; partial Gram sums of a range of
 // the long side), iterate (one workgroup per matrix: joins the partial sums in
-// a fixed order, then the steps), apply (Q times u, and the parameters).
+// a fixed order, then the steps; more than 64 ranks take two launches a step
+// there), apply (Q times u, and the parameters).
 #include <type_traits>
 
 #include "kernels.h"
@@ -36,12 +37,12 @@ struct MuonArgs {
   uint16_t *out;
   int64_t rows, cols, len;   // len: the longer side
   int R, tall;               // tall: element (i, c) of the short and long side at c R + i
-  int vec;                   // every group of four elements is aligned and whole or absent
   uint32_t magic;            // ceil(2^20 / R): x / R for x < 64 * 128
   int split;                 // workgroups per matrix
   int64_t chunks;            // of CK along the long side
   double *part;              // [n][split][tiles][256]
   double *Q;                 // [n][RP][RP], Q / (|u| + eps)
+  double *S, *P, *inv;       // more than 64 ranks: [n][RP][RP], the same, [n]
   MuonScalars s;
 };
 
@@ -79,29 +80,39 @@ QL_DEV float muon_u(float m, float g, const MuonScalars &s) {   // m: the update
 
 // A thread's share of a chunk: NB groups of four elements consecutive in
 // memory, group 256 j + thread. Groups run along the rows of a wide matrix
-// (16 a row) and through the chunk of a tall one.
+// (16 a row) and through the chunk of a tall one. Offsets in a matrix fit 32
+// bits (128 x 2^24 elements).
 struct Group {
-  int64_t off;   // of the first element in the matrix
-  int n;         // elements that exist: 0 .. 4
+  uint32_t off;   // of the first element in the matrix
+  int n;          // elements that exist: 0 .. 4
 };
-template <bool TALL>
-QL_DEV Group group_of(const MuonArgs &a, int64_t c0, int j) {
-  const int e = 256 * j + threadIdx.x;
-  const int w = (int)(a.len - c0 < CK ? a.len - c0 : CK);
-  Group q;
-  if (TALL) {
-    q.off = c0 * a.R + 4 * e;
-    q.n = w * a.R - 4 * e;
-  } else {
-    const int c = 4 * (e & 15);
-    q.off = (e >> 4) * a.cols + c0 + c;
-    q.n = (e >> 4) < a.R ? w - c : 0;
+template <int NB, bool TALL>
+struct Share {
+  uint32_t off[NB];   // of chunk 0
+  uint32_t step;      // from chunk to chunk
+  QL_DEV explicit Share(const MuonArgs &a) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const uint32_t e = 256 * j + threadIdx.x;
+      off[j] = TALL ? 4 * e : (e >> 4) * (uint32_t)a.cols + 4 * (e & 15);
+    }
+    step = TALL ? CK * (uint32_t)a.R : CK;
   }
-  q.n = q.n < 0 ? 0 : q.n > 4 ? 4 : q.n;
-  return q;
-}
-QL_DEV void load4(const float *p, const Group &q, int vec, float (&v)[4]) {
-  if (vec) {
+  QL_DEV Group group(const MuonArgs &a, int64_t ch, int j) const {
+    const int e = 256 * j + (int)threadIdx.x;
+    const bool in = TALL ? e < 16 * a.R : (e >> 4) < a.R;
+    Group q{off[j] + (uint32_t)ch * step, in ? 4 : 0};
+    const int64_t left = a.len - ch * CK;
+    if (left < CK) {   // the last chunk
+      const int n = TALL ? (int)left * a.R - 4 * e : (int)left - 4 * (e & 15);
+      q.n = !in || n < 0 ? 0 : n > 4 ? 4 : n;
+    }
+    return q;
+  }
+};
+template <bool VEC>
+QL_DEV void load4(const float *p, const Group &q, float (&v)[4]) {
+  if (VEC) {
     const float4 x = q.n ? *(const float4 *)(p + q.off) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
   } else {
@@ -109,8 +120,9 @@ QL_DEV void load4(const float *p, const Group &q, int vec, float (&v)[4]) {
     for (int x = 0; x < 4; ++x) v[x] = x < q.n ? p[q.off + x] : 0.0f;
   }
 }
-QL_DEV void load4(const uint16_t *p, const Group &q, int vec, float (&v)[4]) {
-  if (vec) {
+template <bool VEC>
+QL_DEV void load4(const uint16_t *p, const Group &q, float (&v)[4]) {
+  if (VEC) {
     const uint2 x = q.n ? *(const uint2 *)(p + q.off) : make_uint2(0u, 0u);
     v[0] = ql::bf16lo(x.x), v[1] = ql::bf16hi(x.x), v[2] = ql::bf16lo(x.y), v[3] = ql::bf16hi(x.y);
   } else {
@@ -118,8 +130,9 @@ QL_DEV void load4(const uint16_t *p, const Group &q, int vec, float (&v)[4]) {
     for (int x = 0; x < 4; ++x) v[x] = x < q.n ? ql::bf16_to_f(p[q.off + x]) : 0.0f;
   }
 }
-QL_DEV void store4(float *p, const Group &q, int vec, const float (&v)[4]) {
-  if (vec) {
+template <bool VEC>
+QL_DEV void store4(float *p, const Group &q, const float (&v)[4]) {
+  if (VEC) {
     if (q.n) *(float4 *)(p + q.off) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
 #pragma unroll
@@ -127,8 +140,9 @@ QL_DEV void store4(float *p, const Group &q, int vec, const float (&v)[4]) {
       if (x < q.n) p[q.off + x] = v[x];
   }
 }
-QL_DEV void store4(uint16_t *p, const Group &q, int vec, const float (&v)[4]) {
-  if (vec) {
+template <bool VEC>
+QL_DEV void store4(uint16_t *p, const Group &q, const float (&v)[4]) {
+  if (VEC) {
     if (q.n)
       *(uint2 *)(p + q.off) =
           make_uint2(ql::pack_bf16x2(v[0], v[1]), ql::pack_bf16x2(v[2], v[3]));
@@ -174,7 +188,7 @@ QL_DEV void get4(const MuonArgs &a, int j, const float *s, float (&v)[4]) {
   }, [&](int at, int x) { v[x] = s[at]; });
 }
 
-template <int NB, bool TALL>
+template <int NB, bool TALL, bool VEC>
 __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs a) {
   constexpr int ST = gram_stride<NB, TALL>(), LN = chunk_floats<NB, TALL, ST>();
   __shared__ __align__(16) float s_u[LN];
@@ -192,13 +206,14 @@ __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs a) {
   for (int t = 0; t < MY; ++t) acc[t] = f64x4{0.0, 0.0, 0.0, 0.0};
   // the padding of the smaller side stays zero
   for (int e = threadIdx.x; e < LN; e += 256) s_u[e] = 0.0f;
+  const Share<NB, TALL> mine(a);
   float mv[NB][4], gv[NB][4];
   auto fetch = [&](int64_t ch) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const Group q = group_of<TALL>(a, ch * CK, j);
-      load4(m, q, a.vec, mv[j]);
-      load4(g, q, a.vec, gv[j]);
+      const Group q = mine.group(a, ch, j);
+      load4<VEC>(m, q, mv[j]);
+      load4<VEC>(g, q, gv[j]);
     }
   };
   // the chunk's products; W: the wave, whose tiles are known at compile time
@@ -221,8 +236,8 @@ __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs a) {
           }
     }
   };
-  fetch(lo);
   for (int64_t ch = lo; ch < hi; ++ch) {
+    fetch(ch);
     lds_sync();
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -233,10 +248,9 @@ __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs a) {
         u[x] = muon_u(mv[j][x], gv[j][x], a.s);
       }
       put4<TALL, ST>(a, j, s_u, u);
-      store4(m, group_of<TALL>(a, ch * CK, j), a.vec, mv[j]);
+      store4<VEC>(m, mine.group(a, ch, j), mv[j]);
     }
     lds_sync();
-    if (ch + 1 < hi) fetch(ch + 1);   // under this chunk's products
     if (BYK || wave == 0) sums(std::integral_constant<int, 0>());
     else if (wave == 1) sums(std::integral_constant<int, 1>());
     else if (wave == 2) sums(std::integral_constant<int, 2>());
@@ -347,20 +361,27 @@ __global__ __launch_bounds__(iterate_threads<NB>()) void muon_iterate_kernel(Muo
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         d[b] = mfma_f64(s_a[(16 * b + c16) * LS + 4 * x + k4], in[x], d[b]);
-      // keeps the operands of later steps out of registers that three panels fill
-      if (NB > 4) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int q = 0; q < 4; ++q) out[4 * b + q] = d[b][q];
   };
+  if (NB == 1 && !on) return;   // the steps of one block need one wave and no barrier
+  auto sync = [&] {
+    if (NB > 1) {
+      __syncthreads();
+    } else {   // LDS accesses of a wave are in order: keep the compiler to it
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
+    }
+  };
   auto store = [&](const double (&v)[NB * 4]) {
-    __syncthreads();
+    sync();
     if (on)
 #pragma unroll
       for (int x = 0; x < NB * 4; ++x) s_a[(4 * x + k4) * LS + 16 * wave + c16] = v[x];
-    __syncthreads();
+    sync();
   };
 #pragma clang loop unroll(disable)
   for (int step = 0; step < a.s.steps; ++step) {
@@ -393,7 +414,151 @@ __global__ __launch_bounds__(iterate_threads<NB>()) void muon_iterate_kernel(Muo
     for (int x = 0; x < NB * 4; ++x) Q[(4 * x + k4) * RP + 16 * wave + c16] = qp[x] * inv;
 }
 
-template <int NB, bool TALL>
+// ---- more than 64 ranks: a workgroup per 16 columns ------------------------------
+// One compute unit takes 232 us for the 17 products of 128 x 128 in float64, so
+// the columns of a matrix are dealt to NB workgroups and a step is two
+// launches: poly (P from all of S) and advance (the workgroup's columns of Q
+// and S from all of P). Both read their left operand from L2 by rows, as S and
+// P are symmetric up to rounding.
+// Partial sums of one 16 x 16 tile and its mirror image, in order.
+template <int NB>
+__global__ __launch_bounds__(256) void muon_join_kernel(MuonArgs a) {
+  constexpr int RP = 16 * NB, NT = tiles<NB>();
+  const int e = threadIdx.x;
+  const int64_t mat = blockIdx.y;
+  const double *part = a.part + (mat * a.split * NT + blockIdx.x) * 256 + e;
+  double v = 0.0;
+#pragma unroll 8
+  for (int x = 0; x < a.split; ++x) v += part[(int64_t)x * NT * 256];
+  int t = (int)blockIdx.x, i = 0;
+  while (t >= NB - i) t -= NB - i, ++i;
+  const int row = 16 * i + 4 * (e >> 6) + ((e & 63) >> 4), col = 16 * (i + t) + (e & 15);
+  double *S = a.S + mat * RP * RP;
+  S[row * RP + col] = v;
+  if (t) S[col * RP + row] = v;
+}
+
+// 1 / (|u| + eps) of the matrix whose Gram sums are S.
+template <int NB>
+QL_DEV double inverse_size(const MuonArgs &a, const double *S) {
+  constexpr int RP = 16 * NB;
+  double tr = 0.0;   // every wave for itself, in the same order
+  for (int i = threadIdx.x & 63; i < RP; i += 64) tr += S[i * RP + i];
+  for (int o = 32; o; o >>= 1) tr += __shfl_xor(tr, o);
+  return 1.0 / (sqrt(tr) + a.s.eps);
+}
+// Row blocks wave and wave + 4 of (rows of L) times the panel in LDS.
+template <int NB>
+QL_DEV void panel_product(const double *L, const double *panel, f64x4 (&d)[2]) {
+  constexpr int RP = 16 * NB;
+  const int lane = threadIdx.x & 63, c16 = lane & 15, k4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int b1 = wave + 4 < NB ? wave + 4 : wave;   // past the end: computed, not used
+  d[0] = d[1] = f64x4{0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+  for (int x = 0; x < NB * 4; ++x) {
+    const double *l = L + (4 * x + k4) * RP + c16, y = panel[(4 * x + k4) * 16 + c16];
+    d[0] = mfma_f64(l[16 * wave], y, d[0]);
+    d[1] = mfma_f64(l[16 * b1], y, d[1]);
+  }
+}
+
+template <int NB>
+__global__ __launch_bounds__(256) void muon_poly_kernel(MuonArgs a, int first) {
+  constexpr int RP = 16 * NB;
+  __shared__ double s_b[RP * 16];
+  const int lane = threadIdx.x & 63, c16 = lane & 15, k4 = lane >> 4, wave = threadIdx.x >> 6;
+  const int64_t mat = blockIdx.y;
+  const int col = 16 * (int)blockIdx.x;
+  const double *S = a.S + mat * RP * RP;
+  double sc = 1.0;
+  if (first) {   // S holds the Gram sums: S_0 is inv^2 times them
+    const double inv = inverse_size<NB>(a, S);
+    sc = inv * inv;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.inv[mat] = inv;
+  }
+  for (int e = threadIdx.x; e < RP * 16; e += 256)
+    s_b[e] = sc * S[(e >> 4) * RP + col + (e & 15)];
+  __syncthreads();
+  f64x4 d[2];
+  panel_product<NB>(S, s_b, d);
+  double *P = a.P + mat * RP * RP;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int b = wave + 4 * r;
+    if (b >= NB) break;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int row = 16 * b + 4 * q + k4;
+      P[row * RP + col + c16] = (row == col + c16 ? a.s.a : 0.0) + a.s.b * s_b[row * 16 + c16] +
+                                a.s.c * (sc * d[r][q]);
+    }
+  }
+}
+
+template <int NB>
+__global__ __launch_bounds__(256) void muon_advance_kernel(MuonArgs a, int first, int last) {
+  constexpr int RP = 16 * NB;
+  __shared__ double s_b[RP * 16];
+  const int lane = threadIdx.x & 63, c16 = lane & 15, k4 = lane >> 4, wave = threadIdx.x >> 6;
+  const int64_t mat = blockIdx.y;
+  const int col = 16 * (int)blockIdx.x;
+  const double *P = a.P + mat * RP * RP;
+  double *S = a.S + mat * RP * RP, *Q = a.Q + mat * RP * RP;
+  const double inv = a.inv[mat];
+  f64x4 d[2];
+  // Q' = P Q (the first Q is the identity), times 1 / (|u| + eps) at the end
+  if (!first) {
+    for (int e = threadIdx.x; e < RP * 16; e += 256) s_b[e] = Q[(e >> 4) * RP + col + (e & 15)];
+    __syncthreads();
+    panel_product<NB>(P, s_b, d);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int b = wave + 4 * r;
+    if (b >= NB) break;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int at = (16 * b + 4 * q + k4) * RP + col + c16;
+      const double v = first ? P[at] : d[r][q];
+      Q[at] = last ? v * inv : v;
+    }
+  }
+  if (last) return;
+  // S' = P (P S)
+  const double sc = first ? inv * inv : 1.0;
+  for (int e = threadIdx.x; e < RP * 16; e += 256)
+    s_b[e] = sc * S[(e >> 4) * RP + col + (e & 15)];
+  __syncthreads();
+  panel_product<NB>(P, s_b, d);
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    if (wave + 4 * r < NB)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s_b[(16 * (wave + 4 * r) + 4 * q + k4) * 16 + c16] = d[r][q];
+  __syncthreads();
+  panel_product<NB>(P, s_b, d);
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    if (wave + 4 * r < NB)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        S[(16 * (wave + 4 * r) + 4 * q + k4) * RP + col + c16] = d[r][q];
+}
+
+// No steps: Q is the identity over |u| + eps.
+template <int NB>
+__global__ __launch_bounds__(256) void muon_no_steps_kernel(MuonArgs a) {
+  constexpr int RP = 16 * NB;
+  const int64_t mat = blockIdx.x;
+  const double inv = inverse_size<NB>(a, a.S + mat * RP * RP);
+  for (int e = threadIdx.x; e < RP * RP; e += 256)
+    a.Q[mat * RP * RP + e] = e / RP == e % RP ? inv : 0.0;
+}
+
+template <int NB, bool TALL, bool VEC>
 __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
   constexpr int RP = 16 * NB, ST = apply_stride<NB, TALL>(), LN = chunk_floats<NB, TALL, ST>();
   __shared__ __align__(16) float s_u[LN];
@@ -421,17 +586,18 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
     }
   }
   for (int e = threadIdx.x; e < LN; e += 256) s_u[e] = 0.0f;
+  const Share<NB, TALL> mine(a);
   float mv[NB][4], gv[NB][4], pv[NB][4];
   auto fetch = [&](int64_t ch) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const Group x = group_of<TALL>(a, ch * CK, j);
-      load4(m, x, a.vec, mv[j]);
-      load4(g, x, a.vec, gv[j]);
+      const Group x = mine.group(a, ch, j);
+      load4<VEC>(m, x, mv[j]);
+      load4<VEC>(g, x, gv[j]);
     }
   };
-  fetch(lo);
   for (int64_t ch = lo; ch < hi; ++ch) {
+    fetch(ch);
     lds_sync();
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -439,10 +605,9 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) u[x] = muon_u(mv[j][x], gv[j][x], a.s);
       put4<TALL, ST>(a, j, s_u, u);
-      load4((const float *)p, group_of<TALL>(a, ch * CK, j), a.vec, pv[j]);
+      load4<VEC>((const float *)p, mine.group(a, ch, j), pv[j]);
     }
     lds_sync();
-    if (ch + 1 < hi) fetch(ch + 1);   // under this chunk's products
     f64x4 d[CB][RB];
 #pragma unroll
     for (int c = 0; c < CB; ++c)
@@ -470,7 +635,7 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
     lds_sync();
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const Group x = group_of<TALL>(a, ch * CK, j);
+      const Group x = mine.group(a, ch, j);
       float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       get4<TALL, ST>(a, j, s_u, o);
 #pragma unroll
@@ -478,15 +643,15 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
         const float dir = __fadd_rn(__fmul_rn(a.s.scale, o[i]), __fmul_rn(a.s.wd, pv[j][i]));
         o[i] = __fsub_rn(pv[j][i], __fmul_rn(a.s.lr, dir));
       }
-      store4(p, x, a.vec, o);
-      store4(out, x, a.vec, o);
+      store4<VEC>(p, x, o);
+      store4<VEC>(out, x, o);
     }
   }
 }
 
 struct MuonPlan {
   int R, NB, split;
-  int64_t len, chunks, part, q;   // part, q: bytes
+  int64_t len, chunks, part, q, inv;   // part, q, inv: bytes
 };
 MuonPlan muon_plan(int64_t n, int64_t rows, int64_t cols) {
   MuonPlan p;
@@ -499,24 +664,45 @@ MuonPlan muon_plan(int64_t n, int64_t rows, int64_t cols) {
   p.split = (int)s;
   p.part = ql_rup(n * s * (p.NB * (p.NB + 1) / 2) * 2048, 256);
   p.q = ql_rup(n * p.NB * p.NB * 2048, 256);
+  p.inv = ql_rup(n * 8, 256);
   return p;
 }
 
+template <int NB, bool TALL, bool VEC>
+void launch_form(const MuonArgs &a, unsigned n, hipStream_t st) {
+  const dim3 grid((unsigned)a.split, n);
+  muon_gram_kernel<NB, TALL, VEC><<<grid, 256, 0, st>>>(a);
+  if constexpr (NB <= 4) {
+    muon_iterate_kernel<NB><<<n, iterate_threads<NB>(), 0, st>>>(a);
+  } else {
+    const dim3 panels(NB, n);
+    muon_join_kernel<NB><<<dim3(tiles<NB>(), n), 256, 0, st>>>(a);
+    if (a.s.steps == 0) muon_no_steps_kernel<NB><<<n, 256, 0, st>>>(a);
+    for (int i = 0; i < a.s.steps; ++i) {
+      muon_poly_kernel<NB><<<panels, 256, 0, st>>>(a, i == 0);
+      muon_advance_kernel<NB><<<panels, 256, 0, st>>>(a, i == 0, i + 1 == a.s.steps);
+    }
+  }
+  muon_apply_kernel<NB, TALL, VEC><<<grid, 256, 0, st>>>(a);
+}
 template <int NB>
 void launch_nb(const MuonArgs &a, unsigned n, hipStream_t st) {
-  const dim3 grid((unsigned)a.split, n);
-  if (a.tall) muon_gram_kernel<NB, true><<<grid, 256, 0, st>>>(a);
-  else muon_gram_kernel<NB, false><<<grid, 256, 0, st>>>(a);
-  muon_iterate_kernel<NB><<<n, iterate_threads<NB>(), 0, st>>>(a);
-  if (a.tall) muon_apply_kernel<NB, true><<<grid, 256, 0, st>>>(a);
-  else muon_apply_kernel<NB, false><<<grid, 256, 0, st>>>(a);
+  // VEC: every group of four elements is aligned, and whole or absent
+  const bool vec = (a.tall ? a.rows * a.cols : a.cols) % 4 == 0;
+  if (a.tall) {
+    if (vec) launch_form<NB, true, true>(a, n, st);
+    else launch_form<NB, true, false>(a, n, st);
+  } else {
+    if (vec) launch_form<NB, false, true>(a, n, st);
+    else launch_form<NB, false, false>(a, n, st);
+  }
 }
 
 }  // namespace
 
 size_t muon_ws_bytes(int64_t n, int64_t rows, int64_t cols) {
   const MuonPlan p = muon_plan(n, rows, cols);
-  return (size_t)(p.part + p.q);
+  return (size_t)(p.part + (p.NB <= 4 ? p.q : 3 * p.q + p.inv));
 }
 
 qlora_status launch_muon(float *p, float *m, const uint16_t *g, uint16_t *out, int64_t n,
@@ -524,8 +710,11 @@ qlora_status launch_muon(float *p, float *m, const uint16_t *g, uint16_t *out, i
                          hipStream_t st) {
   const MuonPlan pl = muon_plan(n, rows, cols);
   const MuonArgs a{p, m, g, out, rows, cols, pl.len, pl.R, rows > cols,
-                   (rows > cols ? rows * cols : cols) % 4 == 0, (uint32_t)((1u << 20) + pl.R - 1) / (uint32_t)pl.R, pl.split, pl.chunks,
-                   (double *)ws, (double *)((char *)ws + pl.part), s};
+                   (uint32_t)((1u << 20) + pl.R - 1) / (uint32_t)pl.R, pl.split, pl.chunks,
+                   (double *)ws, (double *)((char *)ws + pl.part),
+                   (double *)((char *)ws + pl.part + pl.q),
+                   (double *)((char *)ws + pl.part + 2 * pl.q),
+                   (double *)((char *)ws + pl.part + 3 * pl.q), s};
   QlProf prof(QLORA_K_MUON, st);
   switch (pl.NB) {
     case 1: launch_nb<1>(a, (unsigned)n, st); break;
