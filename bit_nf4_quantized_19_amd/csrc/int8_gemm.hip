@@ -97,22 +97,22 @@ template <int MODE, int TI, int TJ>
 struct EpilogueIn {
   float sx[TJ];
   float4 sw[TI];
-  uint4 l[TI], s[TJ];
+  uint4 l[2][TI], s[2][TJ];   // ranks t0 .. t0 + 15 in buffer t0 / 16 % 2
 
-  QL_DEV void ranks(const I8Args &g, int64_t n0, int64_t m0, int t0) {
+  QL_DEV void ranks(const I8Args &g, int64_t n0, int64_t m0, int t0, int b) {
     const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4, t = t0 + 8 * (grp & 1);
     const uint16_t *S = grp < 2 ? g.Shi : g.Slo;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int64_t m = m0 + 16 * j + c16;
-      s[j] = *(const uint4 *)(S + (m < g.M ? m : g.M - 1) * g.rp + t);
+      s[b][j] = *(const uint4 *)(S + (m < g.M ? m : g.M - 1) * g.rp + t);
     }
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       int64_t n = n0 + 16 * i + c16;
       n = n < g.Ntot ? n : g.Ntot - 1;
       if (g.ldl % 8 == 0) {
-        l[i] = t < g.ldl ? *(const uint4 *)(g.L + n * g.ldl + t) : ql::zero4();
+        l[b][i] = t < g.ldl ? *(const uint4 *)(g.L + n * g.ldl + t) : ql::zero4();
       } else {
         uint32_t e[8];
 #pragma unroll
@@ -121,8 +121,8 @@ struct EpilogueIn {
           e[x] = g.L[n * g.ldl + tc];
           e[x] = t + x < g.ldl ? e[x] : 0u;
         }
-        l[i] = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
-                          e[6] | (e[7] << 16));
+        l[b][i] = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16),
+                             e[6] | (e[7] << 16));
       }
     }
   }
@@ -139,7 +139,7 @@ struct EpilogueIn {
       sw[i] = MODE == 0 ? *(const float4 *)(g.sw + (n < g.d ? n : g.d - 4))
                         : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
     }
-    if (g.rp) ranks(g, n0, m0, 0);
+    if (g.rp) ranks(g, n0, m0, 0, 0);
   }
 };
 
@@ -153,6 +153,7 @@ QL_DEV void epilogue(const I8Args &g, const i32x4 (&acc)[TI][TJ], EpilogueIn<MOD
   const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4;
   constexpr int WB = TI * 32, CPW = WB / 16;   // bytes and chunks of a block's row
   static_assert((CPW & (CPW - 1)) == 0, "a power of two");
+  if (g.rp > 16) in.ranks(g, n0, m0, 16, 1);
   f32x4 v[TI][TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
@@ -165,18 +166,21 @@ QL_DEV void epilogue(const I8Args &g, const i32x4 (&acc)[TI][TJ], EpilogueIn<MOD
         v[i][j][q] = MODE == 0 ? f * w[q] : f;
       }
   }
-  for (int t0 = 0; t0 < g.rp; t0 += 16) {
-    uint4 l[TI], sv[TJ];
+  for (int t0 = 0; t0 < g.rp; t0 += 32)
 #pragma unroll
-    for (int i = 0; i < TI; ++i) l[i] = in.l[i];
+    for (int h = 0; h < 2; ++h) {
+      if (t0 + 16 * h >= g.rp) break;
+      uint4 l[TI], sv[TJ];
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) sv[j] = in.s[j];
-    if (t0 + 16 < g.rp) in.ranks(g, n0, m0, t0 + 16);
+      for (int i = 0; i < TI; ++i) l[i] = in.l[h][i];
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+      for (int j = 0; j < TJ; ++j) sv[j] = in.s[h][j];
+      if (t0 + 16 * h + 32 < g.rp) in.ranks(g, n0, m0, t0 + 16 * h + 32, h);
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) v[i][j] = ql::mfma16(l[i], sv[j], v[i][j]);
-  }
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) v[i][j] = ql::mfma16(l[i], sv[j], v[i][j]);
+    }
   // row j * 16 + c16 of the block, columns 16 i + 4 grp .. +3, the row's 16-byte
   // chunks permuted by the row
 #pragma unroll
@@ -378,12 +382,14 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_join_kernel(I8Args g) {
 }
 
 // ---- decode: up to 16 tokens ------------------------------------------------
-// A workgroup of eight waves owns 16 NR rows of the weight and all tokens; a
-// wave takes UN consecutive 64-code chunks of every row at a time and the
-// waves' int32 sums meet in LDS. Bound by the weight's bytes, each read once.
-// The tokens' codes come from L2 as often as there are workgroups, for which
-// two row blocks share them where there are rows enough. Wave w also takes
-// ranks 16 w .. +15 of the rank-r term, whose operands it loads up front.
+// A workgroup of eight waves owns 16 NR rows of the weight and all tokens; the
+// waves take 128-code steps in turn and their int32 sums meet in LDS. Bound by
+// the weight's bytes, each read once: a wave fetches its steps by LDS DMA, 8 rows
+// x 128 bytes at a time (whole lines; the 16 rows x 64 bytes of an operand read
+// as half lines take a third longer), ST steps ahead in slots of its own, so
+// that no barrier is needed. The tokens' codes come from L2 as often as there
+// are workgroups. Wave w also takes ranks 16 w .. +15 of the rank-r term, whose
+// operands it loads up front.
 struct I8Gemv {
   const int8_t *W;
   const float *sw;
@@ -400,22 +406,41 @@ struct I8Gemv {
 
 constexpr int GV_W = 8;
 
-template <int NR, int UN>
+template <int NR, int ST>
 __global__ __launch_bounds__(64 * GV_W) void int8_gemv_kernel(I8Gemv g) {
-  __shared__ int s_red[GV_W][NR][4][64];
-  __shared__ float s_lr[GV_W][NR][4][64];
+  constexpr int SLOT = NR * 16 * BK;           // bytes of a step's rows
+  constexpr int RED = GV_W * NR * 256 * 8;     // sums: int32, and float32 of the ranks
+  constexpr int LDS = GV_W * ST * SLOT > RED ? GV_W * ST * SLOT : RED;
+  __shared__ __align__(1024) char s_t[LDS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, grp = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16 * NR;
   const int m = c16 < g.M ? c16 : g.M - 1;
-  const int8_t *w[NR], *const x = g.In + m * g.ldi + 16 * grp;
+  const int8_t *const x = g.In + m * g.ldi + 16 * grp;
   int64_t row[NR];
 #pragma unroll
-  for (int b = 0; b < NR; ++b) {
-    row[b] = n0 + 16 * b + c16 < g.d ? n0 + 16 * b + c16 : g.d - 1;
-    w[b] = g.W + row[b] * g.k + 16 * grp;
+  for (int b = 0; b < NR; ++b) row[b] = n0 + 16 * b + c16 < g.d ? n0 + 16 * b + c16 : g.d - 1;
+  // DMA sources: rows 8 i .. +7 of the block, whose chunks are permuted as in
+  // the GEMM's tiles; past the matrix the last valid piece, against zero codes
+  const int8_t *w[2 * NR];
+  uint32_t wc[2 * NR];
+#pragma unroll
+  for (int i = 0; i < 2 * NR; ++i) {
+    const int r = 8 * i + (lane >> 3);
+    w[i] = g.W + (n0 + r < g.d ? n0 + r : g.d - 1) * g.k;
+    wc[i] = 16 * swz(r & 15, lane & 7);
   }
+  const int nk = (int)ql_cdiv(g.k, BK), mine = nk > wave ? (nk - wave + GV_W - 1) / GV_W : 0;
+  const uint32_t slots = lds_addr(s_t) + wave * ST * SLOT, end = (uint32_t)g.k - 16;
+  auto issue = [&](int step) {   // this wave's step-th
+    const uint32_t kk = (uint32_t)(wave + step * GV_W) * BK;
+#pragma unroll
+    for (int i = 0; i < 2 * NR; ++i) {
+      const uint32_t at = kk + wc[i] < end ? kk + wc[i] : end;
+      dma16(w[i] + at, __builtin_amdgcn_readfirstlane(slots + (step % ST) * SLOT + 1024 * i));
+    }
+  };
   // ranks 16 wave .. +15: lanes 0-31 against the high parts, 32-63 the low
   const bool lr = 16 * wave < g.rp;
   uint4 lv[NR], sv = ql::zero4();
@@ -439,27 +464,49 @@ __global__ __launch_bounds__(64 * GV_W) void int8_gemv_kernel(I8Gemv g) {
       }
     }
   }
+  // the tokens' codes of a step, beside its DMAs
+  i32x4 xv[ST][SL];
+  auto tokens = [&](int buf, int step) {
+    const int kk = (wave + step * GV_W) * BK;
+#pragma unroll
+    for (int c = 0; c < SL; ++c) xv[buf][c] = *(const i32x4 *)(x + kk + 64 * c);
+  };
   i32x4 acc[NR];
 #pragma unroll
   for (int b = 0; b < NR; ++b) acc[b] = i32x4{0, 0, 0, 0};
-  const int nc = (int)(g.k >> 6);
-  for (int c = wave * UN; c < nc; c += GV_W * UN) {
-    i32x4 a[UN][NR], v[UN];
+  // A step's DMAs and token loads go out ST steps ahead; they retire in order.
+  constexpr int OPS = 2 * NR + SL;
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      // chunks past the end: the last one against zeros
-      const int at = 64 * (c + u < nc ? c + u : nc - 1);
-#pragma unroll
-      for (int b = 0; b < NR; ++b) a[u][b] = *(const i32x4 *)(w[b] + at);
-      v[u] = *(const i32x4 *)(x + at);
+  for (int u = 0; u < ST; ++u)
+    if (u < mine) {
+      issue(u);
+      tokens(u, u);
     }
+  for (int s0 = 0; s0 < mine; s0 += ST) {
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      if (c + u >= nc) v[u] = i32x4{0, 0, 0, 0};
+    for (int u = 0; u < ST; ++u) {
+      if (s0 + u >= mine) break;
+      if (s0 + u + ST - 1 < mine) wait_vm_le<(ST - 1) * OPS>();
+      else wait_vm_le<0>();
+      asm volatile("" ::: "memory");
+      const char *ws = s_t + wave * ST * SLOT + u * SLOT;
 #pragma unroll
-      for (int b = 0; b < NR; ++b) acc[b] = mfma_i8(a[u][b], v[u], acc[b]);
+      for (int c = 0; c < SL; ++c)
+#pragma unroll
+        for (int b = 0; b < NR; ++b)
+          acc[b] = mfma_i8(*(const i32x4 *)(ws + (16 * b + c16) * BK + 16 * swz(c16, 4 * c + grp)),
+                           xv[u][c], acc[b]);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // the slot has been read
+      if (s0 + u + ST < mine) {
+        issue(s0 + u + ST);
+        tokens(u, s0 + u + ST);
+      }
     }
   }
+  block_sync();   // by every wave: the sums take their place
+  int(*const s_red)[NR][4][64] = (int(*)[NR][4][64])s_t;
+  float(*const s_lr)[NR][4][64] = (float(*)[NR][4][64])(s_t + GV_W * NR * 1024);
 #pragma unroll
   for (int b = 0; b < NR; ++b) {
 #pragma unroll
@@ -501,6 +548,7 @@ I8Plan i8_plan(int64_t M, int64_t N, int64_t K) {
     const double step = cfg == 0 ? 0.95 : cfg == 1 ? 0.5 : 0.3;   // us
     for (int S : {1, 2, 3, 4, 6, 8}) {
       if (S > 1 && (cfg == 0 || S * 2 > nk)) break;
+      if (tiles * S >= int64_t(1) << 23) break;   // 2^32 threads; 128 x 256 tiles stay below
       double t = (double)ql_cdiv(tiles * S, 256) * (step * (double)ql_cdiv(nk, S) + 6.0);
       if (S > 1) t += 3.0 + (double)(S * tiles * bm * 128 * 4) * 2.0 / 5e6;
       if (least < 0.0 || t < least) {
@@ -559,8 +607,8 @@ qlora_status launch_int8_gemv(const int8_t *W, const float *sw, int64_t d, int64
   const I8Gemv g{W, sw, d, k, In, ldi, sx, (int)M, B, hi, lo, r, rp, Y};
   QlProf prof(QLORA_K_INT8_GEMV, st);
   // two row blocks a workgroup once one fills the chip twice
-  if (d >= 8192) int8_gemv_kernel<2, 4><<<(unsigned)ql_cdiv(d, 32), 64 * GV_W, 0, st>>>(g);
-  else int8_gemv_kernel<1, 8><<<(unsigned)ql_cdiv(d, 16), 64 * GV_W, 0, st>>>(g);
+  if (d >= 8192) int8_gemv_kernel<2, 2><<<(unsigned)ql_cdiv(d, 32), 64 * GV_W, 0, st>>>(g);
+  else int8_gemv_kernel<1, 4><<<(unsigned)ql_cdiv(d, 16), 64 * GV_W, 0, st>>>(g);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }

@@ -372,31 +372,44 @@ struct CopyArgs {
   const float *H;
   float *Hp;
 };
-// thread: one row of B (written as a column of Bt, so that neighbours' stores
-// are consecutive), one column of A, or one row of H
+// A thread takes eight ranks (grid row y) of one row of B, written as a column
+// of Bt, of one column of A, or of one row of H; neighbours' are consecutive.
 __global__ __launch_bounds__(256) void int8_layout_kernel(CopyArgs a) {
   int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int t0 = 8 * (int)blockIdx.y;
+  uint32_t e[8];
   if (i < a.d) {
     const uint16_t *b = a.B + i * a.r;
-#pragma unroll 8
-    for (int t = 0; t < a.rp; ++t) a.Bt[t * a.d + i] = t < a.r ? b[t] : 0;
+    if (a.r % 8 == 0) {
+      const uint4 v = t0 < a.r ? *(const uint4 *)(b + t0) : ql::zero4();
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int x = 0; x < 8; ++x) e[x] = w[x >> 1] >> (16 * (x & 1));
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) e[x] = t0 + x < a.r ? b[t0 + x] : 0u;
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) a.Bt[(t0 + x) * a.d + i] = (uint16_t)e[x];
     return;
   }
   i -= ql_rup(a.d, 256);
   if (i < 0) return;
   if (i < a.k) {
-    for (int t0 = 0; t0 < a.rp; t0 += 8) {
-      uint32_t e[8];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) e[x] = t0 + x < a.r ? a.A[(t0 + x) * a.k + i] : 0u;
-      *(uint4 *)(a.At + i * a.rp + t0) = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16),
-                                                    e[4] | (e[5] << 16), e[6] | (e[7] << 16));
-    }
+    for (int x = 0; x < 8; ++x) e[x] = t0 + x < a.r ? a.A[(t0 + x) * a.k + i] : 0u;
+    *(uint4 *)(a.At + i * a.rp + t0) = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16),
+                                                  e[4] | (e[5] << 16), e[6] | (e[7] << 16));
     return;
   }
   i -= ql_rup(a.k, 256);
-  if (a.H && i >= 0 && i < a.M)
-    for (int t = 0; t < a.rp; ++t) a.Hp[i * a.rp + t] = t < a.r ? a.H[i * a.r + t] : 0.0f;
+  if (a.H && i >= 0 && i < a.M) {
+    float h[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) h[x] = t0 + x < a.r ? a.H[i * a.r + t0 + x] : 0.0f;
+    *(float4 *)(a.Hp + i * a.rp + t0) = make_float4(h[0], h[1], h[2], h[3]);
+    *(float4 *)(a.Hp + i * a.rp + t0 + 4) = make_float4(h[4], h[5], h[6], h[7]);
+  }
 }
 
 template <bool MUL>
@@ -428,7 +441,7 @@ qlora_status launch_int8_layout(const uint16_t *A, const uint16_t *B, int64_t d,
   const CopyArgs a{A, B, d, k, M, r, rp, At, Bt, H, Hp};
   const int64_t n = ql_rup(d, 256) + ql_rup(k, 256) + (H ? M : 0);
   QlProf prof(QLORA_K_LAYOUT, st);
-  int8_layout_kernel<<<(unsigned)ql_cdiv(n, 256), 256, 0, st>>>(a);
+  int8_layout_kernel<<<dim3((unsigned)ql_cdiv(n, 256), (unsigned)(rp / 8)), 256, 0, st>>>(a);
   QL_LAUNCH_CHECK();
   return QLORA_OK;
 }
