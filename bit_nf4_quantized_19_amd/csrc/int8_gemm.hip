@@ -8,6 +8,22 @@
 // does not change a bit of the result. As in the NF4 GEMM the product is
 // computed transposed (weights are the MFMA's A operand), so each lane ends
 // with 4 consecutive n of one token, and s H (s G) comes as bf16 hi + lo parts.
+//
+// GEMM: tile 128 (n) x 256 (m), K-step 128, eight waves of 32 x 128, one
+// workgroup per CU. Both tiles' rows of a step (384 x 128 bytes) come by LDS DMA,
+// three stages, two to three steps ahead; in a step every wave reads the operands
+// of a K-slice of 64 while the products of the slice before run, and the one
+// barrier of the step lies between its two slices, so that the first reads of
+// the next stage run under the second slice's products. dX needs the weight's
+// columns: its tile holds 128 rows of the weight as they lie in memory, read by
+// the transposing LDS read (8 rows x 16 columns per 16 lanes). LDS rows are
+// permuted by 16-byte chunks (no bank conflicts counted in either mode).
+// 2048 tokens of 4096 x 4096: forward 36.5 us (1.88 POP/s; the vendor library's
+// int8 product of that shape, without scales and rank-r term, 42), dX 38.5. A
+// step takes 0.82-0.95 us for 0.43 of matrix work at the full clock: on zero
+// operands the same kernel's steps take three quarters of the time, so about a
+// quarter goes to the clock that the chip can hold; without the DMAs they take
+// 0.70. L2 serves 85% of the DMAs (84 MB of misses).
 #include "kernels.h"
 
 namespace {
@@ -532,7 +548,14 @@ __global__ __launch_bounds__(64 * GV_W) void int8_gemv_kernel(I8Gemv g) {
 }
 
 // ---- host -----------------------------------------------------------------------
-// Tile and splits of a product of M tokens, N columns, K codes.
+// Tile and splits of a product of M tokens, N columns, K codes, by the least
+// time of what was measured, in us: a workgroup takes a fixed time for its start
+// and end and a time per K-step that grows by a quarter as the chip fills; a
+// split adds the partial sums' way through memory and the join. Measured, the
+// tiles 128 x 256 / 128 x 128 / the chosen one: 4096 x 4096, 64 tokens 27 / 17 /
+// 10.6 (128 x 64, four splits), 128 tokens 27 / 17 / 13.3, 512 28 / 17.6, 2048
+// 33.7 / 37; 4096 x 11008, 128 tokens 63 / 37 / 17.8, 256 63 / 38 / 23 (128 x 128,
+// four splits), 777 64 / 42; 11008 x 4096, 2048 tokens 91 / 104.
 struct I8Plan {
   int cfg;        // 0: 128 x 256, 1: 128 x 128, 2: 128 x 64 (columns x tokens)
   int S;
@@ -540,20 +563,23 @@ struct I8Plan {
 };
 I8Plan i8_plan(int64_t M, int64_t N, int64_t K) {
   const int64_t tn = ql_cdiv(N, 128), nk = ql_cdiv(K, BK);
+  constexpr double kFixed[3] = {7.3, 5.2, 4.2}, kStep[3] = {0.65, 0.365, 0.268};
   I8Plan best{0, 1, tn * ql_cdiv(M, 256), 0};
   double least = -1.0;
   for (int cfg = 0; cfg < 3; ++cfg) {
     const int64_t bm = cfg == 0 ? 256 : cfg == 1 ? 128 : 64, tiles = tn * ql_cdiv(M, bm);
-    if (cfg == 2 && M > 64) continue;
-    const double step = cfg == 0 ? 0.95 : cfg == 1 ? 0.5 : 0.3;   // us
+    if (cfg == 2 && M > 128) continue;
     for (int S : {1, 2, 3, 4, 6, 8}) {
       if (S > 1 && (cfg == 0 || S * 2 > nk)) break;
       if (tiles * S >= int64_t(1) << 23) break;   // 2^32 threads; 128 x 256 tiles stay below
-      double t = (double)ql_cdiv(tiles * S, 256) * (step * (double)ql_cdiv(nk, S) + 6.0);
-      if (S > 1) t += 3.0 + (double)(S * tiles * bm * 128 * 4) * 2.0 / 5e6;
+      const int64_t wgs = tiles * S, bytes = wgs * bm * 128 * 4;
+      const double fill = wgs < 256 ? (double)wgs / 256.0 : 1.0;
+      double t = (double)ql_cdiv(wgs, 256) *
+                 (kFixed[cfg] + kStep[cfg] * (1.0 + 0.26 * fill) * (double)ql_cdiv(nk, S));
+      if (S > 1) t += 1.0 + (double)bytes / (cfg == 2 ? 1.25e6 : 1.85e6);
       if (least < 0.0 || t < least) {
         least = t;
-        best = I8Plan{cfg, S, tiles, S > 1 ? S * tiles * bm * 128 * 4 : 0};
+        best = I8Plan{cfg, S, tiles, S > 1 ? bytes : 0};
       }
     }
   }

@@ -165,12 +165,13 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(RowsArgs a) {
 // rows in registers, so In is read once, and every four ranks of P meet them in
 // 4x4x4 products of 16 blocks: lane l holds row l % 4 (of In, and of P) and 8
 // columns of block l / 4, so that a load takes 256 consecutive bytes of four
-// rows. (The 16x16 forms want 16 rows x 64 bytes a load, which the address
-// units take twice as long for, and two-element dot products run at a quarter
-// of the rate of other vector instructions: 17 and 15 us for 2048 x 4096, r =
-// 16, against XX here.) The 16 blocks' sums are taken by exchanges that halve
-// the sums a lane holds with the lanes a sum is spread over; the waves' sums
-// meet in LDS in order.
+// rows. The 16 blocks' sums are taken by exchanges that halve the sums a lane
+// holds with the lanes a sum is spread over; the waves' sums meet in LDS in
+// order. 2048 x 4096, r = 16: 14 us; the records and the products one after the
+// other 15, with 16x16 products (16 rows x 64 bytes a load, which the address
+// units take twice as long for) 17, with two-element dot products (a quarter of
+// the rate of other vector instructions) 15. Sixteen more ranks add 4 us: P is
+// read by every workgroup, from L2. 16 tokens: 6 us against 10.
 struct PrepArgs {
   RowsArgs rows;       // rows.q == NULL: no records
   const uint16_t *P;   // pr x cols; rows past pr count as zeros
