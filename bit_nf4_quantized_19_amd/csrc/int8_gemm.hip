@@ -23,7 +23,7 @@
 // step takes 0.82-0.95 us for 0.43 of matrix work at the full clock: on zero
 // operands the same kernel's steps take three quarters of the time, so about a
 // quarter goes to the clock that the chip can hold; without the DMAs they take
-// 0.70. L2 serves 85% of the DMAs (84 MB of misses).
+// 0.70. L2 serves 81% of the requests (85 MB of misses).
 #include "kernels.h"
 
 namespace {

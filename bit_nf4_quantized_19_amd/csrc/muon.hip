@@ -13,6 +13,15 @@
 // and sums are taken in float64 on the matrix cores (16x16x4): products of two
 // float32 are exact there, and nothing overflows.
 //
+// HBM-bound: 10 bytes an element in gram and 16 in apply, 20 if nothing were read
+// twice; the matrix work in float64 is about 0.4 of gram's and of apply's time
+// for 64 ranks. A workgroup's elements of a 64-column chunk go through LDS, so
+// that memory is read and written in 16-byte pieces whatever the orientation;
+// four workgroups a compute unit hide each other's latency (holding the next
+// chunk in registers instead, two a compute unit, took 329 us against 300).
+// 80 matrices of 64 x 8192: 298 us a pass (gram 105, iterate 47, apply 165), 2.8
+// TB/s of the 20 bytes; one of 16 x 4096: 15 us (3.4, 7.1, 3.0); one of 128 x
+// 4096: 139 us, of which the ten launches of its steps take 110.
 // Three launches: gram (updates the momentum; partial Gram sums of a range of
 // the long side), iterate (one workgroup per matrix: joins the partial sums in
 // a fixed order, then the steps; more than 64 ranks take two launches a step
@@ -296,22 +305,26 @@ __global__ __launch_bounds__(iterate_threads<NB>()) void muon_iterate_kernel(Muo
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t mat = blockIdx.x;
   const double *part = a.part + mat * a.split * NT * 256;
-  auto join = [&](int e, int x0, int x1) {   // partial sums x0 .. x1 - 1 of element e
-    double v = 0.0;
-    int x = x0;
-    for (; x + 16 <= x1; x += 16) {
-      double y[16];
+  // Partial sums x0 .. x1 - 1 of the thread's E elements e0, e0 + NTH, ..., the
+  // loads of XB of them in flight.
+  constexpr int E = NB == 1 ? 1 : (NT * 256 + NTH - 1) / NTH, XB = E > 3 ? 8 : 16;
+  auto join = [&](int e0, int x0, int x1, double (&v)[E]) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = part[(int64_t)(x + i) * NT * 256 + e];
+    for (int i = 0; i < E; ++i) v[i] = 0.0;
+    for (int x = x0; x < x1; x += XB) {
+      double y[E][XB];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v += y[i];
+      for (int i = 0; i < E; ++i)
+#pragma unroll
+        for (int h = 0; h < XB; ++h) {
+          const int e = e0 + i * NTH;
+          y[i][h] = x + h < x1 && e < NT * 256 ? part[(int64_t)(x + h) * NT * 256 + e] : 0.0;
+        }
+#pragma unroll
+      for (int h = 0; h < XB; ++h)
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] += y[i][h];
     }
-    double y[15];
-#pragma unroll
-    for (int i = 0; i < 15; ++i) y[i] = x + i < x1 ? part[(int64_t)(x + i) * NT * 256 + e] : 0.0;
-#pragma unroll
-    for (int i = 0; i < 15; ++i) v += y[i];
-    return v;
   };
   auto place_sum = [&](int e, double v) {
     int t = e >> 8, i = 0;
@@ -322,14 +335,20 @@ __global__ __launch_bounds__(iterate_threads<NB>()) void muon_iterate_kernel(Muo
   };
   if (NB == 1) {   // four quarters of the partial sums at once
     const int y = threadIdx.x >> 8;
-    s_j[threadIdx.x] = join(threadIdx.x & 255, y * a.split / 4, (y + 1) * a.split / 4);
+    double v[E];
+    join(threadIdx.x & 255, y * a.split / 4, (y + 1) * a.split / 4, v);
+    s_j[threadIdx.x] = v[0];
     __syncthreads();
     if (threadIdx.x < 256) {
       const int e = threadIdx.x;
       place_sum(e, s_j[e] + s_j[256 + e] + s_j[512 + e] + s_j[768 + e]);
     }
   } else {
-    for (int e = threadIdx.x; e < NT * 256; e += NTH) place_sum(e, join(e, 0, a.split));
+    double v[E];
+    join(threadIdx.x, 0, a.split, v);
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if ((int)threadIdx.x + i * NTH < NT * 256) place_sum(threadIdx.x + i * NTH, v[i]);
   }
   __syncthreads();
   if (wave == 0) {
