@@ -610,8 +610,9 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
   auto fetch = [&](int64_t ch) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const Group x = mine.group(a, ch, j);
+      Group x = mine.group(a, ch, j);
       load4<VEC>(m, x, mv[j]);
+      x.n = a.s.nesterov ? x.n : 0;   // else u is m'
       load4<VEC>(g, x, gv[j]);
     }
   };
