@@ -1018,6 +1018,10 @@ def muon_step(param: torch.Tensor, momentum: torch.Tensor, grad: torch.Tensor,
     param and momentum may be CUDA tensors or page-locked host tensors, as in
     ``adamw_step``."""
     n, rows, cols = _matrices(param)
+    if param.numel() == 0:
+        raise ValueError("param has no elements")
+    if len(coefficients) != 3:
+        raise ValueError("the iteration has three coefficients")
     for t, name in ((param, "param"), (momentum, "momentum")):
         if t.dtype != torch.float32 or not t.is_contiguous() or t.shape != param.shape:
             raise ValueError(f"{name} must be a contiguous float32 tensor of shape "

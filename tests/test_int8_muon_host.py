@@ -190,3 +190,23 @@ def test_host_tensors_and_wrong_shapes_are_refused():
         ops.muon_step(p[0, 0], p[0, 0].clone(), g, g.clone())
     with pytest.raises(ops.QLoRAError):
         ops.muon_workspace(torch.zeros(200, 200), device="cpu")
+
+
+@pytest.mark.parametrize("coefficients", [(), (3.4445,), (3.4445, -4.7750),
+                                          (3.4445, -4.7750, 2.0315, 1.0)])
+def test_other_than_three_coefficients_are_refused(coefficients):
+    """Two of them would put the number of steps in the third's place."""
+    import torch
+    p = torch.zeros(4, 64)
+    g = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="three coefficients"):
+        ops.muon_step(p, p.clone(), g, g.clone(), coefficients=coefficients)
+
+
+@pytest.mark.parametrize("shape", [(4, 0), (0, 64), (0, 4, 64), (2, 4, 0)])
+def test_empty_parameters_are_refused(shape):
+    import torch
+    p = torch.zeros(shape)
+    g = torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="no elements"):
+        ops.muon_step(p, p.clone(), g, g.clone(), ws=torch.zeros(256, dtype=torch.uint8))
