@@ -18,12 +18,12 @@
 // columns: its tile holds 128 rows of the weight as they lie in memory, read by
 // the transposing LDS read (8 rows x 16 columns per 16 lanes). LDS rows are
 // permuted by 16-byte chunks (no bank conflicts counted in either mode).
-// 2048 tokens of 4096 x 4096: forward 36.5 us (1.88 POP/s; the vendor library's
-// int8 product of that shape, without scales and rank-r term, 42), dX 38.5. A
-// step takes 0.82-0.95 us for 0.43 of matrix work at the full clock: on zero
-// operands the same kernel's steps take three quarters of the time, so about a
-// quarter goes to the clock that the chip can hold; without the DMAs they take
-// 0.70. L2 serves 81% of the requests (85 MB of misses).
+// 2048 tokens of 4096 x 4096: forward 37-40 us (1.7-1.85 POP/s; the vendor
+// library's int8 product of that shape, without scales and rank-r term, 42), dX
+// 38-41. A step takes 0.82-0.97 us for 0.43 of matrix work at the full clock and
+// 0.70 without the DMAs. With 32x32x32 products its steps took three quarters of
+// the time on zero operands, so there a quarter went to the clock that the chip
+// can hold. L2 serves 81% of the requests (85 MB of misses).
 #include "kernels.h"
 
 namespace {

@@ -13,15 +13,17 @@
 // and sums are taken in float64 on the matrix cores (16x16x4): products of two
 // float32 are exact there, and nothing overflows.
 //
-// HBM-bound: 10 bytes an element in gram and 16 in apply, 20 if nothing were read
-// twice; the matrix work in float64 is about 0.4 of gram's and of apply's time
-// for 64 ranks. A workgroup's elements of a 64-column chunk go through LDS, so
+// HBM-bound: 10 bytes an element in gram and 16 in apply (14 without Nesterov,
+// where u is m'), 20 if nothing were read twice; the matrix work in float64, at
+// the peak rate of 79 TFLOP/s, is 0.4 of gram's and of apply's time for 64 ranks.
+// A workgroup's elements of a 64-column chunk go through LDS, so
 // that memory is read and written in 16-byte pieces whatever the orientation;
 // four workgroups a compute unit hide each other's latency (holding the next
 // chunk in registers instead, two a compute unit, took 329 us against 300).
-// 80 matrices of 64 x 8192: 298 us a pass (gram 105, iterate 47, apply 165), 2.8
-// TB/s of the 20 bytes; one of 16 x 4096: 15 us (3.4, 7.1, 3.0); one of 128 x
-// 4096: 139 us, of which the ten launches of its steps take 110.
+// 80 matrices of 64 x 8192 with Nesterov: 298 us a pass (gram 104, iterate 46,
+// apply 163; 157 without), 2.8 TB/s of the 20 bytes; one of 16 x 4096: 15 us
+// (3.4, 7.1, 3.0); one of 128 x 4096: 139 us, 106 of them the ten launches of its
+// steps.
 // Three launches: gram (updates the momentum; partial Gram sums of a range of
 // the long side), iterate (one workgroup per matrix: joins the partial sums in
 // a fixed order, then the steps; more than 64 ranks take two launches a step
@@ -612,7 +614,9 @@ __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs a) {
     for (int j = 0; j < NB; ++j) {
       Group x = mine.group(a, ch, j);
       load4<VEC>(m, x, mv[j]);
-      x.n = a.s.nesterov ? x.n : 0;   // else u is m'
+      // without Nesterov u is m'; a mask, as a branch around the loads parted
+      // them from m's and took 172 us, not 157
+      x.n = a.s.nesterov ? x.n : 0;
       load4<VEC>(g, x, gv[j]);
     }
   };
