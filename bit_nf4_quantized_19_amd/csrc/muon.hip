@@ -53,7 +53,7 @@ struct MuonArgs {
   int64_t chunks;            // of CK along the long side
   double *part;              // [n][split][tiles][256]
   double *Q;                 // [n][RP][RP], Q / (|u| + eps)
-  double *S, *P, *inv;       // more than 64 ranks: [n][RP][RP], the same, [n]
+  double *S, *P, *inv;       // more than 64 ranks: [n][RP][RP], the same (P^T), [n]
   MuonScalars s;
 };
 
@@ -439,8 +439,13 @@ __global__ __launch_bounds__(iterate_threads<NB>()) void muon_iterate_kernel(Muo
 // One compute unit takes 232 us for the 17 products of 128 x 128 in float64, so
 // the columns of a matrix are dealt to NB workgroups and a step is two
 // launches: poly (P from all of S) and advance (the workgroup's columns of Q
-// and S from all of P). Both read their left operand from L2 by rows, as S and
-// P are symmetric up to rounding.
+// and S from all of P). Both read their left operand from L2 by rows, that is
+// transposed: S as it is, symmetric up to rounding, P from where poly put its
+// transpose. The difference matters there: with P^T for P, Q comes out as the
+// transpose of what apply, which reads its columns as rows, can use. Rounding
+// then grew by a^3 a step (the update of a rank-one 80 x 300 off by 9e-5 after
+// eight steps and 0.15 after ten, of a size of one; so 3e-8, the rounding of the
+// float32 parameters, after either).
 // Partial sums of one 16 x 16 tile and its mirror image, in order.
 template <int NB>
 __global__ __launch_bounds__(256) void muon_join_kernel(MuonArgs a) {
@@ -511,8 +516,8 @@ __global__ __launch_bounds__(256) void muon_poly_kernel(MuonArgs a, int first) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int row = 16 * b + 4 * q + k4;
-      P[row * RP + col + c16] = (row == col + c16 ? a.s.a : 0.0) + a.s.b * s_b[row * 16 + c16] +
-                                a.s.c * (sc * d[r][q]);
+      P[(col + c16) * RP + row] = (row == col + c16 ? a.s.a : 0.0) +   // transposed
+                                  a.s.b * s_b[row * 16 + c16] + a.s.c * (sc * d[r][q]);
     }
   }
 }
@@ -542,7 +547,7 @@ __global__ __launch_bounds__(256) void muon_advance_kernel(MuonArgs a, int first
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int at = (16 * b + 4 * q + k4) * RP + col + c16;
-      const double v = first ? P[at] : d[r][q];
+      const double v = first ? P[at] : d[r][q];   // the first P: symmetric to a rounding
       Q[at] = last ? v * inv : v;
     }
   }

@@ -1,0 +1,72 @@
+"""The orthogonalised step over its accepted step counts, on updates of low rank.
+
+Bound: the small matrices' roundings move X_steps by less than
+a^(2 steps) 2^-53 of its largest singular value (at most 1.3), where their count
+adds up like its root: sqrt(len + 4 R steps) of them at the most. Then the
+float32 roundings of the elementwise operations, as in test_gpu_muon."""
+
+import numpy as np
+import pytest
+
+from oracle import muon as omu
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+U24, U53 = 2.0 ** -24, 2.0 ** -53
+NS = (3.4445, -4.7750, 2.0315)
+
+
+@pytest.fixture(scope="module")
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from bit_nf4_quantized_19_amd import ops as o
+    o.lib()
+    return o
+
+
+def updates(rows, cols, seed):
+    """Four matrices: an outer product, one of rank 4, one whose rows come in
+    equal pairs, one of three nonzero columns of its long side (all as float32)."""
+    rng = np.random.default_rng(seed)
+    small, long = min(rows, cols), max(rows, cols)
+    n = rng.standard_normal
+    pairs = n((small, long))
+    pairs[small // 2:2 * (small // 2)] = pairs[:small // 2]
+    few = np.zeros((small, long))
+    few[:, :3] = n((small, 3))
+    v = np.stack([np.outer(n(small), n(long)), n((small, 4)) @ n((4, long)), pairs, few])
+    v = (v if rows <= cols else v.transpose(0, 2, 1)).astype(np.float32)
+    return np.ascontiguousarray(v)
+
+
+@pytest.mark.parametrize("coefficients,steps", [(NS, 0), (NS, 1), (NS, 8), (NS, 10),
+                                                ((15 / 8, -10 / 8, 3 / 8), 19),
+                                                ((1.5, -0.5, 0.0), 30)])
+@pytest.mark.parametrize("rows,cols", [(12, 256), (16, 1000), (300, 33), (64, 2048), (513, 64),
+                                       (80, 300), (700, 100), (128, 515)])
+def test_low_rank_updates(ops, rows, cols, coefficients, steps):
+    print(f"[muon low rank] {rows} x {cols} steps={steps} {coefficients}", flush=True)
+    u = updates(rows, cols, rows + cols)
+    p = np.random.default_rng(1).standard_normal(u.shape).astype(np.float32)
+    tp, tm = torch.from_numpy(p).cuda(), torch.from_numpy(u).cuda()
+    g = torch.zeros(u.shape, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(g)
+    lr, beta = 0.25, 0.5     # powers of two: the momentum is u / 2, exactly
+    ops.muon_step(tp, tm, g, out, lr=lr, beta=beta, nesterov=False, steps=steps, eps=0.0,
+                  scale=1.0, coefficients=coefficients)
+    torch.cuda.synchronize()
+    assert torch.equal(tm, torch.from_numpy(u * np.float32(0.5)).cuda())
+    got = tp.cpu().numpy().astype(np.float64)
+    R, length = min(rows, cols), max(rows, cols)
+    grown = max(1.0, abs(coefficients[0])) ** (2 * steps) * U53
+    for i in range(u.shape[0]):
+        x = omu.orthogonalise(u[i] * 0.5, coefficients, steps, 0.0)
+        # the float64 iteration on the matrix has roundings of its own, a^steps 2^-53
+        tol = 1.3 * np.sqrt(length + 4 * R * max(steps, 1)) * grown + 4 * U24 * abs(x)
+        want = p[i] - lr * x
+        tol = lr * tol + U24 * (abs(want) + lr * tol)
+        off = abs(got[i] - want)
+        assert (off <= tol).all(), (i, off.max(), (off / tol).max())
+    assert torch.equal(out, tp.bfloat16())
