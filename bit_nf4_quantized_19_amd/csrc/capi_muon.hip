@@ -11,6 +11,17 @@ bool muon_shape_ok(int64_t n, int64_t rows, int64_t cols) {
   const int64_t small = rows < cols ? rows : cols, len = rows < cols ? cols : rows;
   return n <= 65535 && small <= QLORA_MUON_MAX_RANK && len <= (int64_t(1) << 24);
 }
+// S is carried by S' = P S P, apart from u. A direction of a small singular value
+// has an eigenvalue of S that is wrong by about 2^-53 of the largest, and below
+// zero as often as above: every step multiplies it by a^2, and one that comes
+// near -1 would run to infinity, as all of P's terms then add up. The update's
+// error is 0.1 to 0.6 of a^(2 steps) 2^-53 of its largest direction over spectra
+// of eight decades; the limit, 2^-17 (10 steps of the usual coefficients, 30 of
+// 1.5 and -0.5), keeps it below the parameters' own rounding at lr = 0.02.
+// One step does not use S'.
+bool steps_ok(double a, int steps) {
+  return steps <= 1 || fabs(a) <= 1.0 || 2.0 * steps * log2(fabs(a)) <= 36.0;
+}
 bool not_negative(double x) { return isfinite((float)x) && x >= 0.0; }
 
 }  // namespace
@@ -37,6 +48,7 @@ qlora_status qlora_muon_step(float *param, float *momentum, const uint16_t *grad
     return QLORA_ERR_INVALID_ARG;
   if (hp->steps < 0 || hp->steps > QLORA_MUON_MAX_STEPS || (hp->nesterov & ~1))
     return QLORA_ERR_INVALID_ARG;
+  if (!steps_ok(hp->a, hp->steps)) return QLORA_ERR_UNSUPPORTED;
   if (!ws_ok(ws, ws_bytes, (int64_t)muon_ws_bytes(n, rows, cols))) return QLORA_ERR_WORKSPACE;
   void *dv[4];
   const void *hv[4] = {param, momentum, grad, param_bf16};

@@ -8,10 +8,12 @@
 //   Q_{j+1} = P_j Q_j,   S_{j+1} = P_j S_j P_j,   X_steps = Q_steps X0:
 // the iteration runs on R x R matrices and u is read twice in all, once for
 // S_0 and once for the update, whatever the number of steps. A direction with
-// a small singular value grows by `a` a step, and the rounding of S_0 and Q
-// with it (485-fold after five steps of the usual coefficients), so products
+// a small singular value grows by `a` a step, and the rounding of S_0 by a^2
+// (485- and 235000-fold after five steps of the usual coefficients), so products
 // and sums are taken in float64 on the matrix cores (16x16x4): products of two
-// float32 are exact there, and nothing overflows.
+// float32 are exact there and their sums do not overflow. The caller bounds
+// a^(2 steps): S is not formed from X again, so roundings that grow to its own
+// size could make it negative, and the iteration run to infinity.
 //
 // HBM-bound: 10 bytes an element in gram and 16 in apply (14 without Nesterov,
 // where u is m'), 20 if nothing were read twice; the matrix work in float64, at

@@ -1014,6 +1014,8 @@ def muon_step(param: torch.Tensor, momentum: torch.Tensor, grad: torch.Tensor,
     rows x cols or n x rows x cols, each matrix on its own, the smaller side at
     most 128) with the bf16 gradient, writing the bf16 copy of the updated
     parameter. ``scale`` of the update: sqrt(max(1, rows / cols)) by default.
+    ``steps`` up to 32 and a^(2 steps) <= 2^36, a being the first of the
+    coefficients (10 with these), past which roundings would show.
 
     param and momentum may be CUDA tensors or page-locked host tensors, as in
     ``adamw_step``."""

@@ -70,3 +70,12 @@ def test_low_rank_updates(ops, rows, cols, coefficients, steps):
         off = abs(got[i] - want)
         assert (off <= tol).all(), (i, off.max(), (off / tol).max())
     assert torch.equal(out, tp.bfloat16())
+
+
+def test_counts_past_the_limit_are_refused(ops):
+    p = torch.ones(1, 8, 64, device="cuda")
+    m, g = p.clone(), p.bfloat16()
+    for steps, coefficients in ((11, NS), (32, NS), (31, (1.5, -0.5, 0.0))):
+        with pytest.raises(ops.QLoRAError):
+            ops.muon_step(p, m, g, torch.empty_like(g), steps=steps, coefficients=coefficients)
+    assert bool((p == 1).all()) and bool((m == 1).all())
