@@ -201,6 +201,13 @@ QL_DEV void get4(const MuonArgs &a, int j, const float *s, float (&v)[4]) {
   }, [&](int at, int x) { v[x] = s[at]; });
 }
 
+// 1 / (|u| + eps) from the trace of u's Gram matrix. Nothing scales a zero u
+// (eps = 0: 0 / 0); otherwise |u| is at least 2^-149, so that the square of the
+// result stays finite however small eps is.
+QL_DEV double inverse_size(double trace, double eps) {
+  return trace == 0.0 && eps > 0.0 ? 0.0 : 1.0 / (sqrt(trace) + eps);
+}
+
 template <int NB, bool TALL, bool VEC>
 __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs a) {
   constexpr int ST = gram_stride<NB, TALL>(), LN = chunk_floats<NB, TALL, ST>();
@@ -362,7 +369,7 @@ __global__ __launch_bounds__(iterate_threads<NB>()) void muon_iterate_kernel(Muo
     if (lane == 0) s_tr = tr;
   }
   __syncthreads();
-  const double inv = 1.0 / (sqrt(s_tr) + a.s.eps);
+  const double inv = inverse_size(s_tr, a.s.eps);
   for (int e = threadIdx.x; e < RP * LS; e += NTH) s_a[e] *= inv * inv;
   __syncthreads();
 
@@ -466,14 +473,14 @@ __global__ __launch_bounds__(256) void muon_join_kernel(MuonArgs a) {
   if (t) S[col * RP + row] = v;
 }
 
-// 1 / (|u| + eps) of the matrix whose Gram sums are S.
+// inverse_size of the matrix whose Gram sums are S.
 template <int NB>
 QL_DEV double inverse_size(const MuonArgs &a, const double *S) {
   constexpr int RP = 16 * NB;
   double tr = 0.0;   // every wave for itself, in the same order
   for (int i = threadIdx.x & 63; i < RP; i += 64) tr += S[i * RP + i];
   for (int o = 32; o; o >>= 1) tr += __shfl_xor(tr, o);
-  return 1.0 / (sqrt(tr) + a.s.eps);
+  return inverse_size(tr, a.s.eps);
 }
 // Row blocks wave and wave + 4 of (rows of L) times the panel in LDS.
 template <int NB>

@@ -79,3 +79,31 @@ def test_counts_past_the_limit_are_refused(ops):
         with pytest.raises(ops.QLoRAError):
             ops.muon_step(p, m, g, torch.empty_like(g), steps=steps, coefficients=coefficients)
     assert bool((p == 1).all()) and bool((m == 1).all())
+
+
+@pytest.mark.parametrize("eps", [1e-7, 1e-100, 1e-200, 5e-324])
+@pytest.mark.parametrize("rows,cols,steps", [(12, 256, 5), (300, 40, 5), (80, 300, 5),
+                                             (12, 256, 0), (80, 300, 0), (16, 64, 1)])
+def test_zero_updates_take_the_decay_alone(ops, rows, cols, steps, eps):
+    """Whatever eps > 0 is: the zero matrix beside one that is not, which an eps
+    far below its size leaves as eps = 0 does."""
+    u = updates(rows, cols, 5)[:2]
+    u[0] = 0
+    p = np.random.default_rng(2).standard_normal(u.shape).astype(np.float32)
+    g = torch.zeros(u.shape, dtype=torch.bfloat16, device="cuda")
+
+    def run(first, e):
+        tp, tm = torch.from_numpy(p[first:]).cuda(), torch.from_numpy(u[first:]).cuda()
+        out = torch.empty_like(g[first:])
+        ops.muon_step(tp, tm, g[first:], out, lr=0.5, beta=0.5, weight_decay=0.5, steps=steps,
+                      eps=e)
+        torch.cuda.synchronize()
+        return tp, tm, out
+
+    tp, tm, out = run(0, eps)
+    half = np.float32(0.5)
+    want = p[0] - half * (half * p[0])
+    assert np.array_equal(tp[0].cpu().numpy(), want) and not tm[0].any()
+    assert torch.isfinite(tp).all() and torch.equal(out, tp.bfloat16())
+    if eps < 1e-50:
+        assert torch.equal(tp[1], run(0, 1e-60)[0][1])
