@@ -81,6 +81,13 @@ QL_DEV i32x4 mfma_i8(const i32x4 &a, const i32x4 &b, const i32x4 &c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
+// A token's scale as two factors, (s, 1) or, from 2^96 on, (s 2^-64, 2^64): a sum
+// (below 2^31) times the first does not overflow, so that a small channel scale
+// still makes it the ordinary number that it is before the second is taken.
+QL_DEV float2 token_scale(float s) {
+  return s > 0x1p96f ? make_float2(s * 0x1p-64f, 0x1p64f) : make_float2(s, 1.0f);
+}
+
 constexpr int BK = 128;   // K-step: 128 codes
 constexpr int SL = BK / 64;   // K-slices of a step
 
@@ -175,12 +182,14 @@ QL_DEV void epilogue(const I8Args &g, const i32x4 (&acc)[TI][TJ], EpilogueIn<MOD
   for (int i = 0; i < TI; ++i) {
     const float w[4] = {in.sw[i].x, in.sw[i].y, in.sw[i].z, in.sw[i].w};
 #pragma unroll
-    for (int j = 0; j < TJ; ++j)
+    for (int j = 0; j < TJ; ++j) {
+      const float2 s = token_scale(in.sx[j]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float f = (float)acc[i][j][q] * in.sx[j];
-        v[i][j][q] = MODE == 0 ? f * w[q] : f;
+        const float f = (float)acc[i][j][q];
+        v[i][j][q] = MODE == 0 ? f * s.x * w[q] * s.y : f * in.sx[j];
       }
+    }
   }
   for (int t0 = 0; t0 < g.rp; t0 += 32)
 #pragma unroll
@@ -541,7 +550,8 @@ __global__ __launch_bounds__(64 * GV_W) void int8_gemv_kernel(I8Gemv g) {
     int sum = 0;
 #pragma unroll
     for (int v = 0; v < GV_W; ++v) sum += s_red[v][b][q][l];
-    float y = (float)sum * g.sx[t] * g.sw[n0 + n];
+    const float2 s = token_scale(g.sx[t]);
+    float y = (float)sum * s.x * g.sw[n0 + n] * s.y;
     for (int v = 0; 16 * v < g.rp; ++v) y += s_lr[v][b][q][l];
     g.Y[(int64_t)t * g.d + n0 + n] = ql::f_to_bf16(y);
   }
