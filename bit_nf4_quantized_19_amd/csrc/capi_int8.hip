@@ -36,7 +36,8 @@ struct FwdWs {
   void *part;
   int64_t ldq, bytes;
 };
-FwdWs fwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
+// any: sized for every call of up to M tokens, whose partial sums may be larger
+FwdWs fwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r, bool any = false) {
   const int64_t rp = ql_rup(r, 16);
   Carve c{base};
   FwdWs L{};
@@ -46,7 +47,9 @@ FwdWs fwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
   L.H = c.take<float>(M * rp * 4);
   L.hi = c.take<uint16_t>(M * rp * 2);
   L.lo = c.take<uint16_t>(M * rp * 2);
-  L.part = c.take<void>(M > INT8_GEMV_TOKENS ? (int64_t)int8_gemm_part_bytes(M, d, k) : 0);
+  L.part = c.take<void>(M <= INT8_GEMV_TOKENS ? 0
+                        : (int64_t)(any ? int8_gemm_part_bytes_upto(M, d, k)
+                                        : int8_gemm_part_bytes(M, d, k)));
   L.bytes = c.off;
   return L;
 }
@@ -59,7 +62,7 @@ struct BwdWs {
   int64_t ldq, bytes;
 };
 // sized for the largest case (H recomputed, dX requested)
-BwdWs bwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
+BwdWs bwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r, bool any = false) {
   const int rp = (int)ql_rup(r, 16);
   Carve c{base};
   BwdWs L{};
@@ -75,7 +78,8 @@ BwdWs bwd_layout(char *base, int64_t d, int64_t k, int64_t M, int r) {
     L.Bt = c.take<uint16_t>((int64_t)rp * d * 2);
     L.cpart = c.take<float>((int64_t)colacc_part_bytes(M, d, k, rp));
   }
-  L.part = c.take<void>((int64_t)int8_gemm_part_bytes(M, k, d));
+  L.part = c.take<void>((int64_t)(any ? int8_gemm_part_bytes_upto(M, k, d)
+                                      : int8_gemm_part_bytes(M, k, d)));
   L.bytes = c.off;
   return L;
 }
@@ -95,8 +99,8 @@ qlora_status qlora_int8_quantize(const uint16_t *W, const qlora_int8_weight *out
 size_t qlora_int8_workspace_bytes(int32_t op, int64_t d, int64_t k, int64_t M, int32_t r) {
   if (check_shape(d, k) != QLORA_OK || M < 1 || M > QLORA_INT8_MAX_TOKENS || r < 0 || r > 128)
     return (size_t)-1;
-  if (op == QLORA_OP_FWD) return (size_t)fwd_layout(nullptr, d, k, M, r).bytes;
-  if (op == QLORA_OP_BWD) return (size_t)bwd_layout(nullptr, d, k, M, r).bytes;
+  if (op == QLORA_OP_FWD) return (size_t)fwd_layout(nullptr, d, k, M, r, true).bytes;
+  if (op == QLORA_OP_BWD) return (size_t)bwd_layout(nullptr, d, k, M, r, true).bytes;
   return (size_t)-1;
 }
 

@@ -622,6 +622,20 @@ size_t int8_gemm_part_bytes(int64_t M, int64_t N, int64_t K) {
   return (size_t)i8_plan(M, N, K).part;
 }
 
+// The partial sums grow and fall with M. A plan is the same for 1 to 64 tokens,
+// 65 to 128, and every 128 from there. By the times above a split saves at most
+// the idle part of a round, kFixed + 0.46 nk us, and adds at least
+// tiles (kFixed / 256 + 0.07) us, so that none is taken past 256 + 6 nk tiles.
+size_t int8_gemm_part_bytes_upto(int64_t M, int64_t N, int64_t K) {
+  const int64_t tn = ql_cdiv(N, 128), most = 256 + 6 * ql_cdiv(K, BK);
+  int64_t bytes = 0;
+  for (int64_t m = 1; m <= M && tn * (m / 128) <= most; m = m == 1 ? 65 : m == 65 ? 129 : m + 128) {
+    const int64_t part = i8_plan(m, N, K).part;
+    bytes = part > bytes ? part : bytes;
+  }
+  return (size_t)bytes;
+}
+
 qlora_status launch_int8_gemm(int mode, const int8_t *W, const float *sw, int64_t d, int64_t k,
                               const int8_t *In, int64_t ldi, const float *sx, int64_t M,
                               const uint16_t *L, int ldl, const uint16_t *hi, const uint16_t *lo,

@@ -237,9 +237,11 @@ qlora_status launch_int8_prep(const uint16_t *X, int64_t rows, int64_t cols, con
 // int8_gemm.hip : the product with a d x k record, forward (mode 0) or dX
 // (mode 1). In: M x ldi codes, ldi a multiple of 128, zero past the
 // contraction; sx [M]. The rank-r term is (hi + lo) L^T: hi, lo M x rp, L columns x
-// ldl with ldl = rp (zero past the rank) or the rank itself; rp == 0: none. part: int8_gemm_part_bytes(M, columns,
-// contraction) bytes of workspace.
+// ldl with ldl = rp (zero past the rank) or the rank itself; rp == 0: none. part:
+// int8_gemm_part_bytes(M, columns, contraction) bytes of workspace;
+// int8_gemm_part_bytes_upto: the most that any number of tokens up to M takes.
 size_t int8_gemm_part_bytes(int64_t M, int64_t N, int64_t K);
+size_t int8_gemm_part_bytes_upto(int64_t M, int64_t N, int64_t K);
 qlora_status launch_int8_gemm(int mode, const int8_t *W, const float *sw, int64_t d, int64_t k,
                               const int8_t *In, int64_t ldi, const float *sx, int64_t M,
                               const uint16_t *L, int ldl, const uint16_t *hi, const uint16_t *lo,

@@ -878,8 +878,8 @@ def int8_workspace_bytes(op: int, d: int, k: int, M: int, r: int) -> int:
 
 
 def int8_workspace(w: Int8Weight, M: int, r: int = 0, backward: bool = False) -> torch.Tensor:
-    """Workspace of the forward of M tokens (and of the backward too, when
-    asked); calls on one stream can share it."""
+    """Workspace of the forward of up to M tokens (and of the backward too, when
+    asked) with adapters of up to rank r; calls on one stream can share it."""
     b = int8_workspace_bytes(OP_FWD, w.d, w.k, M, r)
     if backward:
         b = max(b, int8_workspace_bytes(OP_BWD, w.d, w.k, M, r))

@@ -63,8 +63,8 @@ QLORA_API qlora_status qlora_int8_quantize(const uint16_t *W, const qlora_int8_w
                                            void *stream);
 
 /* Device workspace of the calls below in bytes for op QLORA_OP_FWD or
- * QLORA_OP_BWD, M tokens and rank r (0: no adapter); (size_t)-1 for an
- * unsupported shape. */
+ * QLORA_OP_BWD, up to M tokens and up to rank r (0: no adapter); (size_t)-1 for
+ * an unsupported shape. */
 QLORA_API size_t qlora_int8_workspace_bytes(int32_t op, int64_t d, int64_t k, int64_t M,
                                             int32_t r);
 
