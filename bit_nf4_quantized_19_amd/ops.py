@@ -905,12 +905,17 @@ def _int8_args(w: Int8Weight, named, A, B, r: int, ws):
 
 
 def linear_fwd_int8(w: Int8Weight, X: torch.Tensor, A: torch.Tensor | None = None,
-                    B: torch.Tensor | None = None, lora_alpha: float = 0.0, save_h: bool = True,
-                    Y: torch.Tensor | None = None, H: torch.Tensor | None = None,
+                    B: torch.Tensor | None = None, lora_alpha: float | None = None,
+                    save_h: bool = True, Y: torch.Tensor | None = None, H: torch.Tensor | None = None,
                     ws: torch.Tensor | None = None, stream=None):
     """Y = sx sw (Xq Wq^T) + (alpha/r) (X A^T) B^T on an 8-bit base, the tokens
-    quantised by row; without A and B the product alone. Returns (Y, H or None)."""
+    quantised by row; without A and B (and lora_alpha, which they need) the
+    product alone. Returns (Y, H or None)."""
     r = _int8_rank(A, B)
+    if lora_alpha is None:
+        if r:
+            raise ValueError("lora_alpha is needed with A and B")
+        lora_alpha = 0.0
     M = X.shape[0]
     save_h = save_h and r > 0
     if Y is None or ws is None or (save_h and H is None):
