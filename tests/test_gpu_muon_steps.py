@@ -107,3 +107,23 @@ def test_zero_updates_take_the_decay_alone(ops, rows, cols, steps, eps):
     assert torch.isfinite(tp).all() and torch.equal(out, tp.bfloat16())
     if eps < 1e-50:
         assert torch.equal(tp[1], run(0, 1e-60)[0][1])
+
+
+@pytest.mark.parametrize("rows,cols", [(16, 4096), (33, 300), (700, 64), (96, 515), (300, 128)])
+@pytest.mark.parametrize("steps", [5, 10])
+def test_singular_values_over_eight_decades(ops, rows, cols, steps):
+    """Updates whose gains are steepest in S, within the same bound."""
+    print(f"[muon decades] {rows} x {cols} steps={steps}", flush=True)
+    R, length = min(rows, cols), max(rows, cols)
+    rng = np.random.default_rng(rows)
+    q1, _ = np.linalg.qr(rng.standard_normal((R, R)))
+    q2, _ = np.linalg.qr(rng.standard_normal((length, R)))
+    u = ((q1 * np.logspace(0, -8, R)) @ q2.T).astype(np.float32)
+    u = np.ascontiguousarray(u if rows <= cols else u.T)
+    tp, tm = torch.zeros(rows, cols, device="cuda"), torch.from_numpy(u).cuda()
+    g = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    ops.muon_step(tp, tm, g, torch.empty_like(g), lr=1.0, beta=0.5, nesterov=False, steps=steps,
+                  eps=0.0, scale=1.0)
+    x = omu.orthogonalise(u * 0.5, NS, steps, 0.0)
+    tol = 1.3 * np.sqrt(length + 4 * R * steps) * NS[0] ** (2 * steps) * U53 + 2 * U24 * abs(x)
+    assert (abs(tp.cpu().numpy() + x) <= tol).all()
