@@ -16,9 +16,9 @@ bool muon_shape_ok(int64_t n, int64_t rows, int64_t cols) {
 // zero as often as above: every step multiplies it by a^2, and one that comes
 // near -1 would run to infinity, as all of P's terms then add up. The update's
 // error is 0.1 to 0.6 of a^(2 steps) 2^-53 of its largest direction over spectra
-// of eight decades; the limit, 2^-17 (10 steps of the usual coefficients, 30 of
-// 1.5 and -0.5), keeps it below the parameters' own rounding at lr = 0.02.
-// One step does not use S'.
+// of eight decades. At the limit, 2^-17 (10 steps of the usual coefficients, 30 of
+// 1.5 and -0.5), that is spread over a matrix of 16 x 4096 and times lr = 0.02 less
+// than the rounding of its float32 parameters. One step does not use S'.
 bool steps_ok(double a, int steps) {
   return steps <= 1 || fabs(a) <= 1.0 || 2.0 * steps * log2(fabs(a)) <= 36.0;
 }

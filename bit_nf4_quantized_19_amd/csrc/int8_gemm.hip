@@ -7,7 +7,8 @@
 // The integer sums are exact in int32 (K <= 131072), so how they are split
 // does not change a bit of the result. As in the NF4 GEMM the product is
 // computed transposed (weights are the MFMA's A operand), so each lane ends
-// with 4 consecutive n of one token, and s H (s G) comes as bf16 hi + lo parts.
+// with 4 consecutive n of one token, and s H (s G) comes as bf16 hi + lo parts
+// (together to 2^-16 of each value, before the output's rounding to 2^-8).
 //
 // GEMM: tile 128 (n) x 256 (m), K-step 128, eight waves of 32 x 128, one
 // workgroup per CU. Both tiles' rows of a step (384 x 128 bytes) come by LDS DMA,
@@ -20,10 +21,8 @@
 // permuted by 16-byte chunks (no bank conflicts counted in either mode).
 // 2048 tokens of 4096 x 4096: forward 37-40 us (1.7-1.85 POP/s; the vendor
 // library's int8 product of that shape, without scales and rank-r term, 42), dX
-// 38-41. A step takes 0.82-0.97 us for 0.43 of matrix work at the full clock and
-// 0.70 without the DMAs. With 32x32x32 products its steps took three quarters of
-// the time on zero operands, so there a quarter went to the clock that the chip
-// can hold. L2 serves 81% of the requests (85 MB of misses).
+// 38-41. A step takes 0.82-0.97 us for 0.43 of matrix work at the full clock.
+// L2 serves 81% of the requests (85 MB of misses).
 #include "kernels.h"
 
 namespace {
@@ -562,10 +561,11 @@ __global__ __launch_bounds__(64 * GV_W) void int8_gemv_kernel(I8Gemv g) {
 // time of what was measured, in us: a workgroup takes a fixed time for its start
 // and end and a time per K-step that grows by a quarter as the chip fills; a
 // split adds the partial sums' way through memory and the join. Measured, the
-// tiles 128 x 256 / 128 x 128 / the chosen one: 4096 x 4096, 64 tokens 27 / 17 /
-// 10.6 (128 x 64, four splits), 128 tokens 27 / 17 / 13.3, 512 28 / 17.6, 2048
-// 33.7 / 37; 4096 x 11008, 128 tokens 63 / 37 / 17.8, 256 63 / 38 / 23 (128 x 128,
-// four splits), 777 64 / 42; 11008 x 4096, 2048 tokens 91 / 104.
+// tiles 128 x 256 / 128 x 128 / the chosen one with its join: 4096 x 4096, 64
+// tokens 27 / 17 / 11.0 (128 x 64, three splits; four, by the model a hundredth
+// slower, 10.6), 128 tokens 27 / 17 / 13.2 (128 x 64), 512 28 / 18, 2048 35 / 39;
+// 4096 x 11008, 128 tokens 63 / 37 / 18.3 (128 x 64, four splits), 256 64 / 38 / 23
+// (128 x 128, four splits), 777 69 / 45; 11008 x 4096, 2048 tokens 92 / 109.
 struct I8Plan {
   int cfg;        // 0: 128 x 256, 1: 128 x 128, 2: 128 x 64 (columns x tokens)
   int S;

@@ -4,7 +4,7 @@
 // (e = fl(x * mul), the gradient with the channel scales folded in):
 //   s = fl(max|e| / 127),  q = clamp(rne(fl(e / s)), -127, 127),  s = 0: q = 0.
 // One read of the row, which stays in registers between its maximum and its
-// codes: a wave holds a row of up to 4096 values, a workgroup of four waves
+// codes: a wave holds a row of up to 1024 values, a workgroup of four waves
 // one of up to 16384; longer rows are read a second time. HBM-bound: 2 bytes
 // read and 1 written per value.
 //
@@ -178,7 +178,9 @@ struct PrepArgs {
   int pr, rp, r;
   int per;             // ranks of a workgroup, a multiple of NR
   float *out, *out2;   // M x rp, M x r (out2 may be NULL)
-  uint16_t *hi, *lo;   // M x rp: s out as bf16 high and low parts
+  // M x rp: s out as bf16 high and low parts, 2^-16 of it at most left out: two
+  // bf16 products for it in the GEMM's epilogue, whose output is rounded to 2^-8
+  uint16_t *hi, *lo;
   float s;
   int *zero;           // nzero ints cleared, for a later launch of the call
   int64_t nzero;

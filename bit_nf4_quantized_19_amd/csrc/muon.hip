@@ -20,11 +20,13 @@
 // the peak rate of 79 TFLOP/s, is 0.4 of gram's and of apply's time for 64 ranks.
 // A workgroup's elements of a 64-column chunk go through LDS, so
 // that memory is read and written in 16-byte pieces whatever the orientation;
-// four workgroups a compute unit hide each other's latency (holding the next
-// chunk in registers instead, two a compute unit, took 329 us against 300).
+// the workgroups of a compute unit hide each other's latency (by their registers
+// four of gram and three of apply for wide matrices of 64 ranks, eight up to 16;
+// holding the next chunk in registers instead, two a compute unit, took 329 us
+// against 300).
 // 80 matrices of 64 x 8192 with Nesterov: 298 us a pass (gram 104, iterate 46,
-// apply 163; 157 without), 2.8 TB/s of the 20 bytes; one of 16 x 4096: 15 us
-// (3.4, 7.1, 3.0); one of 128 x 4096: 139 us, 106 of them the ten launches of its
+// apply 163; 155 without), 2.8 TB/s of the 20 bytes; one of 16 x 4096: 15 us
+// (3.4, 7.2, 3.0); one of 128 x 4096: 141 us, 107 of them the ten launches of its
 // steps.
 // Three launches: gram (updates the momentum; partial Gram sums of a range of
 // the long side), iterate (one workgroup per matrix: joins the partial sums in
@@ -697,7 +699,9 @@ MuonPlan muon_plan(int64_t n, int64_t rows, int64_t cols) {
   p.len = rows < cols ? cols : rows;
   p.NB = (int)ql_cdiv(p.R, 16);
   p.chunks = ql_cdiv(p.len, CK);
-  int64_t s = n < 1024 ? 1024 / n : 1;   // about four workgroups a compute unit
+  // four workgroups for each compute unit, also where fewer fit (apply of 64
+  // ranks: 960 of 80 matrices on 768 places)
+  int64_t s = n < 1024 ? 1024 / n : 1;
   s = s < p.chunks ? s : p.chunks;
   p.split = (int)s;
   p.part = ql_rup(n * s * (p.NB * (p.NB + 1) / 2) * 2048, 256);

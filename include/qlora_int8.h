@@ -21,7 +21,10 @@
  * codes are taken. The rounding of X is passed straight through by the
  * backward, and that of dY sw changes an entry by at most se / 2. The sums of
  * code products are exact (int32), so they do not depend on how a call is
- * split; the LoRA branch reads X and dY unquantised.
+ * split; the LoRA branch reads X and dY unquantised. H and G are float32 sums;
+ * s H and s G enter Y and dX, and H and G enter dB and dA, as two bf16 parts
+ * that leave out at most 2^-16 of each value (an output is rounded to bf16, 2^-8
+ * of its own), with products and sums in float32.
  *
  * Conventions of qlora_nf4.h: every array is caller-owned device memory,
  * 16-byte aligned unless stated, every call only enqueues work on `stream`,
