@@ -742,9 +742,14 @@ void launch_nb(const MuonArgs &a, unsigned n, hipStream_t st) {
 
 }  // namespace
 
+// The workgroups of n matrices are at most max(n, 1024), n times the chunks of one
+// at the most; counting that many, the size serves fewer matrices too, which
+// may be split further (512 in two each, 600 not at all).
 size_t muon_ws_bytes(int64_t n, int64_t rows, int64_t cols) {
   const MuonPlan p = muon_plan(n, rows, cols);
-  return (size_t)(p.part + (p.NB <= 4 ? p.q : 3 * p.q + p.inv));
+  const int64_t most = n >= 1024 ? n : n * p.chunks < 1024 ? n * p.chunks : 1024;
+  const int64_t part = ql_rup(most * (p.NB * (p.NB + 1) / 2) * 2048, 256);
+  return (size_t)(part + (p.NB <= 4 ? p.q : 3 * p.q + p.inv));
 }
 
 qlora_status launch_muon(float *p, float *m, const uint16_t *g, uint16_t *out, int64_t n,

@@ -1000,8 +1000,9 @@ def _matrices(t: torch.Tensor):
 
 
 def muon_workspace(param: torch.Tensor, device=None) -> torch.Tensor:
-    """Workspace of ``muon_step`` for parameters of this shape, on ``device``
-    (default: the parameters' own, the current one where they are paged out)."""
+    """Workspace of ``muon_step`` for parameters of this shape, or of fewer or
+    smaller matrices, on ``device`` (default: the parameters' own, the current
+    one where they are paged out)."""
     b = lib().qlora_muon_workspace_bytes(*_matrices(param))
     if b == ctypes.c_size_t(-1).value:
         raise QLoRAError(QLORA_ERR_UNSUPPORTED, "muon_workspace")

@@ -45,8 +45,9 @@ typedef struct qlora_muon_hparams {
   int32_t nesterov;        /* 0 or 1 */
 } qlora_muon_hparams;
 
-/* Device workspace in bytes; (size_t)-1 for an unsupported shape (n, rows or
- * cols below 1, min(rows, cols) above QLORA_MUON_MAX_RANK, n above 65535 or
+/* Device workspace in bytes of up to n matrices, each with its smaller and its
+ * larger side no larger than these; (size_t)-1 for an unsupported shape (n, rows
+ * or cols below 1, min(rows, cols) above QLORA_MUON_MAX_RANK, n above 65535 or
  * max(rows, cols) above 2^24). */
 QLORA_API size_t qlora_muon_workspace_bytes(int64_t n, int64_t rows, int64_t cols);
 

@@ -127,3 +127,22 @@ def test_singular_values_over_eight_decades(ops, rows, cols, steps):
     x = omu.orthogonalise(u * 0.5, NS, steps, 0.0)
     tol = 1.3 * np.sqrt(length + 4 * R * steps) * NS[0] ** (2 * steps) * U53 + 2 * U24 * abs(x)
     assert (abs(tp.cpu().numpy() + x) <= tol).all()
+
+
+def test_fewer_matrices_share_the_workspace_of_more(ops):
+    rows, cols = 16, 300
+    rng = np.random.default_rng(4)
+    u = rng.standard_normal((600, rows, cols)).astype(np.float32)
+    ws = ops.muon_workspace(torch.empty(600, rows, cols, device="cuda"))
+    for n, shape in ((600, (rows, cols)), (512, (rows, cols)), (300, (rows, 200)), (1, (7, cols))):
+        v = np.ascontiguousarray(u[:n, :shape[0], :shape[1]])
+
+        def run(**kw):
+            tp, tm = torch.zeros(v.shape, device="cuda"), torch.from_numpy(v).cuda()
+            g = torch.zeros(v.shape, dtype=torch.bfloat16, device="cuda")
+            out = torch.empty_like(g)
+            ops.muon_step(tp, tm, g, out, **kw)
+            torch.cuda.synchronize()
+            return tp, tm, out
+
+        assert all(torch.equal(a, b) for a, b in zip(run(ws=ws), run()))

@@ -18,3 +18,11 @@ def test_sizes_do_not_fall_with_more_tokens(op, d, k, r):
     assert all(a <= b for a, b in zip(sizes, sizes[1:])), [
         (tokens[i], sizes[i], tokens[i + 1], sizes[i + 1]) for i in range(len(sizes) - 1)
         if sizes[i] > sizes[i + 1]]
+
+
+@pytest.mark.parametrize("d,k", SHAPES)
+@pytest.mark.parametrize("M", [1, 17, 65, 300, 2048])
+@pytest.mark.parametrize("op", [ops.OP_FWD, ops.OP_BWD])
+def test_sizes_do_not_fall_with_more_ranks(op, d, k, M):
+    sizes = [ops.int8_workspace_bytes(op, d, k, M, r) for r in range(129)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))

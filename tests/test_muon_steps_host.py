@@ -73,3 +73,20 @@ def test_accepted_counts_stay_with_the_iteration(coefficients, most):
             want = omu.orthogonalise(u, coefficients, steps, 0.0)
             off = np.linalg.norm(small_matrices(u, coefficients, steps) - want)
             assert off <= 16 * abs(coefficients[0]) ** (2 * steps) * 2.0 ** -53, (steps, off)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (16, 64), (16, 4096), (11008, 12), (64, 8192),
+                                       (128, 129), (130, 100), (4, 1 << 20)])
+def test_workspace_sizes_do_not_fall(rows, cols):
+    """With more matrices, a longer or a wider one: the workspace of the largest
+    serves them all."""
+    size = lambda *s: ops.lib().qlora_muon_workspace_bytes(*s)   # noqa: E731
+    by_n = [size(n, rows, cols) for n in range(1, 2100)] + [size(65535, rows, cols)]
+    assert all(a <= b for a, b in zip(by_n, by_n[1:]))
+    for n in (1, 7, 600, 2000):
+        long = [size(n, rows, cols + c) if cols >= rows else size(n, rows + c, cols)
+                for c in range(0, 600, 7)]
+        assert all(a <= b for a, b in zip(long, long[1:]))
+        small = [size(n, min(r, rows), cols) if cols >= rows else size(n, rows, min(r, cols))
+                 for r in range(1, 129)]
+        assert all(a <= b for a, b in zip(small, small[1:]))
